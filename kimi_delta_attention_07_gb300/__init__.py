@@ -9,6 +9,9 @@ Entry points (same names as the C ABI):
   kda_chunk_fwd        chunked prefill over packed (varlen) sequences
   kda_recurrent_step   one decode token per sequence on a pooled state
   kda_chunk_workspace_bytes, kda_workspace_status, kda_status_string
+  kda_page_tables, kda_rms_norm, kda_latent_cache_write, kda_latent_decode,
+  kda_latent_prefill   the operators around the core in a hybrid decoder's
+                       serving step (include/kda_hybrid.h, _hybrid.py)
 """
 from __future__ import annotations
 
@@ -41,7 +44,9 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_workspace_bytes", "kda
            "kda_chunk_fwd_noalloc", "kda_chunk_fwd_gated", "kda_recurrent_step_gated",
            "kda_output_gate_norm", "kda_recurrent_multi_step", "kda_short_conv_fwd",
            "kda_short_conv_update", "kda_short_conv_multi_update", "kda_recurrent_multi_step_gated",
-           "kda_status_from_workspace_flags")
+           "kda_status_from_workspace_flags", "kda_page_tables", "kda_rms_norm",
+           "kda_latent_cache_write", "kda_latent_decode_workspace_bytes", "kda_latent_decode",
+           "kda_latent_prefill")
 NOALLOC_WORKSPACE_BYTES = 64 * 1024 * 1024
 
 _lib = None
@@ -114,6 +119,19 @@ def load(path: str | None = None):
         L.kda_short_conv_multi_update.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, i32,
                                                   i32, vp]
         L.kda_short_conv_multi_update.restype = i32
+        L.kda_page_tables.argtypes = [vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32,
+                                      i64, vp]
+        L.kda_rms_norm.argtypes = [vp, vp, vp, vp, vp, vp, f32, i64, i32, i32, i32, vp]
+        L.kda_latent_cache_write.argtypes = [vp, i64, vp, f32, vp, vp, i64, i64, i32, vp]
+        L.kda_latent_decode_workspace_bytes.argtypes = [i32, i32, i32]
+        L.kda_latent_decode_workspace_bytes.restype = sz
+        L.kda_latent_decode.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, f32, vp,
+                                        sz, vp]
+        L.kda_latent_prefill.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i64, i64, i32,
+                                         i32, f32, vp]
+        for name in ("kda_page_tables", "kda_rms_norm", "kda_latent_cache_write", "kda_latent_decode",
+                     "kda_latent_prefill"):
+            getattr(L, name).restype = i32
         _lib = L
         return L
 
@@ -568,3 +586,8 @@ def kda_chunk_fwd_noalloc(q, k, v, g, beta, *, o, final_state=None, cu_seqlens=N
     if st != KDA_OK:
         raise KdaError(st, "kda_chunk_fwd_noalloc")
     return o, final_state
+
+
+from ._hybrid import (KDA_QUANT_BLOCK, KDA_QUANT_NONE, KDA_QUANT_ROW, kda_latent_cache_write,  # noqa: E402,F401
+                      kda_latent_decode, kda_latent_decode_workspace_bytes, kda_latent_prefill,
+                      kda_page_tables, kda_rms_norm)

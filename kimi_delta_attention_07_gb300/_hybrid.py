@@ -1,0 +1,277 @@
+"""Binding of the operators around the KDA core (include/kda_hybrid.h): page
+tables, residual + RMS norm, the paged latent cache and latent attention.
+
+Arguments are checked on the host, nothing is synchronised.  A call on a
+stream that is not the current one marks what it allocated as in use there.
+Small calls are dominated by the host, so the checks test all of a tensor's
+properties at once and name the property only when one of them fails.
+"""
+from __future__ import annotations
+
+import torch
+
+import kimi_delta_attention_07_gb300 as _core
+
+KDA_QUANT_NONE, KDA_QUANT_ROW, KDA_QUANT_BLOCK = range(3)
+LATENT_DIM, ROPE_DIM, LATENT_ROW, NOPE_DIM, VALUE_DIM = 512, 64, 576, 128, 128
+_QUANT = {"none": KDA_QUANT_NONE, None: KDA_QUANT_NONE, "row": KDA_QUANT_ROW, "block": KDA_QUANT_BLOCK}
+_bf16, _f32, _i32, _u8, _e4m3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
+                                 torch.float8_e4m3fn)
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _need(t, name, dtype, shape, dev):
+    """t is a contiguous CUDA tensor of this dtype and shape on device `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _core._check(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on the same device as the other tensors")
+
+
+def _rows(t, name, dtype, shape, dev):
+    """The same for a tensor whose first stride is free (a slice of a wider
+    projection); returns (address, elements between rows)."""
+    inner = 1
+    ok = t.dtype is dtype and t.shape == shape and t.get_device() == dev
+    if ok:
+        for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+            ok = ok and (stride == inner or size == 1)
+            inner *= size
+    if not ok:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the same device as the other tensors")
+        raise ValueError(f"{name} must be contiguous but for its row stride")
+    stride = t.stride(0) if t.shape[0] > 1 else max(inner, 8)
+    if stride < inner or stride % 8:
+        raise ValueError(f"{name}: its row stride must be a multiple of 8 of at least {inner}, got {stride}")
+    return t.data_ptr(), stride
+
+
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _stream_of(stream, dev, *allocated):
+    if stream is None:
+        return _current_stream(dev)
+    for t in allocated:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _done(status, what):
+    if status:
+        raise _core.KdaError(status, what)
+
+
+def kda_page_tables(ctx_lens, new_lens, free_pages, block_table, *, page_size, n_pages, max_tokens=None,
+                    free_start=None, cu_seqlens=None, seq_lens=None, slots=None, positions=None,
+                    status=None, stream=None):
+    """Block table, slot map, positions and offsets of one step, from request
+    lengths on the device (kda_page_tables in kda_hybrid.h).
+
+    ctx_lens, new_lens int32 [N] (tokens in the cache; tokens this step adds);
+    free_pages int32 [F]; block_table int32 [N, max_pages], extended in place.
+    max_tokens sizes slots and positions (the length of the packed, possibly
+    padded batch) unless they are given.  free_start int32 [1] (status[:1] of
+    the step before) or None.  Returns (cu_seqlens [N+1], seq_lens [N], slots
+    [max_tokens], positions [max_tokens], status [2] = (position in free_pages
+    after the step, requests refused)), all int32.
+    """
+    dev = _device(ctx_lens, "ctx_lens")
+    n = ctx_lens.numel()
+    fresh = []
+
+    def out(t, name, shape):
+        if t is None:
+            t = torch.empty(shape, dtype=_i32, device=ctx_lens.device)
+            fresh.append(t)
+            return t
+        _need(t, name, _i32, shape, dev)
+        return t
+
+    if slots is not None:
+        max_tokens = slots.numel()
+    elif max_tokens is None:
+        raise ValueError("pass max_tokens, or slots and positions")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [N, max_pages]")
+    pc = _need(ctx_lens, "ctx_lens", _i32, (n,), dev)
+    pn = _need(new_lens, "new_lens", _i32, (n,), dev)
+    pf = _need(free_pages, "free_pages", _i32, (free_pages.numel(),), dev)
+    pb = _need(block_table, "block_table", _i32, (n, block_table.shape[1]), dev)
+    ps = None if free_start is None else _need(free_start, "free_start", _i32, (1,), dev)
+    cu_seqlens = out(cu_seqlens, "cu_seqlens", (n + 1,))
+    seq_lens = out(seq_lens, "seq_lens", (n,))
+    slots = out(slots, "slots", (max_tokens,))
+    positions = out(positions, "positions", (max_tokens,))
+    status = out(status, "status", (2,))
+    _done(_core.load().kda_page_tables(
+        pc, pn, pf, free_pages.numel(), ps, pb, cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+        slots.data_ptr(), positions.data_ptr(), status.data_ptr(), n, max_tokens,
+        block_table.shape[1], page_size, n_pages, _stream_of(stream, dev, *fresh)), "kda_page_tables")
+    return cu_seqlens, seq_lens, slots, positions, status
+
+
+def kda_rms_norm(x, weight=None, *, residual=None, eps=1e-6, quant="none", residual_out=None, y=None,
+                 scales=None, stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight over the last axis.
+
+    x, residual [..., D] bf16 or fp32; weight [D] fp32 or None.  quant "none":
+    y in x's dtype; "row" / "block": y in float8_e4m3fn with fp32 scales
+    [...] (shape [..., 1]) / [..., D / 128], y * scale standing for the value.
+    With a residual, h (rounded to x's dtype) is returned too, in residual_out
+    (allocated unless given; may be residual or x).  Returns (y, residual_out
+    or None, scales or None).
+    """
+    dev = _device(x, "x")
+    shape, dtype = x.shape, x.dtype
+    D = shape[-1]
+    rows = x.numel() // D if D else 0
+    q = _QUANT[quant]
+    fresh = []
+    px = _need(x, "x", dtype, shape, dev)
+    dt = _core._dtype_code(x)
+    pr = None if residual is None else _need(residual, "residual", dtype, shape, dev)
+    pw = None if weight is None else _need(weight, "weight", _f32, (D,), dev)
+    if residual_out is not None:
+        _need(residual_out, "residual_out", dtype, shape, dev)
+    elif residual is not None:
+        residual_out = torch.empty_like(x)
+        fresh.append(residual_out)
+    ydt = _e4m3 if q else dtype
+    if y is None:
+        y = torch.empty(shape, dtype=ydt, device=x.device)
+        fresh.append(y)
+    else:
+        _need(y, "y", ydt, shape, dev)
+    if q:
+        groups = (*shape[:-1], 1 if q == KDA_QUANT_ROW else D // 128)
+        if scales is None:
+            scales = torch.empty(groups, dtype=_f32, device=x.device)
+            fresh.append(scales)
+        else:
+            _need(scales, "scales", _f32, groups, dev)
+    else:
+        scales = None
+    _done(_core.load().kda_rms_norm(
+        px, pr, pw, y.data_ptr(), None if scales is None else scales.data_ptr(),
+        None if residual_out is None else residual_out.data_ptr(), eps, rows, D, q, dt,
+        _stream_of(stream, dev, *fresh)), "kda_rms_norm")
+    return y, residual_out, scales
+
+
+def kda_latent_cache_write(kv, weight, cache, slots, *, eps=1e-6, stream=None):
+    """cache row slots[t] = [rms_norm(kv[t, :512]) * weight ; kv[t, 512:]].
+
+    kv [T, 576] bf16 (its row stride is free: a slice of a fused projection);
+    weight fp32 [512], or None to store the latent as it is; cache [n_pages,
+    page_size, 576] bf16, written in place; slots int32 [T] (others than cache
+    rows, such as -1, are skipped).  Returns cache.
+    """
+    dev = _device(kv, "kv")
+    T = kv.shape[0]
+    pk, stride = _rows(kv, "kv", _bf16, (T, LATENT_ROW), dev)
+    if cache.dim() != 3 or cache.shape[2] != LATENT_ROW:
+        raise ValueError(f"cache must be [n_pages, page_size, {LATENT_ROW}]")
+    pc = _need(cache, "cache", _bf16, cache.shape, dev)
+    pw = None if weight is None else _need(weight, "weight", _f32, (LATENT_DIM,), dev)
+    ps = _need(slots, "slots", _i32, (T,), dev)
+    _done(_core.load().kda_latent_cache_write(pk, stride, pw, eps, pc, ps, T, cache.shape[0], cache.shape[1],
+                                              _stream_of(stream, dev)), "kda_latent_cache_write")
+    return cache
+
+
+def kda_latent_decode_workspace_bytes(n_seqs: int, S: int, H: int) -> int:
+    return int(_core.load().kda_latent_decode_workspace_bytes(n_seqs, S, H))
+
+
+def kda_latent_decode(q, cache, block_table, seq_lens, *, scale=None, o=None, lse=None, workspace=None,
+                      stream=None):
+    """Absorbed latent attention of S new tokens a request over the paged cache.
+
+    q [N, S, H, 576] (or [N, H, 576]: S = 1) bf16; cache [n_pages, page_size,
+    576] bf16; block_table int32 [N, max_pages]; seq_lens int32 [N], the S new
+    tokens among them: token s sees positions below seq_lens[n] - S + 1 + s.
+    scale defaults to 192 ** -0.5 (the expanded query's width).  lse, if given,
+    is fp32 [N, S, H] (or [N, H]).  Returns o, q's shape with 512 for 576.
+    """
+    dev = _device(q, "q")
+    shape = q.shape
+    if len(shape) == 4:
+        n, S, H, _ = shape
+    elif len(shape) == 3:
+        (n, H, _), S = shape, 1
+    else:
+        raise ValueError("q must be [N, S, H, 576] or [N, H, 576]")
+    pq = _need(q, "q", _bf16, (*shape[:-1], LATENT_ROW), dev)
+    if cache.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("cache must be [n_pages, page_size, 576], block_table [N, max_pages]")
+    n_pages, page_size, _ = cache.shape
+    pc = _need(cache, "cache", _bf16, (n_pages, page_size, LATENT_ROW), dev)
+    pb = _need(block_table, "block_table", _i32, (n, block_table.shape[1]), dev)
+    pl = _need(seq_lens, "seq_lens", _i32, (n,), dev)
+    fresh = []
+    if o is None:
+        o = torch.empty((*shape[:-1], LATENT_DIM), dtype=_bf16, device=q.device)
+        fresh.append(o)
+    else:
+        _need(o, "o", _bf16, (*shape[:-1], LATENT_DIM), dev)
+    ple = None if lse is None else _need(lse, "lse", _f32, shape[:-1], dev)
+    lib = _core.load()
+    if workspace is None:
+        workspace = torch.empty(max(256, lib.kda_latent_decode_workspace_bytes(n, S, H)), dtype=_u8,
+                                device=q.device)
+        fresh.append(workspace)
+    pw = _need(workspace, "workspace", _u8, (workspace.numel(),), dev)
+    _done(lib.kda_latent_decode(
+        pq, pc, pb, pl, o.data_ptr(), ple, n, S, H, n_pages, page_size, block_table.shape[1],
+        192 ** -0.5 if scale is None else scale, pw, workspace.numel(), _stream_of(stream, dev, *fresh)),
+        "kda_latent_decode")
+    return o
+
+
+def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal=True, scale=None, o=None,
+                       lse=None, stream=None):
+    """Expanded latent attention over packed sequences.
+
+    q [Tq, H, 192] bf16; kv [Tk, H, 256] bf16 (a head's key part, then its
+    value); k_rope [Tk, 64] bf16, shared by the heads; the token strides of the
+    three are free.  cu_seqlens_q / cu_seqlens_k int32 [N+1] (k None: the same
+    as q).  causal: query i of lq sees keys j <= i + lk - lq.  scale defaults to
+    192 ** -0.5.  lse, if given, is fp32 [Tq, H].  Returns o [Tq, H, 128].
+    """
+    dev = _device(q, "q")
+    if q.dim() != 3 or kv.dim() != 3:
+        raise ValueError("q must be [Tq, H, 192], kv [Tk, H, 256]")
+    Tq, H, _ = q.shape
+    Tk = kv.shape[0]
+    pq, sq = _rows(q, "q", _bf16, (Tq, H, NOPE_DIM + ROPE_DIM), dev)
+    pk, sk = _rows(kv, "kv", _bf16, (Tk, H, NOPE_DIM + VALUE_DIM), dev)
+    pr, sr = _rows(k_rope, "k_rope", _bf16, (Tk, ROPE_DIM), dev)
+    n = cu_seqlens_q.numel() - 1
+    if n < 1:
+        raise ValueError("cu_seqlens_q must be int32 [N+1] with N >= 1")
+    pcq = _need(cu_seqlens_q, "cu_seqlens_q", _i32, (n + 1,), dev)
+    pck = None if cu_seqlens_k is None else _need(cu_seqlens_k, "cu_seqlens_k", _i32, (n + 1,), dev)
+    fresh = []
+    if o is None:
+        o = torch.empty((Tq, H, VALUE_DIM), dtype=_bf16, device=q.device)
+        fresh.append(o)
+    else:
+        _need(o, "o", _bf16, (Tq, H, VALUE_DIM), dev)
+    ple = None if lse is None else _need(lse, "lse", _f32, (Tq, H), dev)
+    _done(_core.load().kda_latent_prefill(
+        pq, sq, pk, sk, pr, sr, o.data_ptr(), ple, pcq, pck, n, Tq, Tk, H, 1 if causal else 0,
+        192 ** -0.5 if scale is None else scale, _stream_of(stream, dev, *fresh)), "kda_latent_prefill")
+    return o

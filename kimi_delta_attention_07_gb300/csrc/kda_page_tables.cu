@@ -1,0 +1,170 @@
+// Block tables and slot maps of one step, from request lengths on the device.
+//
+// With P = page_size, request n needs
+//   need_n = ceil((ctx_n + new_n) / P) - ceil(ctx_n / P)
+// pages, which are free_pages[e_n - need_n .. e_n), e the inclusive prefix sum
+// of need; packed token t of request r (cu_r <= t < cu_{r+1}) has position
+// p = ctx_r + t - cu_r and row table[r][p / P] * P + p % P.
+//
+// One launch: the prefix sums over N requests are a few KB, so every CTA takes
+// them itself (in shared memory, one block scan over contiguous pieces) and
+// no CTA waits for another.  A CTA then fills its share of the rows' new table
+// entries (a warp per request) and of the tokens; the page of a token is read
+// from the free list where it is new, so that no CTA reads what another one
+// writes.  Bound by launch and scan latency: the largest map written here
+// (1.1M tokens) is 9 MB.
+#include <algorithm>
+
+#include "kda_hybrid.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokensPerThread = 4;
+
+__device__ __forceinline__ int64_t warp_inclusive_scan(int64_t x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+struct Need {
+    int64_t held, total;  // pages before and after this step
+    int64_t added;        // packed tokens (new_lens, 0 if negative)
+    bool fits;            // lengths and table row admit the request
+};
+
+__device__ __forceinline__ Need request_need(const PageTablesArgs &a, int n) {
+    const int64_t ctx = a.ctx_lens[n], add = a.new_lens[n], r = ((int64_t)1 << a.page_shift) - 1;
+    Need d;
+    d.added = add > 0 ? add : 0;
+    d.held = (ctx + r) >> a.page_shift;
+    d.total = (ctx + add + r) >> a.page_shift;
+    d.fits = ctx >= 0 && add >= 0 && d.total <= a.max_pages;
+    return d;
+}
+
+__device__ __forceinline__ int32_t clamp32(int64_t x) {
+    return (int32_t)(x < INT32_MAX ? x : INT32_MAX);
+}
+
+__global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageTablesArgs a) {
+    extern __shared__ int32_t sh[];
+    int32_t *cu = sh;                  // [N + 1] offsets of the packed new tokens
+    int32_t *first = sh + a.n_seqs + 1;  // [N] place of the first new page in free_pages, -1: refused
+    __shared__ int64_t part[2][kThreads / 32];
+    __shared__ int32_t seen[2];  // {largest end of a request that fits, refused}
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t begin = a.free_start ? max(a.free_start[0], 0) : 0;
+    if (tid < 2) seen[tid] = tid == 0 ? clamp32(begin) : 0;
+    const int per = (a.n_seqs + kThreads - 1) / kThreads;
+    const int n0 = min(tid * per, a.n_seqs), n1 = min(n0 + per, a.n_seqs);
+    int64_t pages = 0, tokens = 0;
+    for (int n = n0; n < n1; ++n) {
+        const Need d = request_need(a, n);
+        pages += d.fits ? d.total - d.held : 0;
+        tokens += d.added;
+    }
+    int64_t ps = warp_inclusive_scan(pages, lane), ts = warp_inclusive_scan(tokens, lane);
+    if (lane == 31) part[0][wid] = ps, part[1][wid] = ts;
+    __syncthreads();
+    for (int w = 0; w < wid; ++w) ps += part[0][w], ts += part[1][w];
+    ps += begin - pages;
+    ts -= tokens;
+    const bool writer = blockIdx.x == 0;
+    for (int n = n0; n < n1; ++n) {
+        const Need d = request_need(a, n);
+        const int64_t need = d.fits ? d.total - d.held : 0;
+        const bool fits = d.fits && (need == 0 || ps + need <= a.n_free);
+        cu[n] = clamp32(ts);
+        first[n] = fits ? clamp32(ps) : -1;
+        if (writer) {
+            const int32_t ctx = a.ctx_lens[n];
+            a.cu_seqlens[n] = clamp32(ts);
+            a.seq_lens[n] = fits ? ctx + a.new_lens[n] : max(ctx, 0);
+            if (fits) {
+                if (need) atomicMax(&seen[0], (int32_t)(ps + need));
+            } else {
+                atomicAdd(&seen[1], 1);
+            }
+        }
+        ps += need;
+        ts += d.added;
+    }
+    if (tid == kThreads - 1) cu[a.n_seqs] = clamp32(ts);
+    __syncthreads();
+    if (writer && tid == 0) {
+        a.cu_seqlens[a.n_seqs] = cu[a.n_seqs];
+        a.status[0] = seen[0];
+        a.status[1] = seen[1];
+    }
+
+    // new table entries: a warp per request
+    for (int n = blockIdx.x * (kThreads / 32) + wid; n < a.n_seqs; n += gridDim.x * (kThreads / 32)) {
+        if (first[n] < 0) continue;
+        const Need d = request_need(a, n);
+        int32_t *row = a.block_table + (int64_t)n * a.max_pages;
+        for (int64_t j = d.held + lane; j < d.total; j += 32)
+            row[j] = a.free_pages[first[n] + (j - d.held)];
+    }
+
+    // slots and positions: kTokensPerThread consecutive packed tokens a thread
+    const int32_t packed = cu[a.n_seqs];
+    const int64_t step = (int64_t)gridDim.x * kThreads * kTokensPerThread;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kThreads + tid) * kTokensPerThread; t0 < a.max_tokens;
+         t0 += step) {
+        // the last request whose tokens begin at or before t0
+        int lo = 0, hi = a.n_seqs;
+        while (lo + 1 < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= t0) lo = mid; else hi = mid;
+        }
+        int r = lo;
+        for (int i = 0; i < kTokensPerThread && t0 + i < a.max_tokens; ++i) {
+            const int64_t t = t0 + i;
+            int32_t slot = -1, pos = -1;
+            if (t < packed) {
+                while (cu[r + 1] <= t) ++r;
+                if (first[r] >= 0) {
+                    const int32_t ctx = a.ctx_lens[r], p = ctx + (int32_t)(t - cu[r]);
+                    const int32_t j = p >> a.page_shift;
+                    const int32_t held = (int32_t)(((int64_t)ctx + (1 << a.page_shift) - 1) >> a.page_shift);
+                    const int32_t page = j < held ? a.block_table[(int64_t)r * a.max_pages + j]
+                                                  : a.free_pages[first[r] + (j - held)];
+                    if (page >= 0 && page < a.n_pages) {
+                        slot = (page << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+                        pos = p;
+                    }
+                }
+            }
+            a.slots[t] = slot;
+            a.positions[t] = pos;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t stream) {
+    const size_t smem = (2 * (size_t)a.n_seqs + 1) * sizeof(int32_t);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t per_cta = kThreads * kTokensPerThread;
+    const int64_t want = std::max<int64_t>((a.max_tokens + per_cta - 1) / per_cta,
+                                           (a.n_seqs + kThreads / 32 - 1) / (kThreads / 32));
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, sm_count() * 4));
+    const cudaError_t e = launch_dependent(page_tables_kernel, dim3(grid), dim3(kThreads), smem, stream, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kda

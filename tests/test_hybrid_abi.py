@@ -1,0 +1,157 @@
+"""Refusals of the operators around the core (include/kda_hybrid.h) and of
+their binding, on the host: nothing here launches a kernel."""
+import ctypes
+
+import pytest
+import torch
+
+import kimi_delta_attention_07_gb300 as kda
+
+BASE = 1 << 20  # a fake, never dereferenced address
+INVALID, UNSUPPORTED, WORKSPACE, OK = (kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED,
+                                       kda.KDA_ERR_WORKSPACE, kda.KDA_OK)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from kimi_delta_attention_07_gb300 import _build
+    _build.build()
+    return kda.load()
+
+
+def _call(fn, order, defaults, kw):
+    a = {**defaults, **kw}
+    assert set(a) == set(order)
+    return fn(*[a[k] for k in order])
+
+
+def _tables(lib, **kw):
+    order = ("ctx", "new", "free", "n_free", "start", "table", "cu", "lens", "slots", "pos", "status", "n",
+             "tokens", "max_pages", "page", "n_pages", "stream")
+    d = dict.fromkeys(order, BASE)
+    d.update(n_free=8, start=None, status=BASE + 64, n=2, tokens=8, max_pages=4, page=64, n_pages=16, stream=None)
+    return _call(lib.kda_page_tables, order, d, kw)
+
+
+@pytest.mark.parametrize("kw", [dict(page=0), dict(page=8), dict(page=48), dict(page=512), dict(n=-1),
+                                dict(tokens=-1), dict(tokens=1 << 31), dict(n_free=-1), dict(max_pages=0),
+                                dict(n_pages=0), dict(n_pages=1 << 25), dict(ctx=None), dict(new=None),
+                                dict(free=None), dict(table=None), dict(cu=None), dict(lens=None),
+                                dict(slots=None), dict(pos=None), dict(status=None), dict(ctx=BASE + 2),
+                                dict(start=BASE + 64)])
+def test_page_tables_refuses(lib, kw):
+    assert _tables(lib, **kw) == INVALID
+
+
+def test_page_tables_refuses_too_many_requests(lib):
+    assert _tables(lib, n=16385) == UNSUPPORTED
+
+
+def _norm(lib, **kw):
+    order = ("x", "res", "w", "y", "scales", "out", "eps", "rows", "D", "quant", "dtype", "stream")
+    d = dict.fromkeys(order, BASE)
+    d.update(eps=1e-6, rows=4, D=256, quant=0, dtype=kda.KDA_BF16, stream=None)
+    return _call(lib.kda_rms_norm, order, d, kw)
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=2), dict(quant=3), dict(quant=-1), dict(rows=-1), dict(D=0),
+                                dict(D=12), dict(D=136, quant=2), dict(eps=float("nan")), dict(eps=-1.0),
+                                dict(x=None), dict(y=None), dict(quant=1, scales=None), dict(x=BASE + 8),
+                                dict(res=BASE + 8), dict(out=BASE + 8), dict(w=BASE + 8), dict(y=BASE + 8),
+                                dict(y=BASE + 4, quant=1)])
+def test_rms_norm_refuses(lib, kw):
+    assert _norm(lib, **kw) == INVALID
+
+
+def test_rms_norm_other_statuses(lib):
+    assert _norm(lib, D=32776) == UNSUPPORTED
+    assert _norm(lib, rows=0) == OK
+
+
+def _write(lib, **kw):
+    order = ("kv", "stride", "w", "eps", "cache", "slots", "T", "n_pages", "page", "stream")
+    d = dict.fromkeys(order, BASE)
+    d.update(stride=576, eps=1e-6, T=4, n_pages=4, page=64, stream=None)
+    return _call(lib.kda_latent_cache_write, order, d, kw)
+
+
+@pytest.mark.parametrize("kw", [dict(stride=568), dict(stride=580), dict(T=-1), dict(page=24), dict(n_pages=0),
+                                dict(kv=None), dict(cache=None), dict(slots=None), dict(kv=BASE + 8),
+                                dict(cache=BASE + 8), dict(w=BASE + 4), dict(eps=float("inf"))])
+def test_cache_write_refuses(lib, kw):
+    assert _write(lib, **kw) == INVALID
+
+
+def test_cache_write_nothing_to_do(lib):
+    assert _write(lib, T=0) == OK
+
+
+def _decode(lib, **kw):
+    order = ("q", "cache", "table", "lens", "o", "lse", "n", "S", "H", "n_pages", "page", "max_pages", "scale",
+             "ws", "wsb", "stream")
+    d = dict.fromkeys(order, BASE)
+    d.update(lse=None, n=2, S=1, H=4, n_pages=8, page=64, max_pages=4, scale=0.1, wsb=1 << 30, stream=None)
+    return _call(lib.kda_latent_decode, order, d, kw)
+
+
+@pytest.mark.parametrize("kw", [dict(n=-1), dict(S=0), dict(H=0), dict(max_pages=0), dict(page=100),
+                                dict(n_pages=0), dict(scale=float("nan")), dict(q=None), dict(cache=None),
+                                dict(table=None), dict(lens=None), dict(o=None), dict(q=BASE + 8),
+                                dict(cache=BASE + 8), dict(o=BASE + 8), dict(lse=BASE + 2)])
+def test_decode_refuses(lib, kw):
+    assert _decode(lib, **kw) == INVALID
+
+
+def test_decode_other_statuses(lib):
+    assert _decode(lib, S=64, H=128) == UNSUPPORTED
+    assert _decode(lib, ws=None) == WORKSPACE
+    assert _decode(lib, ws=BASE + 16) == WORKSPACE
+    assert _decode(lib, wsb=0) == WORKSPACE
+    assert _decode(lib, n=0) == OK
+    f = kda.kda_latent_decode_workspace_bytes
+    assert f(4, 1, 32) > 0 and f(-1, 1, 1) == 0 and f(1, 0, 1) == 0 and f(1, 64, 128) == 0
+    assert _decode(lib, wsb=f(2, 1, 4) - 1) == WORKSPACE
+
+
+def _prefill(lib, **kw):
+    order = ("q", "sq", "kv", "sk", "rope", "sr", "o", "lse", "cq", "ck", "n", "Tq", "Tk", "H", "causal", "scale",
+             "stream")
+    d = dict.fromkeys(order, BASE)
+    d.update(sq=768, sk=1024, sr=64, lse=None, n=2, Tq=16, Tk=32, H=4, causal=1, scale=0.1, stream=None)
+    return _call(lib.kda_latent_prefill, order, d, kw)
+
+
+@pytest.mark.parametrize("kw", [dict(n=0), dict(H=0), dict(Tq=-1), dict(Tk=-1), dict(scale=float("inf")),
+                                dict(sq=760), dict(sq=772), dict(sk=1016), dict(sr=56), dict(sr=66),
+                                dict(q=None), dict(kv=None), dict(rope=None), dict(o=None), dict(cq=None),
+                                dict(ck=None), dict(q=BASE + 8), dict(kv=BASE + 8), dict(rope=BASE + 8),
+                                dict(o=BASE + 8), dict(lse=BASE + 1)])
+def test_prefill_refuses(lib, kw):
+    assert _prefill(lib, **kw) == INVALID
+
+
+def test_prefill_nothing_to_do(lib):
+    assert _prefill(lib, Tq=0) == OK
+    assert _prefill(lib, Tq=0, ck=None, Tk=0) == OK
+
+
+def test_binding_refuses_host_tensors(lib):
+    i = torch.zeros(2, dtype=torch.int32)
+    t = torch.zeros((2, 4), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        kda.kda_page_tables(i, i, i, t, page_size=64, n_pages=4, max_tokens=8)
+    b = torch.zeros((2, 576), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        kda.kda_rms_norm(b)
+    with pytest.raises(ValueError):
+        kda.kda_latent_cache_write(b, None, torch.zeros((1, 16, 576), dtype=torch.bfloat16), i)
+    with pytest.raises(ValueError):
+        kda.kda_latent_decode(b[:, None], torch.zeros((1, 16, 576), dtype=torch.bfloat16), t, i)
+    with pytest.raises(ValueError):
+        kda.kda_latent_prefill(b[:, None, :192], b[:, None, :256], b[:, :64], cu_seqlens_q=i)
+
+
+def test_every_entry_point_of_the_header_has_argument_types(lib):
+    for name in ("kda_page_tables", "kda_rms_norm", "kda_latent_cache_write", "kda_latent_decode", "kda_latent_prefill"):
+        fn = getattr(lib, name)
+        assert fn.argtypes and fn.restype is ctypes.c_int
