@@ -141,6 +141,8 @@ size_t kda_latent_decode_workspace_bytes(int n_seqs, int S, int H);
  * is read).  The probabilities enter the second product as bf16; their sum is
  * taken in fp32 before that rounding.
  *
+ * Limits: S * H <= 4096, N <= 65535, N * max_pages * page_size < 2^36.
+ *
  * The cached tokens are split evenly over the GPU's SMs from the lengths on
  * the device, so that one long request fills the GPU as many short ones do.
  * Results do not depend on timing: parts are joined in a fixed order.

@@ -1,6 +1,5 @@
-// Building blocks shared by the latent-attention kernels: 2-D / 3-D tensor maps
-// over bf16 rows, TMEM stores, the SFU exponential, and reductions over the
-// lanes of a warp that leave one column per lane.
+// Building blocks shared by the latent-attention kernels: 2-D tensor maps
+// over bf16 rows, TMEM accesses and the SFU exponential.
 #pragma once
 
 #include "kda_chunk_tc.cuh"
@@ -23,12 +22,54 @@ __device__ __forceinline__ float log2_sfu(float x) {
     return r;
 }
 
+// Whether the phase of `parity` has completed, without waiting (try_wait may
+// suspend the thread for a while, which a thread that polls two barriers cannot have).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// fetches a tensor map (a kernel parameter) ahead of its first copy
+__device__ __forceinline__ void prefetch_tensormap(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int c0, int c1, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
         "l"(tmap), "r"(c0), "r"(c1), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// True in one thread of the (converged) warp.  Unlike a test of the lane, it lets
+// the compiler keep what the thread issues with in uniform registers: a chain
+// of unrolled MMAs then runs at the tensor core's pace (24 clocks for 64 x 32
+// x 16) instead of 50 clocks each.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
 }
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane (addressed as tmem_ld32)
@@ -48,22 +89,18 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// v[c] of every lane reduced over the warp; lane c returns column c's result.
-// Halves exchange: after the step of distance o, a lane holds the o columns
-// that agree with its own index in that bit (31 shuffles for 32 columns).
-template <typename Op>
-__device__ __forceinline__ float reduce_columns(float (&v)[32], Op op) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
-        }
-    }
-    return v[0];
+// 32 fp32 columns of 16 TMEM lanes (the first 16 of this warp's 32), as an MMA
+// accumulator fragment: r[4 j + 2 h + e] is lane 8 h + t / 4, column
+// 8 j + 2 (t % 4) + e, with t the thread's lane.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&r)[16]) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
+          "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr));
 }
 
 // Map over bf16 rows of `width` elements, `stride` elements apart, with boxes

@@ -103,7 +103,10 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
     if (n_seqs < 0 || S <= 0 || H <= 0 || max_pages <= 0 || !pool_ok(n_pages, shift) ||
         !isfinite(scale))
         return KDA_ERR_INVALID_ARG;
-    if ((int64_t)S * H > 4096 || n_seqs > 65535) return KDA_ERR_UNSUPPORTED;
+    // tiles are counted in 32 bits
+    if ((int64_t)S * H > 4096 || n_seqs > 65535 ||
+        (((int64_t)max_pages << shift) * n_seqs) >> 36 != 0)
+        return KDA_ERR_UNSUPPORTED;
     if (n_seqs == 0) return KDA_OK;
     if (!q || !cache || !block_table || !seq_lens || !o || !aligned(q, 16) || !aligned(cache, 16) ||
         !aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))

@@ -7,14 +7,28 @@
 // operations a token and query row, keep up: 32 rows want 60 operations a byte,
 // which takes the tensor cores.
 //
-// Orientation: tokens are the M axis of both products' first operand,
-//   X^T [128 tokens x 32 rows]   = C [128 x 576] . Q^T         (per tile)
-//   O^T [512 x 32 rows]         += C[:, :512]^T . P^T [128 x 32]
-// so that the few query rows are the N axis (32, where M would be padded to 128)
-// and one shared-memory tile of the cache, as TMA laid it down, serves as the
-// K-major operand of the first product and as the MN-major operand of the
-// second.  A softmax thread owns one token (TMEM lane) and holds its 32 rows'
-// scores in registers; p goes through shared memory as the MN-major B operand.
+// Orientation: tokens are the M axis of the first product and the cache is the
+// first operand of both,
+//   X^T [64 (48 used) tokens x 32 rows] = C [64 x 576] . Q^T      (per tile)
+//   O^T [512 x 32 rows]                += C[:, :512]^T . P^T [48 x 32]
+// so that the few query rows are the N axis (as M they would be padded to 64 or
+// 128) and one shared-memory tile of the cache, as TMA laid it down, serves as
+// the K-major operand of the first product and as the MN-major operand of the
+// second.  The scores of a tile lie in 16 TMEM lanes a warp and are read as
+// accumulator fragments, 16 a thread; p goes through shared memory as the
+// MN-major B operand.
+//
+// Loads: DRAM wants whole rows.  Loading the cache by blocks of 64 columns (a
+// GEMM's K-blocks) reached 3.8 to 5.7 TB/s in a load-only kernel, whole rows of
+// 16 tokens in one copy 6.8 TB/s once 72 KB an SM are in flight.  So a copy is
+// 16 tokens (they are in one page, whatever its size), laid down by a 4-D map as
+// [2 groups of 8 tokens][9 blocks][8 rows][128 B]: a swizzle atom per (group,
+// block), 9216 bytes between groups, which both operand descriptors can step.
+//
+// Tiles of 48 tokens: a tile stays in shared memory until its second product is
+// done, which is about 1.2 us after it has arrived (at 44 bytes a ns); three
+// tiles of 48 keep more in flight (90 KB) than two of 64 (68 KB).  The first
+// product's M is 64: its last 16 rows are whatever follows in the ring.
 //
 // Running maximum: rows keep a reference that is only raised (and O^T in TMEM
 // rescaled) when some score passes it by 2^8, which is decided by one vote a
@@ -27,7 +41,9 @@
 // crosses ranges leaves (O, max, sum) parts in the workspace, which a second,
 // dependent kernel joins in range order.
 //
-// Warps: 0..3 softmax and epilogue, 4 TMA, 5 MMA.
+// Warps: 0..2 softmax (16 tokens each), 0..3 rescaling and epilogue, 4 TMA, 5
+// first products, 6 second products (one warp that polled for both took 135 us
+// where two take 129).
 #include <algorithm>
 
 #include "kda_attn.cuh"
@@ -38,30 +54,58 @@ using namespace tc;
 
 namespace {
 
-constexpr int kTile = 128;   // tokens per tile
-constexpr int kRows = 32;    // query rows per CTA
-constexpr int kPairs = 5;    // ring slots of two 64-column blocks (four per tile)
-constexpr int kThreads = 192;
-constexpr uint32_t kBlock = kTile * 128;  // one 64-column block of a tile
-constexpr float kRaise = 8.0f;            // log2 by which a score may pass its row's reference
+constexpr int kCopy = 16;   // tokens per copy
+constexpr int kCopies = 3;  // copies per tile
+constexpr int kTile = kCopies * kCopy;
+constexpr int kSlots = 3;   // tiles in the ring
+constexpr int kRows = 32;   // query rows per CTA
+constexpr int kThreads = 224;
+constexpr uint32_t kGroup = 9 * 1024;        // 8 tokens
+constexpr uint32_t kCopyBytes = 2 * kGroup;
+constexpr uint32_t kTileBytes = kCopies * kCopyBytes;
+constexpr float kRaise = 8.0f;  // log2 by which a score may pass its row's reference
 
-// shared memory (from a 1024-byte boundary)
-constexpr uint32_t kSmQ = 0;                               // [9][32 rows][128 B]
-constexpr uint32_t kSmP = kSmQ + 9 * kRows * 128;          // [128 tokens][64 B]
-constexpr uint32_t kSmRope = kSmP + kTile * 64;            // one block
-constexpr uint32_t kSmPair = kSmRope + kBlock;             // kPairs x two blocks
-constexpr uint32_t kSmEnd = kSmPair + kPairs * 2 * kBlock;
-constexpr uint32_t kSmemBytes = kSmEnd + 1024;             // + alignment of the base
+// shared memory (from a 1024-byte boundary); the ring comes first, so that the
+// 16 rows which a first product reads past its tile are inside
+constexpr uint32_t kSmTile = 0;
+constexpr uint32_t kSmQ = kSlots * kTileBytes;     // [9][32 rows][128 B]
+constexpr uint32_t kSmP = kSmQ + 9 * kRows * 128;  // 2 x [64 tokens][64 B]
+constexpr uint32_t kSmemBytes = kSmP + 2 * 64 * 64 + 1024;  // + alignment of the base
+static_assert(9 * kRows * 128 >= (8 - 2 * kCopies) * kGroup, "rows past the last tile");
 
-constexpr uint32_t kTmemCols = 256;  // O^T: 4 x 32, X^T: 32
+constexpr uint32_t kTmemCols = 256;  // O^T: 4 x 32 columns, X^T: 2 x 32
 constexpr uint32_t kTmemX = 128;
+
+// Operand descriptors of a tile (128-byte swizzle, 8-token groups kGroup apart):
+// K-major for block b (64 columns) and step k of 16 columns; MN-major for
+// columns 128 b.. and step k of 16 tokens, 64-column blocks 1024 bytes apart.
+constexpr uint32_t kTileDescHi = (kGroup >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t tile_desc_k(uint32_t tile, int b, int k) {
+    return ((uint64_t)kTileDescHi << 32) | (((tile & 0x3FFFFu) >> 4) + b * 64 + k * 2) | (1u << 16);
+}
+__device__ __forceinline__ uint64_t tile_desc_mn(uint32_t tile, int b, int k) {
+    return ((uint64_t)kTileDescHi << 32) | (((tile & 0x3FFFFu) >> 4) + b * 128 + k * (kCopyBytes >> 4)) | (64u << 16);
+}
 
 struct Part {  // of a request that crosses ranges
     float o[kRows][kLatent];
-    float m[kRows], l[kRows];
 };
-struct Join {  // written by the second range of a crossing request
-    int32_t n, first, last, pad;  // ranges first..last hold its parts; n < 0: none
+struct Stat {  // and its rows' reference and sum
+    float m, l;
+};
+struct Join {  // ranges first..last hold request n's parts; n < 0: nothing to join
+    int32_t n, first, last, pad;
+};
+
+// Tiles [0, total) cut into `ranges` pieces that differ by at most one tile.
+struct Cut {
+    int base, rem;
+    __device__ __forceinline__ Cut(int total, int ranges) : base(total / ranges), rem(total - base * ranges) {}
+    __device__ __forceinline__ int begin(int range) const { return range * base + min(range, rem); }
+    __device__ __forceinline__ int range_of(int tile) const {
+        const int longer = rem * (base + 1);
+        return tile < longer ? tile / (base + 1) : rem + (tile - longer) / base;
+    }
 };
 
 struct Grid {
@@ -78,7 +122,9 @@ struct DecodeParams {
     LatentDecodeArgs a;
     int row_blocks, ranges;
     Part *parts;  // [range][row block][2]: begun before the range / begun in it
-    Join *joins;  // [range]
+    Stat *stats;  // [row][2][range]: what a joining warp reads lies together
+    Join *joins;  // [ranges]: a request is joined by entry n if there are no more requests than ranges, else
+                  // by the entry of the range that it begins in (at most one leaves a range)
 };
 
 __device__ __forceinline__ int tiles_of(const LatentDecodeArgs &a, int len) {
@@ -97,17 +143,19 @@ struct Segment {
 // Walks the range's requests; every role keeps its own.
 struct Walk {
     const LatentDecodeArgs &a;
-    int n, off;
-    int64_t left;
+    int n, off, left;
+    int len;  // of request n if it is the first, which the setup has read
+    bool begun;
     __device__ __forceinline__ bool next(Segment &s) {
         if (left <= 0) return false;
         s.n = n;
-        s.len = a.seq_lens[n];
+        s.len = begun ? a.seq_lens[n] : len;
+        begun = true;
         s.ok = s.len >= 0 && (int64_t)s.len <= ((int64_t)a.max_pages << a.page_shift);
         s.total = tiles_of(a, s.len);
         if (!s.ok) s.len = 0;
         s.tile0 = off;
-        s.tiles = (int)min((int64_t)(s.total - off), left);
+        s.tiles = min(s.total - off, left);
         left -= s.tiles;
         ++n;
         off = 0;
@@ -120,77 +168,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap map_c, const DecodeParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full_pair[kPairs], empty_pair[kPairs], full_rope, full_q, x_full, p_full, o_full, o_empty;
+    __shared__ uint64_t full[kSlots], empty[kSlots][kCopies], full_q, empty_q, x_full[2], p_full[2], pv_done[2], o_empty;
     __shared__ uint32_t tmem_base;
-    __shared__ int64_t piece[kThreads], total_tiles;
-    __shared__ int start_n, start_off;
-    __shared__ float sh_m[4][kRows], sh_l[4][kRows];
-    __shared__ volatile int dead;
+    __shared__ int piece[kThreads / 32], start_n, start_off, start_len;
+    __shared__ float sh_col[4][kRows], sh_row[kRows];
+    __shared__ volatile int dead, lost;
 
     const LatentDecodeArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rb = blockIdx.x % p.row_blocks, range = blockIdx.x / p.row_blocks;
 
     if (tid == 0) {
-        for (int i = 0; i < kPairs; ++i) mbar_init(&full_pair[i], 1), mbar_init(&empty_pair[i], 1);
-        mbar_init(&full_rope, 1);
-        mbar_init(&full_q, 1);
-        mbar_init(&x_full, 1);
-        mbar_init(&p_full, 128);
-        mbar_init(&o_full, 1);
-        mbar_init(&o_empty, 128);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&full[i], 1);
+            for (int j = 0; j < kCopies; ++j) mbar_init(&empty[i][j], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&x_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(&full_q, 1), mbar_init(&empty_q, 1), mbar_init(&o_empty, 128);
         fence_mbar_init();
-        dead = 0;
+        dead = lost = 0;
     }
     if (wid == 5) tmem_alloc(&tmem_base, kTmemCols);
+    // (the join is not let in early: its CTAs would settle on the SMs that finish
+    // first and run there one after the other)
     griddep_wait();
-    griddep_launch_dependents();
 
     // this range's first request: sums over contiguous pieces of the requests,
     // then a walk inside the piece where the range begins
-    {
-        const int per = (a.n_seqs + kThreads - 1) / kThreads;
-        const int n0 = min(tid * per, a.n_seqs), n1 = min(n0 + per, a.n_seqs);
-        int64_t mine = 0;
-        for (int n = n0; n < n1; ++n) mine += tiles_of(a, a.seq_lens[n]);
-        piece[tid] = mine;
-        __syncthreads();
-        int64_t before = 0, total = 0;
-        for (int i = 0; i < kThreads; ++i) {
-            if (i < tid) before += piece[i];
-            total += piece[i];
-        }
-        if (tid == 0) total_tiles = total;
-        const int64_t ranges = min((int64_t)p.ranges, total);  // none is empty
-        const int64_t begin = range < ranges ? total * range / ranges : total;
-        if (range >= ranges && rb == 0 && tid == 0) p.joins[range] = {-1, 0, 0, 0};
-        if (begin >= before && begin < before + mine) {
-            int n = n0;
-            for (;; ++n) {
-                const int t = tiles_of(a, a.seq_lens[n]);
-                if (begin < before + t) break;
-                before += t;
-            }
-            start_n = n;
-            start_off = (int)(begin - before);
-            // the range that follows a request's first one names the parts to join
-            Join j = {-1, 0, 0, 0};
-            if (start_off > 0) {
-                const int64_t t0 = before, t1 = before + tiles_of(a, a.seq_lens[n]) - 1;
-                // the range that holds tile t: the last r with total * r / ranges <= t
-                const int first = (int)(((t0 + 1) * ranges + total - 1) / total) - 1;
-                const int last = (int)(((t1 + 1) * ranges + total - 1) / total) - 1;
-                if (first == range - 1) j = {n, first, last, 0};
-            }
-            if (rb == 0) p.joins[range] = j;
-        }
+    const int per = (a.n_seqs + kThreads - 1) / kThreads;
+    const int n0 = min(tid * per, a.n_seqs), n1 = min(n0 + per, a.n_seqs);
+    int mine = 0, last_len = 0;
+    for (int n = n0; n < n1; ++n) {
+        last_len = a.seq_lens[n];
+        mine += tiles_of(a, last_len);
     }
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) piece[wid] = before;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int64_t ranges = min((int64_t)p.ranges, total_tiles);
-    Walk walk{a, start_n, start_off,
-              range < ranges ? total_tiles * (range + 1) / ranges - total_tiles * range / ranges : 0};
+    before -= mine;
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < wid) before += piece[i];
+        total += piece[i];
+    }
+    const int ranges = min(p.ranges, total);  // none is empty
+    const Cut cut(total, ranges);
+    const int range_begin = cut.begin(min(range, ranges)), range_end = cut.begin(min(range + 1, ranges));
+    if (range_begin >= before && range_begin < before + mine) {
+        int n = n0, len = last_len;
+        for (; n + 1 < n1; ++n) {
+            len = a.seq_lens[n];
+            const int t = tiles_of(a, len);
+            if (range_begin < before + t) break;
+            before += t;
+            len = last_len;
+        }
+        start_n = n;
+        start_len = len;
+        start_off = range_begin - before;
+    }
+    __syncthreads();
+    Walk walk{a, start_n, start_off, range_end - range_begin, start_len, false};
     // a bounded wait; once one has given up, none waits any more
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!dead && !mbar_wait(bar, parity)) dead = 1;
@@ -199,259 +247,292 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segment s;
 
     if (wid == 4) {
-        // ---- TMA: Q per request, then per tile pair 0, the key block, pairs 1..3
-        const int box = min(1 << a.page_shift, kTile);
-        const int per_tile = kTile / box;  // pages of a tile
-        const int beyond = (int)(a.n_pages << a.page_shift);  // a row outside: reads zeros
-        int pair = 0, phase = 0, rope_phase = 0;
-        bool first_tile = true;
-        while (!dead && walk.next(s)) {
+        // ---- TMA: the queries of a request, then its tiles
+        int slot = 0, phase = 0, seg = 0;
+        for (; !dead && walk.next(s); ++seg) {
             const int32_t *table = a.block_table + (int64_t)s.n * a.max_pages;
-            auto row_of = [&](int tile) {  // this lane's page of the tile, as a cache row
-                const int64_t pos = (int64_t)tile * kTile + lane * box;
-                if (lane >= per_tile || pos >= s.len) return beyond;
+            // lane j's copy of a tile: the cache row it begins at, negative where there is nothing to copy
+            auto row_of = [&](int tile) {
+                const int64_t pos = (int64_t)tile * kTile + lane * kCopy;
+                if (lane >= kCopies || pos >= s.len) return -1;
                 const int id = table[pos >> a.page_shift];
-                if (id < 0 || id >= a.n_pages) return beyond;
+                if (id < 0 || id >= a.n_pages) return -1;
                 return (id << a.page_shift) + (int)(pos & ((1 << a.page_shift) - 1));
             };
             int next_row = row_of(s.tile0);
             for (int i = 0; i < s.tiles && !dead; ++i) {
-                const int tile = s.tile0 + i, row = next_row;
-                if (i + 1 < s.tiles) next_row = row_of(tile + 1);
-                const int held = min(per_tile, (s.len - tile * kTile + box - 1) / box);  // pages with tokens
-                const int boxes = max(held, 0);
-                auto load_pair = [&](int k) {
-                    wait(&empty_pair[pair], phase ^ 1);
-                    if (lane == 0) mbar_arrive_expect_tx(&full_pair[pair], boxes * 2 * box * 128);
+                const int row = next_row;
+                if (i + 1 < s.tiles) next_row = row_of(s.tile0 + i + 1);
+                const int copies = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                for (int j = 0; j < kCopies; ++j) {
+                    wait(&empty[slot][j], phase ^ 1);
+                    if (j == 0 && lane == 0) mbar_arrive_expect_tx(&full[slot], copies * kCopyBytes);
                     __syncwarp();
-                    const int half = lane & 1, j = lane >> 1;
-                    const int r = __shfl_sync(0xffffffffu, row, j);
-                    if (j < boxes)
-                        tma_load_2d(sm + kSmPair + pair * 2 * kBlock + half * kBlock + j * box * 128, &map_c,
-                                    (2 * k + half) * 64, r, &full_pair[pair]);
-                    if (++pair == kPairs) pair = 0, phase ^= 1;
-                };
-                load_pair(0);
-                // the first product of the tile before has read the key block and, where
-                // the request changes, its queries
-                if (!first_tile) wait(&x_full, rope_phase), rope_phase ^= 1;
-                first_tile = false;
-                if (i == 0) {
-                    if (lane == 0) mbar_arrive_expect_tx(&full_q, 9 * kRows * 128);
-                    __syncwarp();
-                    if (lane < 9)
-                        tma_load_2d(sm + kSmQ + lane * kRows * 128, &map_q, lane * 64,
-                                    s.n * (a.S * a.H) + rb * kRows, &full_q);
+                    if (lane == j && row >= 0)
+                        tma_load_4d(sm + kSmTile + slot * kTileBytes + j * kCopyBytes, &map_c, 0, 0, 0, row >> 3,
+                                    &full[slot]);
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&full_rope, boxes * box * 128);
-                __syncwarp();
-                if (lane < boxes)
-                    tma_load_2d(sm + kSmRope + lane * box * 128, &map_c, kLatent, row, &full_rope);
-                for (int k = 1; k < 4; ++k) load_pair(k);
+                if (i == 0) {
+                    // the queries of the request before have been read by its last first product
+                    wait(&empty_q, (seg & 1) ^ 1);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&full_q, 9 * kRows * 128);
+                        for (int b = 0; b < 9; ++b)
+                            tma_load_2d(sm + kSmQ + b * kRows * 128, &map_q, b * 64, s.n * (a.S * a.H) + rb * kRows,
+                                        &full_q);
+                    }
+                    __syncwarp();
+                }
+                if (++slot == kSlots) slot = 0, phase ^= 1;
             }
         }
     } else if (wid == 5) {
-        // ---- MMA, issued by one thread, in order: X(i), then P.C(i)
-        if (lane == 0) {
-            int pair = 0, phase = 0, tile_phase = 0, seg_phase = 0;
-            bool first_segment = true;
-            const uint32_t q0 = smem_u32(sm + kSmQ), pair0 = smem_u32(sm + kSmPair);
-            while (!dead && walk.next(s)) {
-                wait(&full_q, seg_phase);
-                for (int i = 0; i < s.tiles && !dead; ++i) {
-                    int pr = pair, ph = phase;
-                    for (int k = 0; k < 4; ++k) {
-                        wait(&full_pair[pr], ph);
-                        tc_fence_after();
-                        for (int half = 0; half < 2; ++half)
-                            mma_tile<128, kRows, 64, kTile, kRows>(
-                                tmem + kTmemX, pair0 + pr * 2 * kBlock + half * kBlock,
-                                q0 + (2 * k + half) * kRows * 128, k + half > 0);
-                        if (++pr == kPairs) pr = 0, ph ^= 1;
-                        if (k == 0) {
-                            wait(&full_rope, tile_phase);
-                            tc_fence_after();
-                            mma_tile<128, kRows, 64, kTile, kRows>(tmem + kTmemX, smem_u32(sm + kSmRope),
-                                                                   q0 + 8 * kRows * 128, true);
-                        }
-                    }
-                    mma_commit(&x_full);
-                    wait(&p_full, tile_phase);
-                    if (i == 0 && !first_segment) wait(&o_empty, seg_phase ^ 1);
+        // ---- first products, one tile ahead of the softmax (two accumulators)
+        if (elect_one()) {
+            const uint32_t q0 = smem_u32(sm + kSmQ), tile_0 = smem_u32(sm + kSmTile);
+            constexpr uint32_t idesc = idesc_bf16(64, kRows);
+            int t = 0, slot = 0, phase = 0;
+            for (int seg = 0; !dead && walk.next(s); ++seg) {
+                wait(&full_q, seg & 1);
+                for (int i = 0; i < s.tiles && !dead; ++i, ++t) {
+                    wait(&full[slot], phase);
+                    // its accumulator was read by the softmax of two tiles ago
+                    if (t >= 2) wait(&p_full[t & 1], ((t >> 1) & 1) ^ 1);
                     tc_fence_after();
-                    for (int k = 0; k < 4; ++k) {
-                        mma_tile_n32<128, kTile, kTile, true>(tmem + k * 32, pair0 + pair * 2 * kBlock,
-                                                              smem_u32(sm + kSmP), i > 0);
-                        mma_commit(&empty_pair[pair]);
-                        if (++pair == kPairs) pair = 0, phase ^= 1;
-                    }
-                    tile_phase ^= 1;
+                    const uint32_t d = tmem + kTmemX + (t & 1) * kRows, tile = tile_0 + slot * kTileBytes;
+#pragma unroll
+                    for (int b = 0; b < 9; ++b)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(d, tile_desc_k(tile, b, k),
+                                     ((uint64_t)kDescHi << 32) | operand_lo<false, kRows>(q0 + b * kRows * 128, k),
+                                     idesc, b + k > 0);
+                    mma_commit(&x_full[t & 1]);
+                    if (++slot == kSlots) slot = 0, phase ^= 1;
                 }
-                mma_commit(&o_full);
-                seg_phase ^= 1;
-                first_segment = false;
+                mma_commit(&empty_q);
+            }
+        }
+        __syncwarp();
+    } else if (wid == 6) {
+        // ---- second products
+        if (elect_one()) {
+            const uint32_t tile_0 = smem_u32(sm + kSmTile), p0 = smem_u32(sm + kSmP);
+            constexpr uint32_t idesc = idesc_bf16(128, kRows) | (1u << 15) | (1u << 16);
+            int t = 0, slot = 0;
+            for (int seg = 0; !dead && walk.next(s); ++seg) {
+                for (int i = 0; i < s.tiles && !dead; ++i, ++t) {
+                    wait(&p_full[t & 1], (t >> 1) & 1);
+                    if (i == 0 && seg > 0) wait(&o_empty, (seg - 1) & 1);
+                    tc_fence_after();
+                    const uint32_t tile = tile_0 + slot * kTileBytes, pt = p0 + (t & 1) * 64 * 64;
+#pragma unroll
+                    for (int k = 0; k < kCopies; ++k) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            mma_bf16(tmem + b * kRows, tile_desc_mn(tile, b, k),
+                                     ((uint64_t)kDescHiSw64 << 32) | (((pt & 0x3FFFFu) >> 4) + k * 64), idesc,
+                                     i > 0 || k > 0);
+                        mma_commit(&empty[slot][k]);
+                    }
+                    mma_commit(&pv_done[t & 1]);
+                    if (++slot == kSlots) slot = 0;
+                }
             }
         }
         __syncwarp();
     } else {
-        // ---- softmax: thread = token of the tile, registers = the 32 query rows
+        // ---- softmax: a thread holds 16 scores, tokens 16 w + lane / 4 (+ 8) of the tile by
+        // rows 8 j + 2 (lane % 4) + {0, 1}; warp 3 has no tokens (its scores are hidden)
         const Walk again = walk;
         const uint32_t lanes = (uint32_t)(wid * 32) << 16;
         const float scale2 = a.scale * kLog2e;
         const int rows = min(kRows, a.S * a.H - rb * kRows);
-        int pair = 0, tile_phase = 0, seg_phase = 0;
+        const int tok = 16 * wid + (lane >> 2), col = 2 * (lane & 3);
+        int limit[8];  // of the thread's rows: new token r / H sees positions below len - S + 1 + r / H
+#pragma unroll
+        for (int c = 0; c < 8; ++c) limit[c] = (rb * kRows + 8 * (c >> 1) + col + (c & 1)) / a.H - a.S + 1;
+        int at = range_begin, slot = 0, t = 0;
         bool gave_up = false;  // the same in all four warps: decided by their votes
         while (!gave_up && walk.next(s)) {
-            float m[kRows], l[kRows];
+            float m[8], l[8];
 #pragma unroll
-            for (int c = 0; c < kRows; ++c) m[c] = -INFINITY, l[c] = 0.0f;
+            for (int c = 0; c < 8; ++c) m[c] = -INFINITY, l[c] = 0.0f;
             bool bad = !s.ok;
-            for (int i = 0; i < s.tiles; ++i) {
-                const int64_t pos = (int64_t)(s.tile0 + i) * kTile + tid;
-                if (pos < s.len) {
-                    const int id = a.block_table[(int64_t)s.n * a.max_pages + (pos >> a.page_shift)];
+            for (int i = 0; i < s.tiles; ++i, ++t) {
+                const int64_t pos0 = (int64_t)(s.tile0 + i) * kTile;
+                if (tid >= 96 && tid < 96 + kCopies && pos0 + (tid - 96) * kCopy < s.len) {
+                    const int64_t page = (pos0 + (tid - 96) * kCopy) >> a.page_shift;
+                    const int id = a.block_table[(int64_t)s.n * a.max_pages + page];
                     bad |= id < 0 || id >= a.n_pages;
                 }
-                wait(&x_full, tile_phase);
+                wait(&x_full[t & 1], (t >> 1) & 1);
                 tc_fence_after();
-                float x[kRows];
-                tmem_ld32(tmem + kTmemX + lanes, x);
+                float x[16];
+                tmem_ld_16x32(tmem + kTmemX + (t & 1) * kRows + lanes, x);
                 tmem_ld_wait();
-                const int64_t tile_end = (int64_t)(s.tile0 + i + 1) * kTile;
-                if (tile_end > s.len - a.S + 1) {
-                    // row r (new token r / H) sees positions below len - S + 1 + r / H
 #pragma unroll
-                    for (int c = 0; c < kRows; ++c) {
-                        const int64_t limit = s.len - a.S + 1 + (rb * kRows + c) / a.H;
-                        x[c] = pos < limit ? x[c] * scale2 : -INFINITY;
+                for (int j = 0; j < 16; ++j) x[j] *= scale2;
+                if (pos0 + kTile > s.len - a.S + 1 || wid >= kCopies) {
+                    // the last tiles: what a row does not see, and rows of the tile that hold no token
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int64_t pos = pos0 + tok + ((j >> 1) & 1) * 8;
+                        if (wid >= kCopies || pos >= (int64_t)s.len + limit[(j >> 2) * 2 + (j & 1)]) x[j] = -INFINITY;
                     }
-                    if (pos >= s.len) {
-                        // no token: its row in shared memory may hold anything, and 0 times that has to be 0
-                        int pr = pair;
-                        for (int k = 0; k < 4; ++k) {
-                            for (int half = 0; half < 2; ++half) {
-                                uint4 *r = (uint4 *)(sm + kSmPair + pr * 2 * kBlock + half * kBlock + tid * 128);
+                    if (tid < 2 * kTile && pos0 + (tid >> 1) >= s.len) {
+                        // shared memory may hold anything there, and 0 times that has to be 0
+                        uint8_t *r = sm + kSmTile + slot * kTileBytes + (tid >> 4) * kGroup + ((tid >> 1) & 7) * 128 +
+                                     (tid & 1) * 4096;
+                        for (int b = 0; b < 4; ++b)
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) r[j] = make_uint4(0, 0, 0, 0);
-                            }
-                            if (++pr == kPairs) pr = 0;
-                        }
+                            for (int j = 0; j < 8; ++j) *(uint4 *)(r + b * 1024 + j * 16) = make_uint4(0, 0, 0, 0);
                     }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < kRows; ++c) x[c] *= scale2;
                 }
-                pair = (pair + 4) % kPairs;
+                if (++slot == kSlots) slot = 0;
                 float over = -INFINITY;  // fmaxf skips the NaN of -inf - -inf
 #pragma unroll
-                for (int c = 0; c < kRows; ++c) over = fmaxf(over, x[c] - m[c]);
-                const bool lost = dead;
-                if (!named_bar_and(1, 128, !(over > kRaise) && !lost)) {
-                    if (!named_bar_and(1, 128, !lost)) {
+                for (int j = 0; j < 16; ++j) over = fmaxf(over, x[j] - m[(j >> 2) * 2 + (j & 1)]);
+                const bool given = dead;
+                if (given) lost = 1;
+                if (!named_bar_and(1, 128, !(over > kRaise) && !given)) {
+                    if (lost) {  // written before the vote only
                         gave_up = true;
                         break;
                     }
-                    float t[kRows];
+                    // raise every row's reference to its maximum so far
 #pragma unroll
-                    for (int c = 0; c < kRows; ++c) t[c] = x[c];
-                    sh_m[wid][lane] = reduce_columns(t, [](float u, float v) { return fmaxf(u, v); });
-                    named_bar_sync(1, 128);
-                    float f[kRows];
+                    for (int c = 0; c < 8; ++c) {
+                        const int j = (c >> 1) * 4 + (c & 1);
+                        float top = fmaxf(x[j], x[j + 2]);
 #pragma unroll
-                    for (int c = 0; c < kRows; ++c) {
-                        const float top = fmaxf(fmaxf(fmaxf(sh_m[0][c], sh_m[1][c]), fmaxf(sh_m[2][c], sh_m[3][c])), m[c]);
-                        f[c] = top == -INFINITY ? 1.0f : exp2_sfu(m[c] - top);
-                        m[c] = top;
-                        l[c] *= f[c];
+                        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        if (lane < 4) sh_col[wid][8 * (c >> 1) + col + (c & 1)] = top;
                     }
-                    if (i > 0) {  // the second product of the tile before is done: X(i) was issued after it
+                    named_bar_sync(1, 128);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const int r = 8 * (c >> 1) + col + (c & 1);
+                        const float top = fmaxf(fmaxf(fmaxf(sh_col[0][r], sh_col[1][r]), fmaxf(sh_col[2][r], sh_col[3][r])), m[c]);
+                        const float f = top == -INFINITY ? 1.0f : exp2_sfu(m[c] - top);
+                        m[c] = top;
+                        l[c] *= f;
+                        if (wid == 0 && lane < 4) sh_row[r] = f;
+                    }
+                    if (i > 0) {
+                        wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
+                        tc_fence_after();
+                        named_bar_sync(1, 128);
                         for (int k = 0; k < 4; ++k) {
                             float o[kRows];
                             tmem_ld32(tmem + k * 32 + lanes, o);
                             tmem_ld_wait();
                             uint32_t u[kRows];
 #pragma unroll
-                            for (int c = 0; c < kRows; ++c) u[c] = __float_as_uint(o[c] * f[c]);
+                            for (int c = 0; c < kRows; ++c) u[c] = __float_as_uint(o[c] * sh_row[c]);
                             tmem_st32(tmem + k * 32 + lanes, u);
                         }
                         tmem_st_wait();
                     }
-                    named_bar_sync(1, 128);  // sh_m is read before it is written again
+                    named_bar_sync(1, 128);  // sh_col and sh_row are read before they are written again
                 }
 #pragma unroll
-                for (int c = 0; c < kRows; ++c) {
-                    x[c] = exp2_sfu(x[c] - (m[c] == -INFINITY ? 0.0f : m[c]));
-                    l[c] += x[c];
+                for (int c = 0; c < 8; ++c) {
+                    const int j = (c >> 1) * 4 + (c & 1);
+                    const float ref = m[c] == -INFINITY ? 0.0f : m[c];
+                    x[j] = exp2_sfu(x[j] - ref);
+                    x[j + 2] = exp2_sfu(x[j + 2] - ref);
+                    l[c] += x[j] + x[j + 2];
                 }
+                // this buffer's p was read by the second product of two tiles ago
+                if (t >= 2) wait(&pv_done[t & 1], ((t >> 1) & 1) ^ 1);
+                uint8_t *ps = sm + kSmP + (t & 1) * 64 * 64;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint4 v = make_uint4(pack2(x[8 * j], x[8 * j + 1]), pack2(x[8 * j + 2], x[8 * j + 3]),
-                                               pack2(x[8 * j + 4], x[8 * j + 5]), pack2(x[8 * j + 6], x[8 * j + 7]));
-                    *(uint4 *)(sm + kSmP + sw64_off(tid, 8 * j)) = v;
+                    *(uint32_t *)(ps + sw64_off(tok, 8 * j + col)) = pack2(x[4 * j], x[4 * j + 1]);
+                    *(uint32_t *)(ps + sw64_off(tok + 8, 8 * j + col)) = pack2(x[4 * j + 2], x[4 * j + 3]);
                 }
                 fence_async_smem();
                 tc_fence_before();
-                mbar_arrive(&p_full);
-                tile_phase ^= 1;
+                mbar_arrive(&p_full[t & 1]);
             }
             if (gave_up) break;
             // ---- the request's part of this range is done
-            sh_l[wid][lane] = reduce_columns(l, [](float u, float v) { return u + v; });
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+                if (lane < 4) {
+                    const int r = 8 * (c >> 1) + col + (c & 1);
+                    sh_col[wid][r] = l[c];
+                    if (wid == 0) sh_row[r] = m[c];
+                }
+            }
             const bool fine = named_bar_and(1, 128, !bad);
-            wait(&o_full, seg_phase);
-            seg_phase ^= 1;
+            wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
             tc_fence_after();
             const int64_t row0 = (int64_t)s.n * a.S * a.H + rb * kRows;
             Part *part = p.parts + ((int64_t)range * p.row_blocks + rb) * 2 + (s.tile0 == 0 ? 1 : 0);
-            float lt[kRows];
-#pragma unroll
-            for (int c = 0; c < kRows; ++c) {
-                lt[c] = sh_l[0][c] + sh_l[1][c] + sh_l[2][c] + sh_l[3][c];
-                if (!fine) lt[c] = NAN;
-            }
+            Stat *stat = p.stats + ((int64_t)2 * rb * kRows + (s.tile0 == 0 ? 1 : 0)) * p.ranges + range;  // row 0's
+            auto sum = [&](int c) {
+                const float l = (sh_col[0][c] + sh_col[1][c]) + (sh_col[2][c] + sh_col[3][c]);
+                return fine ? l : NAN;
+            };
             if (tid < rows) {
-                float mt = 0.0f, ls = 0.0f;
-#pragma unroll
-                for (int c = 0; c < kRows; ++c)
-                    if (c == tid) mt = m[c], ls = lt[c];
-                if (!s.whole()) part->m[tid] = mt, part->l[tid] = ls;
-                else if (a.lse) a.lse[row0 + tid] = mt == -INFINITY && ls == 0.0f ? -INFINITY : (mt + log2_sfu(ls)) * kLn2;
+                const float mt = sh_row[tid], lt = sum(tid);
+                if (!s.whole()) stat[2 * p.ranges * tid] = {mt, lt};
+                else if (a.lse) a.lse[row0 + tid] = lt == 0.0f ? -INFINITY : (mt + log2_sfu(lt)) * kLn2;
             }
+            if (tid == 0 && rb == 0 && s.tile0 == 0) {
+                const bool by_request = a.n_seqs <= p.ranges;
+                Join j = {-1, 0, 0, 0};
+                if (!s.whole()) j = {s.n, range, cut.range_of(at + s.total - 1), 0};
+                if (by_request) p.joins[s.n] = j;
+                else if (!s.whole()) p.joins[range] = j;
+            }
+            if (s.whole()) {
+                float inv[kRows];
 #pragma unroll
-            for (int c = 0; c < kRows; ++c) lt[c] = lt[c] == 0.0f ? 1.0f : 1.0f / lt[c];
-            for (int k = 0; k < 4; ++k) {
-                float o[kRows];
-                tmem_ld32(tmem + k * 32 + lanes, o);
-                tmem_ld_wait();
-                const int d = k * 128 + tid;
-                if (s.whole()) {
+                for (int c = 0; c < kRows; ++c) inv[c] = sum(c), inv[c] = inv[c] == 0.0f ? 1.0f : 1.0f / inv[c];
+                for (int k = 0; k < 4; ++k) {
+                    float o[kRows];
+                    tmem_ld32(tmem + k * 32 + lanes, o);
+                    tmem_ld_wait();
+                    __nv_bfloat16 *dst = a.o + row0 * kLatent + k * 128 + tid;
 #pragma unroll
                     for (int c = 0; c < kRows; ++c)
-                        if (c < rows) a.o[(row0 + c) * kLatent + d] = __float2bfloat16_rn(o[c] * lt[c]);
-                } else {
+                        if (c < rows) dst[c * kLatent] = __float2bfloat16_rn(o[c] * inv[c]);
+                }
+            } else {
+                for (int k = 0; k < 4; ++k) {
+                    float o[kRows];
+                    tmem_ld32(tmem + k * 32 + lanes, o);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < kRows; ++c)
-                        if (c < rows) part->o[c][d] = o[c];
+                        if (c < rows) part->o[c][k * 128 + tid] = o[c];
                 }
             }
             tc_fence_before();
             mbar_arrive(&o_empty);
-            named_bar_sync(1, 128);  // sh_l is read before the next request writes it
+            at += s.tiles;
+            named_bar_sync(1, 128);  // sh_col and sh_row are read before the next request writes them
         }
+        if (tid == 0 && rb == 0 && a.n_seqs > p.ranges && (range >= ranges || s.whole() || s.tile0 > 0))
+            p.joins[range] = {-1, 0, 0, 0};
         if (!named_bar_and(1, 128, !dead)) {
-            // a wait gave up: the range's outputs are NaN
+            // a wait gave up: the range's outputs are NaN, and requests that cross it are left unjoined
             Walk w = again;
             while (w.next(s)) {
                 const int64_t row0 = (int64_t)s.n * a.S * a.H + rb * kRows;
-                Part *part = p.parts + ((int64_t)range * p.row_blocks + rb) * 2 + (s.tile0 == 0 ? 1 : 0);
                 for (int c = 0; c < rows; ++c) {
-                    if (!s.whole()) {
-                        if (tid == 0) part->m[c] = NAN, part->l[c] = NAN;
-                        continue;
-                    }
                     for (int d = tid; d < kLatent; d += 128) a.o[(row0 + c) * kLatent + d] = __float2bfloat16_rn(NAN);
                     if (a.lse && tid == 0) a.lse[row0 + c] = NAN;
                 }
+                if (tid == 0 && s.tile0 == 0 && a.n_seqs <= p.ranges) p.joins[s.n] = {-1, 0, 0, 0};
+                if (tid == 0 && a.n_seqs > p.ranges) p.joins[range] = {-1, 0, 0, 0};
+                if (!s.whole() && tid < rows)
+                    p.stats[(2 * (rb * kRows + tid) + (s.tile0 == 0 ? 1 : 0)) * p.ranges + range] = {NAN, NAN};
             }
         }
     }
@@ -464,66 +545,136 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (wid == 5) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the parts of a request that crosses ranges, in range order; a thread
-// owns four values of a row.
-constexpr int kJoinRows = 4;
-__global__ void __launch_bounds__(128) latent_decode_join_kernel(const DecodeParams p) {
+// Joins the parts of a request that crosses ranges.  With many rows a warp takes
+// a query row.  With few (MANY parts each, as a single long request leaves) a
+// CTA takes a quarter of a row's 512 values, each of its eight warps every
+// eighth part, and their sums are added in order.
+constexpr int kJoinThreads = 256;
+template <bool MANY>
+__global__ void __launch_bounds__(kJoinThreads) latent_decode_join_kernel(const DecodeParams p) {
+    extern __shared__ float weights[];  // [8 warps][ranges]
+    constexpr int kVec = MANY ? 1 : 4, kStep = MANY ? 8 : 1, kBatch = MANY ? 10 : 4;
+    __shared__ float4 sums[kStep][32];
     griddep_wait();
     griddep_launch_dependents();
     const LatentDecodeArgs &a = p.a;
-    const int range = blockIdx.x / p.row_blocks, rb = blockIdx.x % p.row_blocks;
-    const Join j = p.joins[range];
+    const Join j = p.joins[blockIdx.x];
     if (j.n < 0) return;
-    for (int c = blockIdx.y * kJoinRows; c < (int)(blockIdx.y + 1) * kJoinRows; ++c) {
-        const int row = rb * kRows + c;
-        if (row >= a.S * a.H) return;
-        auto part = [&](int r) { return p.parts + ((int64_t)r * p.row_blocks + rb) * 2 + (r == j.first ? 1 : 0); };
-        float top = -INFINITY;
-        bool nan = false;
-        for (int r = j.first; r <= j.last; ++r) {
-            const float m = part(r)->m[c], l = part(r)->l[c];
-            nan |= !(l == l) || !(m == m);
-            top = fmaxf(top, m);
-        }
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float l = 0.0f;
-        for (int r = j.first; r <= j.last; ++r) {
-            const float m = part(r)->m[c];
-            const float w = m == -INFINITY ? 0.0f : exp2_sfu(m - top);
-            const float4 v = *(const float4 *)&part(r)->o[c][4 * threadIdx.x];
-            if (m != -INFINITY) {
-                l += w * part(r)->l[c];
-                o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int row = MANY ? blockIdx.y : blockIdx.y * 8 + wid, sub = MANY ? wid : 0;
+    if (row >= a.S * a.H) return;
+    const int d0 = (MANY ? blockIdx.z * 128 : 0) + 4 * lane;
+    const int rb = row / kRows, c = row % kRows, parts = j.last - j.first + 1;
+    auto part = [&](int i) {  // the first range began the request
+        return p.parts + ((int64_t)(j.first + i) * p.row_blocks + rb) * 2 + (i == 0 ? 1 : 0);
+    };
+    // values are requested in batches, the first one before the weights that it waits for
+    float4 v[kBatch][kVec];
+    auto request = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                v[i][k] = i0 + i * kStep < parts ? *(const float4 *)&part(i0 + i * kStep)->o[c][128 * k + d0]
+                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    request(sub);
+    // the largest reference (fmaxf skips NaN, whose weight is NaN below); a part that saw nothing
+    // has no reference, and its sum is 0, or NaN where the request cannot be read
+    float top = -INFINITY, l = 0.0f;
+    const Stat *stat = p.stats + (int64_t)2 * row * p.ranges + j.first;
+    auto stat_of = [&](int i) { return stat[i == 0 ? p.ranges : i]; };
+    float *weight = weights + wid * p.ranges;
+    constexpr int kEach = 5;  // parts a lane keeps; beyond them (no GPU of 160 SMs) they are read again
+    Stat mine[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        mine[i] = lane + 32 * i < parts ? stat_of(lane + 32 * i) : Stat{-INFINITY, 0.0f};
+        top = fmaxf(top, mine[i].m);
+    }
+    for (int i = lane + 32 * kEach; i < parts; i += 32) top = fmaxf(top, stat_of(i).m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    auto weigh = [&](int i, const Stat &s) {
+        const float w = s.m == -INFINITY ? 0.0f : exp2_sfu(s.m - top);
+        weight[i] = w;
+        l += w * s.l;
+    };
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        if (lane + 32 * i < parts) weigh(lane + 32 * i, mine[i]);
+    for (int i = lane + 32 * kEach; i < parts; i += 32) weigh(i, stat_of(i));
+    l = warp_sum(l);
+    __syncwarp();
+    float4 o[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = sub; i0 < parts; i0 += kBatch * kStep) {
+        if (i0 > sub) request(i0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float w = weight[min(i0 + i * kStep, parts - 1)];
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                const float4 &u = v[i][k];
+                if (i0 + i * kStep < parts) o[k].x += w * u.x, o[k].y += w * u.y, o[k].z += w * u.z, o[k].w += w * u.w;
             }
         }
-        const float inv = nan ? NAN : l == 0.0f ? 1.0f : 1.0f / l;
-        const int64_t out = (int64_t)j.n * a.S * a.H + row;
-        uint2 u;
-        u.x = pack2(o.x * inv, o.y * inv);
-        u.y = pack2(o.z * inv, o.w * inv);
-        *(uint2 *)(a.o + out * kLatent + 4 * threadIdx.x) = u;
-        if (a.lse && threadIdx.x == 0)
-            a.lse[out] = nan ? NAN : top == -INFINITY ? -INFINITY : (top + log2_sfu(l)) * kLn2;
     }
+    if (MANY) {
+        sums[sub][lane] = o[0];
+        __syncthreads();
+        if (wid) return;
+#pragma unroll
+        for (int i = 1; i < kStep; ++i) {
+            const float4 u = sums[i][lane];
+            o[0].x += u.x, o[0].y += u.y, o[0].z += u.z, o[0].w += u.w;
+        }
+    }
+    const float inv = l == 0.0f ? 1.0f : 1.0f / l;
+    const int64_t out = (int64_t)j.n * a.S * a.H + row;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k)
+        *(uint2 *)(a.o + out * kLatent + 128 * k + d0) =
+            make_uint2(pack2(o[k].x * inv, o[k].y * inv), pack2(o[k].z * inv, o[k].w * inv));
+    if (a.lse && lane == 0 && d0 == 0) a.lse[out] = l == 0.0f ? -INFINITY : (top + log2_sfu(l)) * kLn2;
+}
+
+// The cache as {64 columns, 8 rows, 9 blocks, groups of 8 rows}, a copy being two groups.
+inline bool encode_cache(CUtensorMap *m, const void *base, int64_t rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {64, 8, 9, (cuuint64_t)rows / 8};
+    const cuuint64_t strides[3] = {kLatentRow * 2, 128, 8 * kLatentRow * 2};
+    const cuuint32_t box[4] = {64, 8, 9, 2};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline size_t joins_bytes(const Grid &g) { return align_up((size_t)g.ranges * sizeof(Join), 256); }
+inline size_t stats_bytes(const Grid &g) {
+    return align_up((size_t)g.ranges * g.row_blocks * kRows * 2 * sizeof(Stat), 256);
+}
 
 }  // namespace
 
 size_t latent_decode_workspace_bytes(int n_seqs, int S, int H) {
     const Grid g = decode_grid(S, H);
-    return joins_bytes(g) + (size_t)g.ranges * g.row_blocks * 2 * sizeof(Part);
+    return joins_bytes(g) + stats_bytes(g) + (size_t)g.ranges * g.row_blocks * 2 * sizeof(Part);
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
     const Grid g = decode_grid(a.S, a.H);
-    DecodeParams p{a, g.row_blocks, g.ranges, nullptr, (Join *)a.workspace};
-    p.parts = (Part *)((uint8_t *)a.workspace + joins_bytes(g));
+    DecodeParams p{a, g.row_blocks, g.ranges};
+    uint8_t *ws = (uint8_t *)a.workspace;
+    p.joins = (Join *)ws;
+    p.stats = (Stat *)(ws + joins_bytes(g));
+    p.parts = (Part *)(ws + joins_bytes(g) + stats_bytes(g));
     CUtensorMap map_q, map_c;
-    const int box = std::min(1 << a.page_shift, kTile);
     if (!encode_rows64(&map_q, a.q, kLatentRow, (int64_t)a.n_seqs * a.S * a.H, kLatentRow, kRows) ||
-        !encode_rows64(&map_c, a.cache, kLatentRow, a.n_pages << a.page_shift, kLatentRow, box))
+        !encode_cache(&map_c, a.cache, a.n_pages << a.page_shift))
         return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
@@ -531,8 +682,14 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream)
     e = launch_dependent(latent_decode_kernel, dim3(g.ranges * g.row_blocks), dim3(kThreads), kSmemBytes,
                          stream, map_q, map_c, p);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(latent_decode_join_kernel, dim3(g.ranges * g.row_blocks, kRows / kJoinRows), dim3(128),
-                         0, stream, p);
+    const size_t weights = (size_t)8 * g.ranges * sizeof(float);
+    const int joins = std::min(a.n_seqs, g.ranges), rows = a.S * a.H;
+    if (joins * rows <= 128)
+        e = launch_dependent(latent_decode_join_kernel<true>, dim3(joins, rows, 4), dim3(kJoinThreads), weights, stream,
+                             p);
+    else
+        e = launch_dependent(latent_decode_join_kernel<false>, dim3(joins, (rows + 7) / 8), dim3(kJoinThreads), weights,
+                             stream, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -104,6 +104,8 @@ def test_decode_refuses(lib, kw):
 
 def test_decode_other_statuses(lib):
     assert _decode(lib, S=64, H=128) == UNSUPPORTED
+    assert _decode(lib, n=65536) == UNSUPPORTED
+    assert _decode(lib, n=1 << 10, page=256, max_pages=1 << 18) == UNSUPPORTED
     assert _decode(lib, ws=None) == WORKSPACE
     assert _decode(lib, ws=BASE + 16) == WORKSPACE
     assert _decode(lib, wsb=0) == WORKSPACE
