@@ -103,6 +103,44 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
+// D[M x N] (+)= A[M x 16] * B[N x 16]^T with A in TMEM (lane = row, two bf16 a column)
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Cluster launch control: asks for a CTA of this grid that has not been
+// launched yet; the 16-byte answer lands in shared memory.  Not asked again
+// after a refusal.
+__device__ __forceinline__ void next_cta_request(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// blockIdx.x of the CTA that the answer hands over, -1 if there is none
+__device__ __forceinline__ int next_cta_answer(const void *answer) {
+    int x;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\t"
+        "mov.b32 %0, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}\n"
+        : "=r"(x), "=r"(ok)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return ok ? x : -1;
+}
+
 // Map over bf16 rows of `width` elements, `stride` elements apart, with boxes
 // of 64 columns (128 bytes, 128-byte swizzle) by `box_rows` rows: one K-block
 // of an SW128 operand tile.  Rows outside are filled with zeros.
@@ -115,6 +153,20 @@ inline bool encode_rows64(CUtensorMap *m, const void *base, int64_t width, int64
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same per head: {width of a head, heads, tokens}, tokens `stride` elements apart.
+inline bool encode_heads64(CUtensorMap *m, const void *base, int width, int heads, int64_t tokens, int64_t stride,
+                           int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
