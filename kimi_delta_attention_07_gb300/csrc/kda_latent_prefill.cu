@@ -59,10 +59,12 @@ constexpr uint32_t kTmemO = 256;  // X_t at 128 t, O_t at 256 + 128 t
 
 struct Item {
     int n, h, q0, lq, off;  // sequence, head, first query in it, its queries, lk - lq
-    int lk, steps[2];       // keys, steps of each tile
+    int lk, steps0, steps1; // keys, steps of each tile
     int64_t qa, ka;         // the sequence's first query and key
     int masked;             // first step with a key that some row does not see
     int valid;              // 0: no further item
+    __device__ __forceinline__ int steps(int t) const { return t ? steps1 : steps0; }
+    __device__ __forceinline__ int most() const { return max(steps0, steps1); }
 };
 
 struct PrefillParams {
@@ -80,6 +82,8 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t two_bf16) {
            ((two_bf16 & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
 
+// POSITIVE: scale > 0, so that the largest product is the largest score
+template <bool POSITIVE>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv,
                           const __grid_constant__ CUtensorMap map_r, const PrefillParams p) {
@@ -142,11 +146,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto item_done = [&](int it) { mbar_arrive(&item_empty[it & 1]); };
 
-    // a row of scores takes 128 registers: 2 x 128 threads of 208 and 128 of 88 are what the CTA
-    // was launched with (384 of 168)
-    if (wid >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-
     if (wid == 8) {
         // ---- scheduling and TMA
         if (elect_one()) {
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int t = 0; t < 2; ++t) {
                         const int r0 = s.q0 + t * kTile, r1 = min(r0 + kTile, s.lq);  // rows [r0, r1)
                         const int seen = r1 <= r0 ? 0 : a.causal ? min(s.lk, r1 + s.off) : s.lk;
-                        s.steps[t] = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+                        (t ? s.steps1 : s.steps0) = seen > 0 ? (seen + kTile - 1) / kTile : 0;
                         if (r1 > r0 && a.causal) first = min(first, max(r0 + 1 + s.off, 0));
                     }
                     s.masked = first / kTile;
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&item_full[it & 1]);
                     ++it;
                     for (int t = 0; t < 2; ++t) {
-                        if (cur.steps[t] == 0) continue;
+                        if (cur.steps(t) == 0) continue;
                         wait(&q_empty[t], (qn[t] & 1) ^ 1);
                         ++qn[t];
                         mbar_arrive_expect_tx(&q_full[t], 3 * kBlock);
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_3d(sm + kSmQ + (t * 3 + b) * kBlock, &map_q, b * 64, cur.h,
                                         (int)cur.qa + cur.q0 + t * kTile, &q_full[t]);
                     }
-                    const int steps = max(cur.steps[0], cur.steps[1]);
+                    const int steps = cur.most();
                     for (int i = 0; i < steps && !dead; ++i) {
                         const int row = (int)cur.ka + i * kTile;
                         for (int b = 0; b < 5; ++b, ++c) {
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0;; ++it) {
                 const Item s = item_of(it);
                 if (dead || !s.valid) break;
-                const int steps = max(s.steps[0], s.steps[1]);
+                const int steps = s.most();
                 // X_t(i); its K blocks are released by the last tile that reads them
                 auto first_product = [&](int t, uint32_t ck, bool release) {
 #pragma unroll
@@ -258,23 +257,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&x_full[t]);
                 };
                 for (int t = 0; t < 2; ++t)
-                    if (s.steps[t] > 0) {
+                    if (s.steps(t) > 0) {
                         wait(&q_full[t], qn[t] & 1);
                         ++qn[t];
-                        first_product(t, c, t == 1 || s.steps[1] == 0);
-                        if (s.steps[t] == 1) mma_commit(&q_empty[t]);
+                        first_product(t, c, t == 1 || s.steps1 == 0);
+                        if (s.steps(t) == 1) mma_commit(&q_empty[t]);
                     }
                 for (int i = 0; i < steps && !dead; ++i, c += 5) {
 #pragma unroll 1
                     for (int t = 0; t < 2; ++t) {
-                        if (i >= s.steps[t]) continue;
+                        if (i >= s.steps(t)) continue;
                         wait(&p_full[t], pn[t] & 1);
                         ++pn[t];
                         if (i == 0) {
                             if (on[t] > 0) wait(&o_empty[t], (on[t] - 1) & 1);
                             ++on[t];
                         }
-                        const bool last_v = t == 1 || i >= s.steps[1];
+                        const bool last_v = t == 1 || i >= s.steps1;
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             const uint32_t cv = c + 3 + b, slot = cv % kRing;
@@ -287,10 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             idesc_o, i > 0 || k > 0);
                             if (last_v) mma_commit(&empty[slot]);
                         }
-                        if (i + 1 == s.steps[t]) mma_commit(&o_full[t]);
-                        if (i + 1 < s.steps[t]) {
-                            first_product(t, c + 5, t == 1 || i + 1 >= s.steps[1]);
-                            if (i + 2 == s.steps[t]) mma_commit(&q_empty[t]);
+                        if (i + 1 == s.steps(t)) mma_commit(&o_full[t]);
+                        if (i + 1 < s.steps(t)) {
+                            first_product(t, c + 5, t == 1 || i + 1 >= s.steps1);
+                            if (i + 2 == s.steps(t)) mma_commit(&q_empty[t]);
                         }
                     }
                 }
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0;; ++it) {
             const Item s = item_of(it);
             if (__any_sync(0xffffffffu, dead || !s.valid)) break;
-            const int steps = max(s.steps[0], s.steps[1]);
+            const int steps = s.most();
             for (int i = 0; i < steps; ++i, c += 5) {
                 if (i < s.masked) continue;
                 const uint32_t slot = (c + 3 + g) % kRing;
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool real = row < s.lq;
             const int limit = !real ? 0 : a.causal ? min(s.lk, row + 1 + s.off) : s.lk;  // keys below it are seen
             float m = -INFINITY, l = 0.0f;  // m in units of x / |scale|
-            const int steps = s.steps[t];
+            const int steps = s.steps(t);
             bool gave_up = false;
             for (int i = 0; i < steps; ++i, ++xn) {
                 wait(&x_full[t], xn & 1);
@@ -361,22 +360,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                float x[kTile];
+                // scores 32 k .. 32 k + 31 of the row, requested and then prepared
+                const int left = limit - i * kTile;
+                const bool hide = __any_sync(0xffffffffu, left < kTile);
+                auto prepare = [&](int k, float (&x)[32]) {
+                    if (!POSITIVE) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(tx + 32 * k, *reinterpret_cast<float(*)[32]>(x + 32 * k));
-                tmem_ld_wait();
-                if (a.scale <= 0.0f) {
+                        for (int j = 0; j < 32; ++j) x[j] = a.scale < 0.0f ? -x[j] : 0.0f;
+                    }
+                    if (hide) {
 #pragma unroll
-                    for (int j = 0; j < kTile; ++j) x[j] = a.scale < 0.0f ? -x[j] : 0.0f;
-                }
-                if (__any_sync(0xffffffffu, limit < (i + 1) * kTile)) {
-                    const int left = limit - i * kTile;
+                        for (int j = 0; j < 32; ++j) x[j] = 32 * k + j < left ? x[j] : -INFINITY;
+                    }
+                };
+                float x0[32], x1[32], top = -INFINITY;
+                auto largest = [&](int k, float (&x)[32]) {
+                    prepare(k, x);
 #pragma unroll
-                    for (int j = 0; j < kTile; ++j) x[j] = j < left ? x[j] : -INFINITY;
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < kTile; ++j) top = fmaxf(top, x[j]);
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, x[j]);
+                };
+                tmem_ld32(tx, x0);
+                tmem_ld_wait32(x0);
+                tmem_ld32(tx + 32, x1);
+                largest(0, x0);
+                tmem_ld_wait32(x1);
+                tmem_ld32(tx + 64, x0);
+                largest(1, x1);
+                tmem_ld_wait32(x0);
+                tmem_ld32(tx + 96, x1);
+                largest(2, x0);
+                tmem_ld_wait32(x1);
+                tmem_ld32(tx, x0);
+                largest(3, x1);
+                tmem_ld_wait32(x0);
+                tmem_ld32(tx + 32, x1);
                 const bool raise = (top - m) * scale2 > kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? exp2_sfu((m - top) * scale2) : 1.0f;
@@ -384,32 +401,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= f;
                     if (i > 0) {  // X_t(i) was issued after P_t V(i-1): O_t is complete
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float o[32];
-                            tmem_ld32(to + 32 * k, o);
+                        for (int k = 0; k < 8; ++k) {
+                            float o[16];
+                            tmem_ld16(to + 16 * k, o);
                             tmem_ld_wait();
-                            uint32_t u[32];
+                            uint32_t u[16];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * f);
-                            tmem_st32(to + 32 * k, u);
+                            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * f);
+                            tmem_st16(to + 16 * k, u);
                         }
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m * scale2;
-                float sum = 0.0f;
+                // P over the columns of scores that have been read: p_k takes 16 k .. 16 k + 15
+                auto weigh = [&](int k, float (&x)[32]) {
+                    prepare(k, x);
+                    uint32_t u[16];
+                    float sum = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float e0 = exp2_sfu(fmaf(x[64 * k + 2 * j], scale2, -ref));
-                        const float e1 = exp2_sfu(fmaf(x[64 * k + 2 * j + 1], scale2, -ref));
+                    for (int j = 0; j < 16; ++j) {
+                        const float e0 = exp2_sfu(fmaf(x[2 * j], scale2, -ref));
+                        const float e1 = exp2_sfu(fmaf(x[2 * j + 1], scale2, -ref));
                         sum += e0 + e1;
                         u[j] = pack2(e0, e1);
                     }
-                    tmem_st32(tx + 32 * k, u);
-                }
-                l += sum;
+                    l += sum;
+                    tmem_st16(tx + 16 * k, u);
+                };
+                weigh(0, x0);
+                tmem_ld_wait32(x1);
+                tmem_ld32(tx + 64, x0);
+                weigh(1, x1);
+                tmem_ld_wait32(x0);
+                tmem_ld32(tx + 96, x1);
+                weigh(2, x0);
+                tmem_ld_wait32(x1);
+                weigh(3, x1);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&p_full[t]);
@@ -487,14 +514,14 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t strea
     } else {
         map_kv = map_r = map_q;  // no key: not used
     }
-    cudaError_t e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    auto kernel = a.scale > 0.0f ? latent_prefill_kernel<true> : latent_prefill_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     // every sequence adds at most one incomplete block
     const int64_t blocks = a.total_q / kItem + std::min<int64_t>(a.n_seqs, a.total_q);
     if (blocks * a.H > INT32_MAX) return cudaErrorInvalidValue;
-    latent_prefill_kernel<<<dim3((unsigned)(blocks * a.H)), kThreads, kSmemBytes, stream>>>(map_q, map_kv, map_r,
-                                                                                        PrefillParams{a});
+    kernel<<<dim3((unsigned)(blocks * a.H)), kThreads, kSmemBytes, stream>>>(map_q, map_kv, map_r, PrefillParams{a});
     return cudaGetLastError();
 }
 
