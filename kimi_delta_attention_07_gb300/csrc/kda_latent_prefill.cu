@@ -12,13 +12,17 @@
 //   P_0 V(i), X_0(i+1), P_1 V(i), X_1(i+1), ...
 // 768 + 512 clocks a tile and step at the tensor core's 4096 products a clock.
 //
-// Softmax: a thread owns a query row (TMEM lane), so maximum, sum and rescaling
-// need no exchange.  The reference that p is taken against is raised (and the
+// What bounds a step is the chain X_t(i), softmax, P_t V(i), X_t(i+1) of a tile, whose
+// scores and P share columns; with one thread a row it took 4650 clocks against
+// the 2560 that the tensor core needs for both tiles.  So two threads own a query
+// row (TMEM lane), 64 keys of a step each: they exchange their maxima in a step
+// and their sums at the end, and hand P over in two parts, the first of which is
+// multiplied while the second is computed.  The reference that p is taken against is raised (and the
 // row of O rescaled) only where the row's maximum passes it by 2^8; p, its sum
 // and O share it, so that the quotient is unchanged.
 //
 // K and V tiles come as blocks of 64 columns (16 KB) through a ring of eight,
-// K(i) three, V(i) two, released block by block.  The positional key's block is
+// K(i) three, V(i) two.  The positional key's block is
 // read for every head from the one shared copy.
 //
 // Masked places: keys that a row does not see get p = 0, and 0 times a value has
@@ -31,9 +35,10 @@
 // queries and head, heaviest first within a sequence, and a running CTA takes
 // over the next unlaunched one, so that its loads overlap the last epilogue.
 //
-// Warps: 0..3 and 4..7 softmax and epilogue of the two tiles, 8 TMA and
-// scheduling, 9 MMA, 10 and 11 the value blocks' check.
+// Warps: 0..7 and 8..15 softmax and epilogue of the two tiles, 16 TMA and
+// scheduling, 17 MMA, 18 and 19 the value blocks' check.
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_attn.cuh"
 
@@ -45,7 +50,7 @@ namespace {
 
 constexpr int kTile = 128;           // queries per tile, keys per step
 constexpr int kItem = 2 * kTile;     // queries per CTA
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kRing = 8;             // 16 KB blocks
 constexpr uint32_t kBlock = kTile * 128;
 constexpr float kRaise = 8.0f;       // log2 by which a score may pass its row's reference
@@ -53,7 +58,8 @@ constexpr float kRaise = 8.0f;       // log2 by which a score may pass its row's
 // shared memory (from a 1024-byte boundary)
 constexpr uint32_t kSmQ = 0;                          // [2 tiles][3 blocks]
 constexpr uint32_t kSmRing = kSmQ + 2 * 3 * kBlock;   // kRing blocks
-constexpr uint32_t kSmemBytes = kSmRing + kRing * kBlock + 1024;
+constexpr uint32_t kSmShared = kSmRing + kRing * kBlock;
+constexpr int kPieces = 128;  // of the sequences, for finding the one that a block belongs to
 
 constexpr uint32_t kTmemO = 256;  // X_t at 128 t, O_t at 256 + 128 t
 
@@ -66,6 +72,20 @@ struct Item {
     __device__ __forceinline__ int steps(int t) const { return t ? steps1 : steps0; }
     __device__ __forceinline__ int most() const { return max(steps0, steps1); }
 };
+
+struct Shared {
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], x_full[2], p_full[2][2], o_full[2], o_empty[2],
+        unchecked[2][2], item_full[2], item_empty[2], next_full;
+    uint4 next_answer;
+    Item items[2];
+    float half[2][2][kTile];  // what the two threads of a row exchange
+    int piece[kPieces];       // blocks of 256 queries of the sequences before each piece
+    int warp_total[kPieces / 32];
+    volatile int dead, odd[2];
+    uint32_t tmem_base;
+};
+constexpr uint32_t kSmemBytes = kSmShared + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct PrefillParams {
     LatentPrefillArgs a;
@@ -87,82 +107,85 @@ template <bool POSITIVE>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv,
                           const __grid_constant__ CUtensorMap map_r, const PrefillParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    __shared__ uint64_t full[kRing], empty[kRing], q_full[2], q_empty[2], x_full[2], p_full[2], o_full[2], o_empty[2],
-        unchecked[2][2], item_full[2], item_empty[2], next_full;
-    __shared__ __align__(16) uint4 next_answer;
-    __shared__ Item items[2];
-    __shared__ int piece[kThreads];  // blocks of the sequences before each thread's
-    __shared__ int warp_total[kThreads / 32];
-    __shared__ volatile int dead, odd[2];
-    __shared__ uint32_t tmem_base;
+    // all shared memory is dynamic, so that it begins on a 1024-byte boundary
+    extern __shared__ __align__(1024) uint8_t sm[];
+    Shared &sh = *reinterpret_cast<Shared *>(sm + kSmShared);
+    auto &k_full = sh.k_full, &k_empty = sh.k_empty, &v_full = sh.v_full, &v_empty = sh.v_empty;
+    auto &q_full = sh.q_full, &q_empty = sh.q_empty, &x_full = sh.x_full, &o_full = sh.o_full, &o_empty = sh.o_empty,
+         &item_full = sh.item_full, &item_empty = sh.item_empty;
+    auto &p_full = sh.p_full, &unchecked = sh.unchecked;
+    volatile int &dead = sh.dead;
+    volatile int *odd = sh.odd;
 
     const LatentPrefillArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 2), mbar_init(&v_empty[i], 1);  // a copy and a second arrival, or two checks
             mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1);
-            mbar_init(&x_full[i], 1), mbar_init(&p_full[i], 128);
-            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 128);
+            mbar_init(&x_full[i], 1), mbar_init(&p_full[i][0], 256), mbar_init(&p_full[i][1], 256);
+            mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 256);
             mbar_init(&unchecked[0][i], 1), mbar_init(&unchecked[1][i], 1);
-            mbar_init(&item_full[i], 1), mbar_init(&item_empty[i], 11);
+            mbar_init(&item_full[i], 1), mbar_init(&item_empty[i], 19);
         }
-        mbar_init(&next_full, 1);
+        mbar_init(&sh.next_full, 1);
         fence_mbar_init();
         dead = 0;
     }
-    if (wid == 9) tmem_alloc(&tmem_base, 512);
+    if (wid == 17) tmem_alloc(&sh.tmem_base, 512);
     // the blocks of 256 queries of the sequences before each thread's piece
-    const int per = (a.n_seqs + kThreads - 1) / kThreads;
-    {
+    const int per = (a.n_seqs + kPieces - 1) / kPieces;
+    int upto = 0, own = 0;
+    if (tid < kPieces) {
         const int n0 = min(tid * per, a.n_seqs), n1 = min(n0 + per, a.n_seqs);
-        int mine = 0;
-        for (int n = n0; n < n1; ++n) mine += blocks_of(a, n);
-        int upto = mine;
+        for (int n = n0; n < n1; ++n) own += blocks_of(a, n);
+        upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += y;
         }
-        if (lane == 31) warp_total[wid] = upto;
-        __syncthreads();
-        for (int w = 0; w < wid; ++w) upto += warp_total[w];
-        piece[tid] = upto - mine;
+        if (lane == 31) sh.warp_total[wid] = upto;
+    }
+    __syncthreads();
+    if (tid < kPieces) {
+        for (int w = 0; w < wid; ++w) upto += sh.warp_total[w];
+        sh.piece[tid] = upto - own;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = sh.tmem_base;
     // a bounded wait; once one has given up, none waits any more
     auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return;
         if (!dead && !mbar_wait(bar, parity)) dead = 1;
     };
     // the it-th item of this CTA, as the scheduling thread published it
     auto item_of = [&](int it) -> const Item & {
         wait(&item_full[it & 1], (it >> 1) & 1);
-        return items[it & 1];
+        return sh.items[it & 1];
     };
     auto item_done = [&](int it) { mbar_arrive(&item_empty[it & 1]); };
 
-    if (wid == 8) {
+    if (wid == 16) {
         // ---- scheduling and TMA
         if (elect_one()) {
             int it = 0, qn[2] = {0, 0};  // items published; queries' tiles loaded
-            uint32_t c = 0, checks = 0;  // blocks loaded; steps whose values are checked
+            uint32_t step = 0, checks = 0;  // steps loaded; those whose values are checked
             int cta = blockIdx.x;
             for (int asked = 0; cta >= 0; ++asked) {
-                mbar_arrive_expect_tx(&next_full, 16);
-                next_cta_request(&next_answer, &next_full);
+                mbar_arrive_expect_tx(&sh.next_full, 16);
+                next_cta_request(&sh.next_answer, &sh.next_full);
                 const int rank = cta / a.H;
                 // the piece that holds block `rank`, then the sequence in it
-                int lo = 0, hi = kThreads;
+                int lo = 0, hi = kPieces;
                 while (lo + 1 < hi) {
                     const int mid = (lo + hi) >> 1;
-                    if (piece[mid] <= rank) lo = mid; else hi = mid;
+                    if (sh.piece[mid] <= rank) lo = mid; else hi = mid;
                 }
-                int n = lo * per, before = piece[lo], blocks = 0;
+                int n = lo * per, before = sh.piece[lo], blocks = 0;
                 for (; n < min((lo + 1) * per, a.n_seqs); ++n) {
                     blocks = blocks_of(a, n);
                     if (rank < before + blocks) break;
@@ -171,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (blocks > 0) {
                     wait(&item_empty[it & 1], ((it >> 1) & 1) ^ 1);
-                    Item &s = items[it & 1];
+                    Item &s = sh.items[it & 1];
                     s.n = n;
                     s.h = cta - rank * a.H;
                     s.qa = a.cu_q[n];
@@ -203,112 +226,140 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         (int)cur.qa + cur.q0 + t * kTile, &q_full[t]);
                     }
                     const int steps = cur.most();
-                    for (int i = 0; i < steps && !dead; ++i) {
+                    for (int i = 0; i < steps && !dead; ++i, ++step) {
+                        // ring blocks 5 step ..: K three, V two; block c takes the place of block c - 8, which
+                        // for K(step) are K(step - 2)'s last and V(step - 2)'s, for V(step) K(step - 1)'s first two
                         const int row = (int)cur.ka + i * kTile;
-                        for (int b = 0; b < 5; ++b, ++c) {
-                            const uint32_t slot = c % kRing;
-                            wait(&empty[slot], ((c / kRing) & 1) ^ 1);
-                            // values to be checked land on the checking warp's barrier; it signals `full`
-                            uint64_t *bar = b >= 3 && i >= cur.masked ? &unchecked[b - 3][checks & 1] : &full[slot];
-                            mbar_arrive_expect_tx(bar, kBlock);
-                            uint8_t *dst = sm + kSmRing + slot * kBlock;
-                            if (b == 2) tma_load_2d(dst, &map_r, 0, row, bar);
-                            else tma_load_3d(dst, &map_kv, (b < 2 ? b : b - 1) * 64, cur.h, row, bar);
+                        const uint32_t par = step & 1, before = ((step >> 1) & 1) ^ 1, c = 5 * step;
+                        auto block = [&](uint32_t b) { return sm + kSmRing + ((c + b) % kRing) * kBlock; };
+                        wait(&k_empty[par], before);
+                        mbar_arrive_expect_tx(&k_full[par], 3 * kBlock);
+                        tma_load_3d(block(0), &map_kv, 0, cur.h, row, &k_full[par]);
+                        wait(&v_empty[par], before);
+                        tma_load_3d(block(1), &map_kv, 64, cur.h, row, &k_full[par]);
+                        tma_load_2d(block(2), &map_r, 0, row, &k_full[par]);
+                        if (step > 0) wait(&k_empty[par ^ 1], ((step - 1) >> 1) & 1);
+                        if (i >= cur.masked) {  // to the checking warps, which signal v_full
+                            for (int g = 0; g < 2; ++g) {
+                                mbar_arrive_expect_tx(&unchecked[g][checks & 1], kBlock);
+                                tma_load_3d(block(3 + g), &map_kv, kNope + 64 * g, cur.h, row, &unchecked[g][checks & 1]);
+                            }
+                            ++checks;
+                        } else {
+                            mbar_arrive_expect_tx(&v_full[par], 2 * kBlock);
+                            tma_load_3d(block(3), &map_kv, kNope, cur.h, row, &v_full[par]);
+                            tma_load_3d(block(4), &map_kv, kNope + 64, cur.h, row, &v_full[par]);
+                            mbar_arrive(&v_full[par]);
                         }
-                        if (i >= cur.masked) ++checks;
                     }
                 }
-                wait(&next_full, asked & 1);
-                cta = dead ? -1 : next_cta_answer(&next_answer);
+                wait(&sh.next_full, asked & 1);
+                cta = dead ? -1 : next_cta_answer(&sh.next_answer);
                 fence_async_smem();
             }
             wait(&item_empty[it & 1], ((it >> 1) & 1) ^ 1);
-            items[it & 1].valid = 0;
+            sh.items[it & 1].valid = 0;
             mbar_arrive(&item_full[it & 1]);
         }
         __syncwarp();
-    } else if (wid == 9) {
-        // ---- MMA, issued by one thread
+    } else if (wid == 17) {
+        // ---- MMA, issued by one thread.  It shares its scheduler with four softmax warps, so that
+        // every instruction between two MMAs costs some twenty clocks: one wait for a whole K
+        // or V tile, ahead of the wait for P, and nothing recomputed.
         if (elect_one()) {
-            const uint32_t q_s = smem_u32(sm + kSmQ), ring = smem_u32(sm + kSmRing);
+            const uint32_t q_lo = (smem_u32(sm + kSmQ) >> 4) | (1u << 16), k_lo = (smem_u32(sm + kSmRing) >> 4) | (1u << 16),
+                           v_lo = (smem_u32(sm + kSmRing) >> 4) | ((uint32_t)((kTile * 128) >> 4) << 16);
+            constexpr uint32_t kStep = kBlock >> 4;  // a block, in descriptor units
+            constexpr uint64_t hi = (uint64_t)kDescHi << 32;
             constexpr uint32_t idesc_x = idesc_bf16(kTile, kTile);
             constexpr uint32_t idesc_o = idesc_bf16(kTile, 64) | (1u << 16);
-            uint32_t c = 0;  // ring blocks before this step
-            int qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
+            uint32_t step = 0, pn0 = 0, pn1 = 0;  // steps and P tiles so far
+            int qn[2] = {0, 0}, on[2] = {0, 0};
+            // X_t of step n: K's ring blocks are 5 n ..
+            auto scores = [&](auto t, uint32_t n) {
+                tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < 3; ++b) {
+                    const uint32_t k = k_lo + ((5 * n + b) % kRing) * kStep;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_bf16(tmem + t * kTile, hi | (q_lo + (t * 3 + b) * kStep + 2 * j), hi | (k + 2 * j), idesc_x,
+                                 b + j > 0);
+                }
+                mma_commit(&x_full[t]);
+            };
+            // O_t += P_t V(step); P comes in two parts: keys 0..31 and 64..95, then the others
+            auto values = [&](auto t, uint32_t pn, bool first) {
+                const uint32_t v0 = v_lo + ((5 * step + 3) % kRing) * kStep, v1 = v_lo + ((5 * step + 4) % kRing) * kStep;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    wait(&p_full[t][part], pn & 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = (j >> 1) * 4 + part * 2 + (j & 1);
+                            mma_bf16_ts(tmem + kTmemO + t * kTile + b * 64, tmem + t * kTile + k * 8,
+                                        hi | ((b ? v1 : v0) + 128 * k), idesc_o, !first || part + j > 0);
+                        }
+                }
+            };
+            const std::integral_constant<int, 0> t0;
+            const std::integral_constant<int, 1> t1;
             for (int it = 0;; ++it) {
                 const Item s = item_of(it);
                 if (dead || !s.valid) break;
-                const int steps = s.most();
-                // X_t(i); its K blocks are released by the last tile that reads them
-                auto first_product = [&](int t, uint32_t ck, bool release) {
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) {
-                        const uint32_t slot = (ck + b) % kRing;
-                        wait(&full[slot], ((ck + b) / kRing) & 1);
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + t * kTile,
-                                     ((uint64_t)kDescHi << 32) | operand_lo<false, kTile>(q_s + (t * 3 + b) * kBlock, k),
-                                     ((uint64_t)kDescHi << 32) | operand_lo<false, kTile>(ring + slot * kBlock, k),
-                                     idesc_x, b + k > 0);
-                        if (release) mma_commit(&empty[slot]);
+                const int s0 = s.steps0, s1 = s.steps1, steps = s.most();
+                if (s0 > 0) wait(&q_full[0], qn[0]++ & 1);
+                if (s1 > 0) wait(&q_full[1], qn[1]++ & 1);
+                if (steps > 0) {
+                    wait(&k_full[step & 1], (step >> 1) & 1);
+                    if (s0 > 0) scores(t0, step);
+                    if (s1 > 0) scores(t1, step);
+                    mma_commit(&k_empty[step & 1]);
+                    if (s0 == 1) mma_commit(&q_empty[0]);
+                    if (s1 == 1) mma_commit(&q_empty[1]);
+                    if (s0 > 0 && on[0]++ > 0) wait(&o_empty[0], on[0] & 1);
+                    if (s1 > 0 && on[1]++ > 0) wait(&o_empty[1], on[1] & 1);
+                }
+                for (int i = 0; i < steps && !dead; ++i, ++step) {
+                    const uint32_t next = step + 1;
+                    wait(&v_full[step & 1], (step >> 1) & 1);
+                    if (i + 1 < steps) wait(&k_full[next & 1], (next >> 1) & 1);
+                    if (i < s0) {
+                        values(t0, pn0++, i == 0);
+                        if (i + 1 < s0) scores(t0, next);
+                        else mma_commit(&o_full[0]);
+                        if (i + 2 == s0) mma_commit(&q_empty[0]);
                     }
-                    mma_commit(&x_full[t]);
-                };
-                for (int t = 0; t < 2; ++t)
-                    if (s.steps(t) > 0) {
-                        wait(&q_full[t], qn[t] & 1);
-                        ++qn[t];
-                        first_product(t, c, t == 1 || s.steps1 == 0);
-                        if (s.steps(t) == 1) mma_commit(&q_empty[t]);
+                    if (i < s1) {
+                        values(t1, pn1++, i == 0);
+                        mma_commit(&v_empty[step & 1]);
+                        if (i + 1 < s1) scores(t1, next);
+                        else mma_commit(&o_full[1]);
+                        if (i + 2 == s1) mma_commit(&q_empty[1]);
+                    } else {
+                        mma_commit(&v_empty[step & 1]);
                     }
-                for (int i = 0; i < steps && !dead; ++i, c += 5) {
-#pragma unroll 1
-                    for (int t = 0; t < 2; ++t) {
-                        if (i >= s.steps(t)) continue;
-                        wait(&p_full[t], pn[t] & 1);
-                        ++pn[t];
-                        if (i == 0) {
-                            if (on[t] > 0) wait(&o_empty[t], (on[t] - 1) & 1);
-                            ++on[t];
-                        }
-                        const bool last_v = t == 1 || i >= s.steps1;
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const uint32_t cv = c + 3 + b, slot = cv % kRing;
-                            wait(&full[slot], (cv / kRing) & 1);
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                mma_bf16_ts(tmem + kTmemO + t * kTile + b * 64, tmem + t * kTile + k * 8,
-                                            ((uint64_t)kDescHi << 32) | operand_lo<true, kTile>(ring + slot * kBlock, k),
-                                            idesc_o, i > 0 || k > 0);
-                            if (last_v) mma_commit(&empty[slot]);
-                        }
-                        if (i + 1 == s.steps(t)) mma_commit(&o_full[t]);
-                        if (i + 1 < s.steps(t)) {
-                            first_product(t, c + 5, t == 1 || i + 1 >= s.steps1);
-                            if (i + 2 == s.steps(t)) mma_commit(&q_empty[t]);
-                        }
-                    }
+                    if (i + 1 < steps) mma_commit(&k_empty[next & 1]);
                 }
                 item_done(it);
             }
         }
         __syncwarp();
-    } else if (wid >= 10) {
-        // ---- the check of V's block g in steps with masked places, between its copy and `full`
-        const int g = wid - 10;
-        uint32_t c = 0;
+    } else if (wid >= 18) {
+        // ---- the check of V's block g in steps with masked places, between its copy and v_full
+        const int g = wid - 18;
+        uint32_t step = 0;
         int checks = 0;
         for (int it = 0;; ++it) {
             const Item s = item_of(it);
             if (__any_sync(0xffffffffu, dead || !s.valid)) break;
             const int steps = s.most();
-            for (int i = 0; i < steps; ++i, c += 5) {
+            for (int i = 0; i < steps; ++i, ++step) {
                 if (i < s.masked) continue;
-                const uint32_t slot = (c + 3 + g) % kRing;
+                const uint32_t slot = (5 * step + 3 + g) % kRing;
                 wait(&unchecked[g][checks & 1], (checks >> 1) & 1);
                 const int rows = min(s.lk - i * kTile, kTile);  // keys of the sequence in this tile
                 uint8_t *blk = sm + kSmRing + slot * kBlock;
@@ -331,69 +382,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (found) odd[it & 1] = 1;
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[slot]);
+                if (lane == 0) mbar_arrive(&v_full[step & 1]);
                 ++checks;
             }
             __syncwarp();
             if (lane == 0) item_done(it);
         }
     } else {
-        // ---- softmax of tile t: a thread owns a query row
-        const int t = wid >> 2, quad = wid & 3;
+        // ---- softmax of tile t: two threads own a query row, 64 keys of a step each
+        const int t = wid >> 3, half = (wid >> 2) & 1, quad = wid & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t tx = tmem + t * kTile + lanes, to = tmem + kTmemO + t * kTile + lanes;
+        const uint32_t tx = tmem + t * kTile + lanes, to = tmem + kTmemO + t * kTile + half * 64 + lanes;
         const float scale2 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
+        float *mine = &sh.half[t][half][quad * 32 + lane], *other = &sh.half[t][half ^ 1][quad * 32 + lane];
         int xn = 0, on = 0;
         for (int it = 0;; ++it) {
             const Item s = item_of(it);
-            if (__any_sync(0xffffffffu, dead || !s.valid)) break;
+            if (!named_bar_and(1 + t, 256, !dead && s.valid)) break;
             const int row = s.q0 + t * kTile + quad * 32 + lane;
             const bool real = row < s.lq;
             const int limit = !real ? 0 : a.causal ? min(s.lk, row + 1 + s.off) : s.lk;  // keys below it are seen
             float m = -INFINITY, l = 0.0f;  // m in units of x / |scale|
             const int steps = s.steps(t);
-            bool gave_up = false;
+            bool gave_up = false;  // the same in both halves: decided by their votes
             for (int i = 0; i < steps; ++i, ++xn) {
                 wait(&x_full[t], xn & 1);
-                if (__any_sync(0xffffffffu, dead)) {
+                const bool given = dead;
+                tc_fence_after();
+                float x[2][32], top = -INFINITY;
+                tmem_ld32(tx + 64 * half, x[0]);
+                tmem_ld32(tx + 64 * half + 32, x[1]);
+                tmem_ld_wait32(x[0]);
+                tmem_ld_wait32(x[1]);
+                const int left = limit - i * kTile - 64 * half;
+                if (!POSITIVE) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) x[j >> 5][j & 31] = a.scale < 0.0f ? -x[j >> 5][j & 31] : 0.0f;
+                }
+                if (__any_sync(0xffffffffu, left < 64)) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (j >= left) x[j >> 5][j & 31] = -INFINITY;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    top = max3(max3(top, x[0][j], x[0][j + 1]), x[1][j], x[1][j + 1]);
+                *mine = top;
+                if (!named_bar_and(1 + t, 256, !given)) {
                     gave_up = true;
                     break;
                 }
-                tc_fence_after();
-                // scores 32 k .. 32 k + 31 of the row, requested and then prepared
-                const int left = limit - i * kTile;
-                const bool hide = __any_sync(0xffffffffu, left < kTile);
-                auto prepare = [&](int k, float (&x)[32]) {
-                    if (!POSITIVE) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = a.scale < 0.0f ? -x[j] : 0.0f;
-                    }
-                    if (hide) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = 32 * k + j < left ? x[j] : -INFINITY;
-                    }
-                };
-                float x0[32], x1[32], top = -INFINITY;
-                auto largest = [&](int k, float (&x)[32]) {
-                    prepare(k, x);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, x[j]);
-                };
-                tmem_ld32(tx, x0);
-                tmem_ld_wait32(x0);
-                tmem_ld32(tx + 32, x1);
-                largest(0, x0);
-                tmem_ld_wait32(x1);
-                tmem_ld32(tx + 64, x0);
-                largest(1, x1);
-                tmem_ld_wait32(x0);
-                tmem_ld32(tx + 96, x1);
-                largest(2, x0);
-                tmem_ld_wait32(x1);
-                tmem_ld32(tx, x0);
-                largest(3, x1);
-                tmem_ld_wait32(x0);
-                tmem_ld32(tx + 32, x1);
+                top = fmaxf(top, *other);
                 const bool raise = (top - m) * scale2 > kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? exp2_sfu((m - top) * scale2) : 1.0f;
@@ -402,59 +441,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i > 0) {  // X_t(i) was issued after P_t V(i-1): O_t is complete
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            float o[16];
-                            tmem_ld16(to + 16 * k, o);
+                            float o[8];
+                            tmem_ld8(to + 8 * k, o);
                             tmem_ld_wait();
-                            uint32_t u[16];
+                            uint32_t u[8];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * f);
-                            tmem_st16(to + 16 * k, u);
+                            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(o[j] * f);
+                            tmem_st8(to + 8 * k, u);
                         }
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m * scale2;
-                // P over the columns of scores that have been read: p_k takes 16 k .. 16 k + 15
-                auto weigh = [&](int k, float (&x)[32]) {
-                    prepare(k, x);
+                // P over columns of scores that both halves have read: key j of the step in column j / 2
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
                     uint32_t u[16];
                     float sum = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float e0 = exp2_sfu(fmaf(x[2 * j], scale2, -ref));
-                        const float e1 = exp2_sfu(fmaf(x[2 * j + 1], scale2, -ref));
+                        const float e0 = exp2_sfu(fmaf(x[part][2 * j], scale2, -ref));
+                        const float e1 = exp2_sfu(fmaf(x[part][2 * j + 1], scale2, -ref));
                         sum += e0 + e1;
                         u[j] = pack2(e0, e1);
                     }
                     l += sum;
-                    tmem_st16(tx + 16 * k, u);
-                };
-                weigh(0, x0);
-                tmem_ld_wait32(x1);
-                tmem_ld32(tx + 64, x0);
-                weigh(1, x1);
-                tmem_ld_wait32(x0);
-                tmem_ld32(tx + 96, x1);
-                weigh(2, x0);
-                tmem_ld_wait32(x1);
-                weigh(3, x1);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&p_full[t]);
+                    tmem_st16(tx + 32 * half + 16 * part, u);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&p_full[t][part]);
+                }
             }
             const int64_t out = ((s.qa + row) * a.H + s.h);
-            const float inv = gave_up ? NAN : l == 0.0f ? 1.0f : 1.0f / l;
             if (steps > 0 && !gave_up) {
                 wait(&o_full[t], on & 1);
                 ++on;
                 tc_fence_after();
+                *mine = l;
+                gave_up = !named_bar_and(1 + t, 256, !dead);
+                l += *other;
             }
+            const float inv = gave_up ? NAN : l == 0.0f ? 1.0f : 1.0f / l;
             const bool add = odd[it & 1] != 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
                 float o[32];
                 if (steps > 0) {
                     tmem_ld32(to + 32 * k, o);
-                    tmem_ld_wait();
+                    tmem_ld_wait32(o);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0.0f;
@@ -462,7 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, add)) {
                     // values that were taken out of V because they are not finite
                     for (int key = s.masked * kTile; key < limit; ++key) {
-                        const __nv_bfloat16 *v = a.kv + (s.ka + key) * a.kv_stride + (int64_t)s.h * kKvRow + kNope + 32 * k;
+                        const __nv_bfloat16 *v =
+                            a.kv + (s.ka + key) * a.kv_stride + (int64_t)s.h * kKvRow + kNope + 64 * half + 32 * k;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const float w = __bfloat162float(v[j]);
@@ -478,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                    pack2(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
                                                    pack2(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
                                                    pack2(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
-                        *(uint4 *)(a.o + out * kHeadDim + 32 * k + 8 * j) = u;
+                        *(uint4 *)(a.o + out * kHeadDim + 64 * half + 32 * k + 8 * j) = u;
                     }
                 }
             }
-            if (real && a.lse)
+            if (real && a.lse && half == 0)
                 a.lse[out] = gave_up ? NAN : l == 0.0f ? -INFINITY : (m * scale2 + log2_sfu(l)) * kLn2;
             if (steps > 0) {
                 tc_fence_before();
@@ -499,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long t0 = clock64();
         while (clock64() - t0 < 100000000LL) __nanosleep(1000);
     }
-    if (wid == 9) tmem_dealloc(tmem, 512);
+    if (wid == 17) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
