@@ -64,9 +64,9 @@ constexpr int kPieces = 128;  // of the sequences, for finding the one that a bl
 constexpr uint32_t kTmemO = 256;  // X_t at 128 t, O_t at 256 + 128 t
 
 struct Item {
-    int n, h, q0, lq, off;  // sequence, head, first query in it, its queries, lk - lq
+    int h, q0, lq, off;     // head, first query in the sequence, its queries, lk - lq
     int lk, steps0, steps1; // keys, steps of each tile
-    int64_t qa, ka;         // the sequence's first query and key
+    int qa, ka;             // the sequence's first query and key
     int masked;             // first step with a key that some row does not see
     int valid;              // 0: no further item
     __device__ __forceinline__ int steps(int t) const { return t ? steps1 : steps0; }
@@ -173,11 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- scheduling and TMA
         if (elect_one()) {
             int it = 0, qn[2] = {0, 0};  // items published; queries' tiles loaded
-            uint32_t step = 0, checks = 0;  // steps loaded; those whose values are checked
-            int cta = blockIdx.x;
-            for (int asked = 0; cta >= 0; ++asked) {
-                mbar_arrive_expect_tx(&sh.next_full, 16);
-                next_cta_request(&sh.next_answer, &sh.next_full);
+            uint32_t step = 0, checks = 0, asked = 0;  // steps loaded; those whose values are checked
+            // the item of a CTA of the grid; false if there is none (the grid is an upper bound)
+            auto item_of_cta = [&](int cta, Item &s) {
                 const int rank = cta / a.H;
                 // the piece that holds block `rank`, then the sequence in it
                 int lo = 0, hi = kPieces;
@@ -192,70 +190,102 @@ __global__ void __launch_bounds__(kThreads, 1)
                     before += blocks;
                     blocks = 0;
                 }
-                if (blocks > 0) {
-                    wait(&item_empty[it & 1], ((it >> 1) & 1) ^ 1);
-                    Item &s = sh.items[it & 1];
-                    s.n = n;
-                    s.h = cta - rank * a.H;
-                    s.qa = a.cu_q[n];
-                    s.ka = a.cu_k[n];
-                    s.lq = a.cu_q[n + 1] - a.cu_q[n];
-                    s.lk = a.cu_k[n + 1] - a.cu_k[n];
-                    s.off = s.lk - s.lq;
-                    s.q0 = (blocks - 1 - (rank - before)) * kItem;
-                    int first = s.lk;  // keys that every row of the item sees
-                    for (int t = 0; t < 2; ++t) {
-                        const int r0 = s.q0 + t * kTile, r1 = min(r0 + kTile, s.lq);  // rows [r0, r1)
-                        const int seen = r1 <= r0 ? 0 : a.causal ? min(s.lk, r1 + s.off) : s.lk;
-                        (t ? s.steps1 : s.steps0) = seen > 0 ? (seen + kTile - 1) / kTile : 0;
-                        if (r1 > r0 && a.causal) first = min(first, max(r0 + 1 + s.off, 0));
-                    }
-                    s.masked = first / kTile;
-                    s.valid = 1;
-                    odd[it & 1] = 0;
-                    const Item cur = s;
-                    mbar_arrive(&item_full[it & 1]);
-                    ++it;
-                    for (int t = 0; t < 2; ++t) {
-                        if (cur.steps(t) == 0) continue;
-                        wait(&q_empty[t], (qn[t] & 1) ^ 1);
-                        ++qn[t];
-                        mbar_arrive_expect_tx(&q_full[t], 3 * kBlock);
-                        for (int b = 0; b < 3; ++b)
-                            tma_load_3d(sm + kSmQ + (t * 3 + b) * kBlock, &map_q, b * 64, cur.h,
-                                        (int)cur.qa + cur.q0 + t * kTile, &q_full[t]);
-                    }
-                    const int steps = cur.most();
-                    for (int i = 0; i < steps && !dead; ++i, ++step) {
-                        // ring blocks 5 step ..: K three, V two; block c takes the place of block c - 8, which
-                        // for K(step) are K(step - 2)'s last and V(step - 2)'s, for V(step) K(step - 1)'s first two
-                        const int row = (int)cur.ka + i * kTile;
-                        const uint32_t par = step & 1, before = ((step >> 1) & 1) ^ 1, c = 5 * step;
-                        auto block = [&](uint32_t b) { return sm + kSmRing + ((c + b) % kRing) * kBlock; };
-                        wait(&k_empty[par], before);
-                        mbar_arrive_expect_tx(&k_full[par], 3 * kBlock);
-                        tma_load_3d(block(0), &map_kv, 0, cur.h, row, &k_full[par]);
-                        wait(&v_empty[par], before);
-                        tma_load_3d(block(1), &map_kv, 64, cur.h, row, &k_full[par]);
-                        tma_load_2d(block(2), &map_r, 0, row, &k_full[par]);
-                        if (step > 0) wait(&k_empty[par ^ 1], ((step - 1) >> 1) & 1);
-                        if (i >= cur.masked) {  // to the checking warps, which signal v_full
-                            for (int g = 0; g < 2; ++g) {
-                                mbar_arrive_expect_tx(&unchecked[g][checks & 1], kBlock);
-                                tma_load_3d(block(3 + g), &map_kv, kNope + 64 * g, cur.h, row, &unchecked[g][checks & 1]);
-                            }
-                            ++checks;
-                        } else {
-                            mbar_arrive_expect_tx(&v_full[par], 2 * kBlock);
-                            tma_load_3d(block(3), &map_kv, kNope, cur.h, row, &v_full[par]);
-                            tma_load_3d(block(4), &map_kv, kNope + 64, cur.h, row, &v_full[par]);
-                            mbar_arrive(&v_full[par]);
+                if (blocks == 0) return false;
+                s.h = cta - rank * a.H;
+                s.qa = a.cu_q[n];
+                s.ka = a.cu_k[n];
+                s.lq = a.cu_q[n + 1] - s.qa;
+                s.lk = a.cu_k[n + 1] - s.ka;
+                s.off = s.lk - s.lq;
+                s.q0 = (blocks - 1 - (rank - before)) * kItem;
+                int first = s.lk;  // keys that every row of the item sees
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int r0 = s.q0 + t * kTile, r1 = min(r0 + kTile, s.lq);  // rows [r0, r1)
+                    const int seen = r1 <= r0 ? 0 : a.causal ? min(s.lk, r1 + s.off) : s.lk;
+                    (t ? s.steps1 : s.steps0) = seen > 0 ? (seen + kTile - 1) / kTile : 0;
+                    if (r1 > r0 && a.causal) first = min(first, max(r0 + 1 + s.off, 0));
+                }
+                s.masked = first / kTile;
+                s.valid = 1;
+                return true;
+            };
+            auto ask = [&] {
+                mbar_arrive_expect_tx(&sh.next_full, 16);
+                next_cta_request(&sh.next_answer, &sh.next_full);
+            };
+            // the next item that the answers name; false once there is none
+            auto next_item = [&](Item &s) {
+                for (;;) {
+                    wait(&sh.next_full, asked++ & 1);
+                    const int cta = dead ? -1 : next_cta_answer(&sh.next_answer);
+                    fence_async_smem();
+                    if (cta < 0) return false;
+                    if (item_of_cta(cta, s)) return true;
+                    ask();
+                }
+            };
+            Item cur, next;
+            bool more = item_of_cta(blockIdx.x, cur);
+            if (!more) {
+                ask();
+                more = next_item(cur);
+            }
+            while (more) {
+                wait(&item_empty[it & 1], ((it >> 1) & 1) ^ 1);
+                sh.items[it & 1] = cur;
+                odd[it & 1] = 0;
+                mbar_arrive(&item_full[it & 1]);
+                ++it;
+                ask();
+                auto queries = [&](int t) {
+                    if (cur.steps(t) == 0) return;
+                    wait(&q_empty[t], (qn[t]++ & 1) ^ 1);
+                    mbar_arrive_expect_tx(&q_full[t], 3 * kBlock);
+                    for (int b = 0; b < 3; ++b)
+                        tma_load_3d(sm + kSmQ + (t * 3 + b) * kBlock, &map_q, b * 64, cur.h,
+                                    cur.qa + cur.q0 + t * kTile, &q_full[t]);
+                };
+                queries(0);
+                const int steps = cur.most();
+                for (int i = 0; i < steps && !dead; ++i, ++step) {
+                    // ring blocks 5 step ..: K three, V two; block c takes the place of block c - 8, which
+                    // for K(step) are K(step - 2)'s last and V(step - 2)'s, for V(step) K(step - 1)'s first two
+                    const int row = cur.ka + i * kTile;
+                    const uint32_t par = step & 1, before = ((step >> 1) & 1) ^ 1, c = 5 * step;
+                    auto block = [&](uint32_t b) { return sm + kSmRing + ((c + b) % kRing) * kBlock; };
+                    wait(&k_empty[par], before);
+                    mbar_arrive_expect_tx(&k_full[par], 3 * kBlock);
+                    tma_load_3d(block(0), &map_kv, 0, cur.h, row, &k_full[par]);
+                    wait(&v_empty[par], before);
+                    tma_load_3d(block(1), &map_kv, 64, cur.h, row, &k_full[par]);
+                    tma_load_2d(block(2), &map_r, 0, row, &k_full[par]);
+                    if (i == 0) queries(1);
+                    if (step > 0) wait(&k_empty[par ^ 1], ((step - 1) >> 1) & 1);
+                    if (i >= cur.masked) {  // to the checking warps, which signal v_full
+                        for (int g = 0; g < 2; ++g) {
+                            mbar_arrive_expect_tx(&unchecked[g][checks & 1], kBlock);
+                            tma_load_3d(block(3 + g), &map_kv, kNope + 64 * g, cur.h, row, &unchecked[g][checks & 1]);
                         }
+                        ++checks;
+                    } else {
+                        mbar_arrive_expect_tx(&v_full[par], 2 * kBlock);
+                        tma_load_3d(block(3), &map_kv, kNope, cur.h, row, &v_full[par]);
+                        tma_load_3d(block(4), &map_kv, kNope + 64, cur.h, row, &v_full[par]);
+                        mbar_arrive(&v_full[par]);
+                    }
+                    if (i == 0) {
+                        // the queries of the item after this one, from DRAM into L2 while this one runs
+                        more = next_item(next);
+                        if (more)
+                            for (int b = 0; b < 6; ++b)
+                                if (next.steps(b / 3) > 0)
+                                    tma_prefetch_3d(&map_q, (b % 3) * 64, next.h, next.qa + next.q0 + (b / 3) * kTile);
                     }
                 }
-                wait(&sh.next_full, asked & 1);
-                cta = dead ? -1 : next_cta_answer(&sh.next_answer);
-                fence_async_smem();
+                if (steps == 0) more = next_item(next);
+                if (dead) break;
+                cur = next;
             }
             wait(&item_empty[it & 1], ((it >> 1) & 1) ^ 1);
             sh.items[it & 1].valid = 0;
@@ -362,24 +392,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t slot = (5 * step + 3 + g) % kRing;
                 wait(&unchecked[g][checks & 1], (checks >> 1) & 1);
                 const int rows = min(s.lk - i * kTile, kTile);  // keys of the sequence in this tile
-                uint8_t *blk = sm + kSmRing + slot * kBlock;
-                bool found = false;
+                uint4 *v = (uint4 *)(sm + kSmRing + slot * kBlock) + lane;  // rows lane / 8 + 4 j
+                for (int j = (rows - (lane >> 3) + 3) >> 2; j < kTile / 4; ++j) v[32 * j] = make_uint4(0, 0, 0, 0);
+                // an exponent of ones carries into the sign's place
+                uint32_t ones = 0;
 #pragma unroll 8
-                for (int j = 0; j < kTile * 8 / 32; ++j) {
-                    const int row = j * 4 + (lane >> 3);
-                    uint4 *v = (uint4 *)(blk + row * 128 + (lane & 7) * 16);
-                    if (row >= rows) {
-                        *v = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    const uint4 u = *v;
-                    const uint4 m = make_uint4(not_finite(u.x), not_finite(u.y), not_finite(u.z), not_finite(u.w));
-                    if (m.x | m.y | m.z | m.w) {
-                        found = true;
-                        *v = make_uint4(u.x & ~m.x, u.y & ~m.y, u.z & ~m.z, u.w & ~m.w);
+                for (int j = 0; j < kTile / 4; ++j) {
+                    const uint4 u = v[32 * j];
+                    ones |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                            ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
+                }
+                if (ones & 0x80008000u) {
+                    odd[it & 1] = 1;
+                    for (int j = 0; j < kTile / 4; ++j) {
+                        const uint4 u = v[32 * j];
+                        v[32 * j] = make_uint4(u.x & ~not_finite(u.x), u.y & ~not_finite(u.y), u.z & ~not_finite(u.z),
+                                               u.w & ~not_finite(u.w));
                     }
                 }
-                if (found) odd[it & 1] = 1;
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&v_full[step & 1]);
@@ -471,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&p_full[t][part]);
                 }
             }
-            const int64_t out = ((s.qa + row) * a.H + s.h);
+            const int64_t out = (int64_t)(s.qa + row) * a.H + s.h;
             if (steps > 0 && !gave_up) {
                 wait(&o_full[t], on & 1);
                 ++on;
@@ -482,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float inv = gave_up ? NAN : l == 0.0f ? 1.0f : 1.0f / l;
             const bool add = odd[it & 1] != 0;
+            uint32_t w[8][4];  // the thread's 64 values of its row, eight units of 16 bytes
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float o[32];
@@ -495,33 +526,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, add)) {
                     // values that were taken out of V because they are not finite
                     for (int key = s.masked * kTile; key < limit; ++key) {
-                        const __nv_bfloat16 *v =
-                            a.kv + (s.ka + key) * a.kv_stride + (int64_t)s.h * kKvRow + kNope + 64 * half + 32 * k;
+                        const __nv_bfloat16 *v = a.kv + (int64_t)(s.ka + key) * a.kv_stride +
+                                                 (int64_t)s.h * kKvRow + kNope + 64 * half + 32 * k;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            const float w = __bfloat162float(v[j]);
-                            if (!(fabsf(w) < INFINITY)) o[j] += w;
+                            const float u = __bfloat162float(v[j]);
+                            if (!(fabsf(u) < INFINITY)) o[j] += u;
                         }
                     }
                     __syncwarp();
                 }
-                if (real) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 u = make_uint4(pack2(o[8 * j] * inv, o[8 * j + 1] * inv),
-                                                   pack2(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
-                                                   pack2(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
-                                                   pack2(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
-                        *(uint4 *)(a.o + out * kHeadDim + 64 * half + 32 * k + 8 * j) = u;
-                    }
-                }
+                for (int j = 0; j < 16; ++j) w[4 * k + (j >> 2)][j & 3] = pack2(o[2 * j] * inv, o[2 * j + 1] * inv);
             }
-            if (real && a.lse && half == 0)
-                a.lse[out] = gave_up ? NAN : l == 0.0f ? -INFINITY : (m * scale2 + log2_sfu(l)) * kLn2;
             if (steps > 0) {
                 tc_fence_before();
                 mbar_arrive(&o_empty[t]);
             }
+            // Eight lanes exchange their units, so that a store writes whole 128-byte lines of four rows
+            // (16 bytes of 32 rows a store kept the load/store unit busy for 4000 clocks a tile pair).
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const bool up = lane & o;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (!(u & o))
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[u][j] : w[u | o][j], o);
+                            if (up) w[u][j] = got; else w[u | o][j] = got;
+                        }
+            }
+            {
+                const int first = s.q0 + t * kTile + quad * 32 + (lane & ~7);
+                __nv_bfloat16 *dst = a.o + ((int64_t)(s.qa + first) * a.H + s.h) * kHeadDim + 64 * half + 8 * (lane & 7);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (first + r < s.lq)
+                        *(uint4 *)(dst + (int64_t)r * a.H * kHeadDim) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
+            }
+            if (real && a.lse && half == 0)
+                a.lse[out] = gave_up ? NAN : l == 0.0f ? -INFINITY : (m * scale2 + log2_sfu(l)) * kLn2;
             __syncwarp();
             if (lane == 0) item_done(it);
             if (gave_up) break;
