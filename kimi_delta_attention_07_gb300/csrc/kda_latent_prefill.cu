@@ -356,9 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < steps && !dead; ++i, ++step) {
                     const uint32_t next = step + 1;
                     wait(&v_full[step & 1], (step >> 1) & 1);
-                    if (i + 1 < steps) wait(&k_full[next & 1], (next >> 1) & 1);
                     if (i < s0) {
                         values(t0, pn0++, i == 0);
+                        if (i + 1 < steps) wait(&k_full[next & 1], (next >> 1) & 1);
                         if (i + 1 < s0) scores(t0, next);
                         else mma_commit(&o_full[0]);
                         if (i + 2 == s0) mma_commit(&q_empty[0]);
@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i < s1) {
                         values(t1, pn1++, i == 0);
                         mma_commit(&v_empty[step & 1]);
+                        if (i + 1 < s1 && i >= s0) wait(&k_full[next & 1], (next >> 1) & 1);
                         if (i + 1 < s1) scores(t1, next);
                         else mma_commit(&o_full[1]);
                         if (i + 2 == s1) mma_commit(&q_empty[1]);
