@@ -13,16 +13,24 @@ import torch
 import kimi_delta_attention_07_gb300 as _core
 
 KDA_QUANT_NONE, KDA_QUANT_ROW, KDA_QUANT_BLOCK = range(3)
+KDA_BF16 = 1
 LATENT_DIM, ROPE_DIM, LATENT_ROW, NOPE_DIM, VALUE_DIM = 512, 64, 576, 128, 128
 _QUANT = {"none": KDA_QUANT_NONE, None: KDA_QUANT_NONE, "row": KDA_QUANT_ROW, "block": KDA_QUANT_BLOCK}
 _bf16, _f32, _i32, _u8, _e4m3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
                                  torch.float8_e4m3fn)
 _current_stream = torch._C._cuda_getCurrentRawStream
+_lib = None
+
+
+def _library():
+    global _lib
+    _lib = _core.load()
+    return _lib
 
 
 def _need(t, name, dtype, shape, dev):
-    """t is a contiguous CUDA tensor of this dtype and shape on device `dev`."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+    """The address of t: a contiguous CUDA tensor of this dtype and shape on device `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev >= 0:
         return t.data_ptr()
     _core._check(t, name, dtype, shape)
     raise ValueError(f"{name} must be on the same device as the other tensors")
@@ -31,47 +39,31 @@ def _need(t, name, dtype, shape, dev):
 def _rows(t, name, dtype, shape, dev):
     """The same for a tensor whose first stride is free (a slice of a wider
     projection); returns (address, elements between rows)."""
-    inner = 1
-    ok = t.dtype is dtype and t.shape == shape and t.get_device() == dev
-    if ok:
-        for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
-            ok = ok and (stride == inner or size == 1)
-            inner *= size
-    if not ok:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on the same device as the other tensors")
+    strides = t.stride()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0:
+        # below the first axis the strides are those of a contiguous tensor
+        inner = shape[-1] if len(shape) == 2 else shape[-1] * shape[-2]
+        if strides[-1] == 1 and (len(shape) == 2 or strides[1] == shape[2] or shape[1] == 1):
+            stride = strides[0] if shape[0] > 1 else inner
+            if stride >= inner and stride % 8 == 0:
+                return t.data_ptr(), stride
+            raise ValueError(f"{name}: its row stride must be a multiple of 8 of at least {inner}, got {stride}")
         raise ValueError(f"{name} must be contiguous but for its row stride")
-    stride = t.stride(0) if t.shape[0] > 1 else max(inner, 8)
-    if stride < inner or stride % 8:
-        raise ValueError(f"{name}: its row stride must be a multiple of 8 of at least {inner}, got {stride}")
-    return t.data_ptr(), stride
-
-
-def _device(t, name):
-    dev = t.get_device()
-    if dev < 0:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    raise ValueError(f"{name} must be on the same device as the other tensors")
 
 
-def _stream_of(stream, dev, *allocated):
-    if stream is None:
-        return _current_stream(dev)
+def _stream_of(stream, *allocated):
+    """A given stream's handle; what the call allocated is marked as in use there."""
     for t in allocated:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream
-
-
-def _done(status, what):
-    if status:
-        raise _core.KdaError(status, what)
 
 
 def kda_page_tables(ctx_lens, new_lens, free_pages, block_table, *, page_size, n_pages, max_tokens=None,
@@ -88,38 +80,40 @@ def kda_page_tables(ctx_lens, new_lens, free_pages, block_table, *, page_size, n
     [max_tokens], positions [max_tokens], status [2] = (position in free_pages
     after the step, requests refused)), all int32.
     """
-    dev = _device(ctx_lens, "ctx_lens")
+    dev = ctx_lens.get_device()
     n = ctx_lens.numel()
-    fresh = []
-
-    def out(t, name, shape):
-        if t is None:
-            t = torch.empty(shape, dtype=_i32, device=ctx_lens.device)
-            fresh.append(t)
-            return t
-        _need(t, name, _i32, shape, dev)
-        return t
-
     if slots is not None:
         max_tokens = slots.numel()
     elif max_tokens is None:
         raise ValueError("pass max_tokens, or slots and positions")
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [N, max_pages]")
-    pc = _need(ctx_lens, "ctx_lens", _i32, (n,), dev)
-    pn = _need(new_lens, "new_lens", _i32, (n,), dev)
-    pf = _need(free_pages, "free_pages", _i32, (free_pages.numel(),), dev)
-    pb = _need(block_table, "block_table", _i32, (n, block_table.shape[1]), dev)
+    max_pages, n_free = block_table.shape[1], free_pages.numel()
+    shape = (n,)
+    pc = _need(ctx_lens, "ctx_lens", _i32, shape, dev)
+    pn = _need(new_lens, "new_lens", _i32, shape, dev)
+    pf = _need(free_pages, "free_pages", _i32, (n_free,), dev)
+    pb = _need(block_table, "block_table", _i32, (n, max_pages), dev)
     ps = None if free_start is None else _need(free_start, "free_start", _i32, (1,), dev)
-    cu_seqlens = out(cu_seqlens, "cu_seqlens", (n + 1,))
-    seq_lens = out(seq_lens, "seq_lens", (n,))
-    slots = out(slots, "slots", (max_tokens,))
-    positions = out(positions, "positions", (max_tokens,))
-    status = out(status, "status", (2,))
-    _done(_core.load().kda_page_tables(
-        pc, pn, pf, free_pages.numel(), ps, pb, cu_seqlens.data_ptr(), seq_lens.data_ptr(),
-        slots.data_ptr(), positions.data_ptr(), status.data_ptr(), n, max_tokens,
-        block_table.shape[1], page_size, n_pages, _stream_of(stream, dev, *fresh)), "kda_page_tables")
+    new = []
+
+    def fresh(size):
+        new.append(torch.empty(size, dtype=_i32, device=ctx_lens.device))
+        return new[-1]
+
+    cu_seqlens = fresh(n + 1) if cu_seqlens is None else cu_seqlens
+    seq_lens = fresh(n) if seq_lens is None else seq_lens
+    slots = fresh(max_tokens) if slots is None else slots
+    positions = fresh(max_tokens) if positions is None else positions
+    status = fresh(2) if status is None else status
+    st = (_lib or _library()).kda_page_tables(
+        pc, pn, pf, n_free, ps, pb, _need(cu_seqlens, "cu_seqlens", _i32, (n + 1,), dev),
+        _need(seq_lens, "seq_lens", _i32, shape, dev), _need(slots, "slots", _i32, (max_tokens,), dev),
+        _need(positions, "positions", _i32, (max_tokens,), dev), _need(status, "status", _i32, (2,), dev), n,
+        max_tokens, max_pages, page_size, n_pages,
+        _current_stream(dev) if stream is None else _stream_of(stream, *new))
+    if st:
+        raise _core.KdaError(st, "kda_page_tables")
     return cu_seqlens, seq_lens, slots, positions, status
 
 
@@ -134,40 +128,37 @@ def kda_rms_norm(x, weight=None, *, residual=None, eps=1e-6, quant="none", resid
     (allocated unless given; may be residual or x).  Returns (y, residual_out
     or None, scales or None).
     """
-    dev = _device(x, "x")
+    dev = x.get_device()
     shape, dtype = x.shape, x.dtype
     D = shape[-1]
-    rows = x.numel() // D if D else 0
     q = _QUANT[quant]
-    fresh = []
     px = _need(x, "x", dtype, shape, dev)
-    dt = _core._dtype_code(x)
-    pr = None if residual is None else _need(residual, "residual", dtype, shape, dev)
+    new_r = new_y = new_s = None
+    if residual is None:
+        pr = None
+    else:
+        pr = _need(residual, "residual", dtype, shape, dev)
+        if residual_out is None:
+            residual_out = new_r = torch.empty_like(x)
+    po = None if residual_out is None else _need(residual_out, "residual_out", dtype, shape, dev)
     pw = None if weight is None else _need(weight, "weight", _f32, (D,), dev)
-    if residual_out is not None:
-        _need(residual_out, "residual_out", dtype, shape, dev)
-    elif residual is not None:
-        residual_out = torch.empty_like(x)
-        fresh.append(residual_out)
     ydt = _e4m3 if q else dtype
     if y is None:
-        y = torch.empty(shape, dtype=ydt, device=x.device)
-        fresh.append(y)
-    else:
-        _need(y, "y", ydt, shape, dev)
+        y = new_y = torch.empty(shape, dtype=ydt, device=x.device)
+    py = _need(y, "y", ydt, shape, dev)
     if q:
         groups = (*shape[:-1], 1 if q == KDA_QUANT_ROW else D // 128)
         if scales is None:
-            scales = torch.empty(groups, dtype=_f32, device=x.device)
-            fresh.append(scales)
-        else:
-            _need(scales, "scales", _f32, groups, dev)
+            scales = new_s = torch.empty(groups, dtype=_f32, device=x.device)
+        ps = _need(scales, "scales", _f32, groups, dev)
     else:
-        scales = None
-    _done(_core.load().kda_rms_norm(
-        px, pr, pw, y.data_ptr(), None if scales is None else scales.data_ptr(),
-        None if residual_out is None else residual_out.data_ptr(), eps, rows, D, q, dt,
-        _stream_of(stream, dev, *fresh)), "kda_rms_norm")
+        scales = ps = None
+    st = (_lib or _library()).kda_rms_norm(
+        px, pr, pw, py, ps, po, eps, x.numel() // D if D else 0, D, q,
+        KDA_BF16 if dtype is _bf16 else _core._dtype_code(x),
+        _current_stream(dev) if stream is None else _stream_of(stream, new_r, new_y, new_s))
+    if st:
+        raise _core.KdaError(st, "kda_rms_norm")
     return y, residual_out, scales
 
 
@@ -179,21 +170,25 @@ def kda_latent_cache_write(kv, weight, cache, slots, *, eps=1e-6, stream=None):
     page_size, 576] bf16, written in place; slots int32 [T] (others than cache
     rows, such as -1, are skipped).  Returns cache.
     """
-    dev = _device(kv, "kv")
+    dev = kv.get_device()
     T = kv.shape[0]
     pk, stride = _rows(kv, "kv", _bf16, (T, LATENT_ROW), dev)
-    if cache.dim() != 3 or cache.shape[2] != LATENT_ROW:
+    if cache.dim() != 3:
         raise ValueError(f"cache must be [n_pages, page_size, {LATENT_ROW}]")
-    pc = _need(cache, "cache", _bf16, cache.shape, dev)
+    n_pages, page_size, _ = cache.shape
+    pc = _need(cache, "cache", _bf16, (n_pages, page_size, LATENT_ROW), dev)
     pw = None if weight is None else _need(weight, "weight", _f32, (LATENT_DIM,), dev)
     ps = _need(slots, "slots", _i32, (T,), dev)
-    _done(_core.load().kda_latent_cache_write(pk, stride, pw, eps, pc, ps, T, cache.shape[0], cache.shape[1],
-                                              _stream_of(stream, dev)), "kda_latent_cache_write")
+    st = (_lib or _library()).kda_latent_cache_write(
+        pk, stride, pw, eps, pc, ps, T, n_pages, page_size,
+        _current_stream(dev) if stream is None else _stream_of(stream))
+    if st:
+        raise _core.KdaError(st, "kda_latent_cache_write")
     return cache
 
 
 def kda_latent_decode_workspace_bytes(n_seqs: int, S: int, H: int) -> int:
-    return int(_core.load().kda_latent_decode_workspace_bytes(n_seqs, S, H))
+    return int((_lib or _library()).kda_latent_decode_workspace_bytes(n_seqs, S, H))
 
 
 def kda_latent_decode(q, cache, block_table, seq_lens, *, scale=None, o=None, lse=None, workspace=None,
@@ -206,7 +201,7 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, scale=None, o=None, ls
     scale defaults to 192 ** -0.5 (the expanded query's width).  lse, if given,
     is fp32 [N, S, H] (or [N, H]).  Returns o, q's shape with 512 for 576.
     """
-    dev = _device(q, "q")
+    dev = q.get_device()
     shape = q.shape
     if len(shape) == 4:
         n, S, H, _ = shape
@@ -221,23 +216,23 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, scale=None, o=None, ls
     pc = _need(cache, "cache", _bf16, (n_pages, page_size, LATENT_ROW), dev)
     pb = _need(block_table, "block_table", _i32, (n, block_table.shape[1]), dev)
     pl = _need(seq_lens, "seq_lens", _i32, (n,), dev)
-    fresh = []
+    out = (*shape[:-1], LATENT_DIM)
+    new_o = new_w = None
     if o is None:
-        o = torch.empty((*shape[:-1], LATENT_DIM), dtype=_bf16, device=q.device)
-        fresh.append(o)
-    else:
-        _need(o, "o", _bf16, (*shape[:-1], LATENT_DIM), dev)
+        o = new_o = torch.empty(out, dtype=_bf16, device=q.device)
+    po = _need(o, "o", _bf16, out, dev)
     ple = None if lse is None else _need(lse, "lse", _f32, shape[:-1], dev)
-    lib = _core.load()
+    lib = _lib or _library()
     if workspace is None:
-        workspace = torch.empty(max(256, lib.kda_latent_decode_workspace_bytes(n, S, H)), dtype=_u8,
-                                device=q.device)
-        fresh.append(workspace)
-    pw = _need(workspace, "workspace", _u8, (workspace.numel(),), dev)
-    _done(lib.kda_latent_decode(
-        pq, pc, pb, pl, o.data_ptr(), ple, n, S, H, n_pages, page_size, block_table.shape[1],
-        192 ** -0.5 if scale is None else scale, pw, workspace.numel(), _stream_of(stream, dev, *fresh)),
-        "kda_latent_decode")
+        workspace = new_w = torch.empty(max(256, lib.kda_latent_decode_workspace_bytes(n, S, H)), dtype=_u8,
+                                        device=q.device)
+    ws = workspace.numel()
+    st = lib.kda_latent_decode(
+        pq, pc, pb, pl, po, ple, n, S, H, n_pages, page_size, block_table.shape[1],
+        192 ** -0.5 if scale is None else scale, _need(workspace, "workspace", _u8, (ws,), dev), ws,
+        _current_stream(dev) if stream is None else _stream_of(stream, new_o, new_w))
+    if st:
+        raise _core.KdaError(st, "kda_latent_decode")
     return o
 
 
@@ -251,7 +246,7 @@ def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal
     as q).  causal: query i of lq sees keys j <= i + lk - lq.  scale defaults to
     192 ** -0.5.  lse, if given, is fp32 [Tq, H].  Returns o [Tq, H, 128].
     """
-    dev = _device(q, "q")
+    dev = q.get_device()
     if q.dim() != 3 or kv.dim() != 3:
         raise ValueError("q must be [Tq, H, 192], kv [Tk, H, 256]")
     Tq, H, _ = q.shape
@@ -264,14 +259,15 @@ def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal
         raise ValueError("cu_seqlens_q must be int32 [N+1] with N >= 1")
     pcq = _need(cu_seqlens_q, "cu_seqlens_q", _i32, (n + 1,), dev)
     pck = None if cu_seqlens_k is None else _need(cu_seqlens_k, "cu_seqlens_k", _i32, (n + 1,), dev)
-    fresh = []
+    new_o = None
     if o is None:
-        o = torch.empty((Tq, H, VALUE_DIM), dtype=_bf16, device=q.device)
-        fresh.append(o)
-    else:
-        _need(o, "o", _bf16, (Tq, H, VALUE_DIM), dev)
+        o = new_o = torch.empty((Tq, H, VALUE_DIM), dtype=_bf16, device=q.device)
+    po = _need(o, "o", _bf16, (Tq, H, VALUE_DIM), dev)
     ple = None if lse is None else _need(lse, "lse", _f32, (Tq, H), dev)
-    _done(_core.load().kda_latent_prefill(
-        pq, sq, pk, sk, pr, sr, o.data_ptr(), ple, pcq, pck, n, Tq, Tk, H, 1 if causal else 0,
-        192 ** -0.5 if scale is None else scale, _stream_of(stream, dev, *fresh)), "kda_latent_prefill")
+    st = (_lib or _library()).kda_latent_prefill(
+        pq, sq, pk, sk, pr, sr, po, ple, pcq, pck, n, Tq, Tk, H, 1 if causal else 0,
+        192 ** -0.5 if scale is None else scale,
+        _current_stream(dev) if stream is None else _stream_of(stream, new_o))
+    if st:
+        raise _core.KdaError(st, "kda_latent_prefill")
     return o

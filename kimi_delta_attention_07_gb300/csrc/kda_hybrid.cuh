@@ -49,6 +49,7 @@ struct PageTablesArgs {
     int32_t *block_table, *cu_seqlens, *seq_lens, *slots, *positions, *status;
     int64_t n_free, max_tokens, n_pages;
     int n_seqs, max_pages, page_shift;
+    bool vector_stores;  // slots and positions are 16-byte aligned
 };
 cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t stream);
 

@@ -53,7 +53,8 @@ int kda_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, const int3
         if (!aligned(p, 4)) return KDA_ERR_INVALID_ARG;
     const PageTablesArgs a{ctx_lens, new_lens,  free_pages, free_start, block_table, cu_seqlens,
                            seq_lens, slots,     positions,  status,     n_free,      max_tokens,
-                           n_pages,  n_seqs,    max_pages,  shift};
+                           n_pages,  n_seqs,    max_pages,  shift,
+                           aligned(slots, 16) && aligned(positions, 16)};
     return launched([&] { return launch_page_tables(a, (cudaStream_t)stream); });
 }
 

@@ -19,7 +19,6 @@ __global__ void __launch_bounds__(kThreads) latent_cache_write_kernel(const Cach
     const int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (t >= a.n_tokens) return;
     const int64_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.n_rows) return;
     const __nv_bfloat16 *src = a.kv + t * a.kv_stride;
     __nv_bfloat16 *dst = a.cache + slot * kLatentRow;
     float c[2][8];
@@ -42,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) latent_cache_write_kernel(const Cach
 #pragma unroll
             for (int j = 0; j < 8; ++j) c[i][j] *= rn * w[i][j];
     }
+    if (slot < 0 || slot >= a.n_rows) return;
     store8(dst + 8 * lane, c[0]);
     store8(dst + 8 * lane + 256, c[1]);
     if (lane < kRope / 8) *reinterpret_cast<uint4 *>(dst + kLatent + 8 * lane) = key;

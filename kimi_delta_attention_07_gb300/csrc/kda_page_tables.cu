@@ -55,7 +55,8 @@ __device__ __forceinline__ int32_t clamp32(int64_t x) {
 __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageTablesArgs a) {
     extern __shared__ int32_t sh[];
     int32_t *cu = sh;                  // [N + 1] offsets of the packed new tokens
-    int32_t *first = sh + a.n_seqs + 1;  // [N] place of the first new page in free_pages, -1: refused
+    int32_t *first = cu + a.n_seqs + 1;  // [N] place of the first new page in free_pages, -1: refused
+    int32_t *ctx = first + a.n_seqs;     // [N] ctx_lens
     __shared__ int64_t part[2][kThreads / 32];
     __shared__ int32_t seen[2];  // {largest end of a request that fits, refused}
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -85,10 +86,10 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageTablesA
         const bool fits = d.fits && (need == 0 || ps + need <= a.n_free);
         cu[n] = clamp32(ts);
         first[n] = fits ? clamp32(ps) : -1;
+        ctx[n] = a.ctx_lens[n];
         if (writer) {
-            const int32_t ctx = a.ctx_lens[n];
             a.cu_seqlens[n] = clamp32(ts);
-            a.seq_lens[n] = fits ? ctx + a.new_lens[n] : max(ctx, 0);
+            a.seq_lens[n] = fits ? ctx[n] + a.new_lens[n] : max(ctx[n], 0);
             if (fits) {
                 if (need) atomicMax(&seen[0], (int32_t)(ps + need));
             } else {
@@ -115,37 +116,42 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageTablesA
             row[j] = a.free_pages[first[n] + (j - d.held)];
     }
 
-    // slots and positions: kTokensPerThread consecutive packed tokens a thread
-    const int32_t packed = cu[a.n_seqs];
+    // slots and positions: four consecutive packed tokens a thread, which mostly share a
+    // request and a page, stored as one vector each
+    const int32_t packed = cu[a.n_seqs], mask = (1 << a.page_shift) - 1;
     const int64_t step = (int64_t)gridDim.x * kThreads * kTokensPerThread;
     for (int64_t t0 = ((int64_t)blockIdx.x * kThreads + tid) * kTokensPerThread; t0 < a.max_tokens;
          t0 += step) {
         // the last request whose tokens begin at or before t0
-        int lo = 0, hi = a.n_seqs;
-        while (lo + 1 < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t0) lo = mid; else hi = mid;
+        int r = 0, hi = a.n_seqs;
+        while (r + 1 < hi) {
+            const int mid = (r + hi) >> 1;
+            if (cu[mid] <= t0) r = mid; else hi = mid;
         }
-        int r = lo;
-        for (int i = 0; i < kTokensPerThread && t0 + i < a.max_tokens; ++i) {
+        int32_t slot[kTokensPerThread], pos[kTokensPerThread];
+        int32_t page = -1, of = -1;  // page id of table entry `of` of request r
+#pragma unroll
+        for (int i = 0; i < kTokensPerThread; ++i) {
+            slot[i] = pos[i] = -1;
             const int64_t t = t0 + i;
-            int32_t slot = -1, pos = -1;
-            if (t < packed) {
-                while (cu[r + 1] <= t) ++r;
-                if (first[r] >= 0) {
-                    const int32_t ctx = a.ctx_lens[r], p = ctx + (int32_t)(t - cu[r]);
-                    const int32_t j = p >> a.page_shift;
-                    const int32_t held = (int32_t)(((int64_t)ctx + (1 << a.page_shift) - 1) >> a.page_shift);
-                    const int32_t page = j < held ? a.block_table[(int64_t)r * a.max_pages + j]
-                                                  : a.free_pages[first[r] + (j - held)];
-                    if (page >= 0 && page < a.n_pages) {
-                        slot = (page << a.page_shift) + (p & ((1 << a.page_shift) - 1));
-                        pos = p;
-                    }
-                }
+            if (t >= packed) continue;
+            while (cu[r + 1] <= t) ++r, of = -1;
+            if (first[r] < 0) continue;
+            const int32_t p = ctx[r] + (int32_t)(t - cu[r]), j = p >> a.page_shift;
+            if (j != of) {
+                const int32_t held = (int32_t)(((int64_t)ctx[r] + mask) >> a.page_shift);
+                page = j < held ? a.block_table[(int64_t)r * a.max_pages + j] : a.free_pages[first[r] + (j - held)];
+                of = j;
             }
-            a.slots[t] = slot;
-            a.positions[t] = pos;
+            if (page >= 0 && page < a.n_pages) slot[i] = (page << a.page_shift) + (p & mask), pos[i] = p;
+        }
+        if (a.vector_stores && t0 + kTokensPerThread <= a.max_tokens) {
+            *reinterpret_cast<int4 *>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTokensPerThread; ++i)
+                if (t0 + i < a.max_tokens) a.slots[t0 + i] = slot[i], a.positions[t0 + i] = pos[i];
         }
     }
 }
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(const PageTablesA
 }  // namespace
 
 cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t stream) {
-    const size_t smem = (2 * (size_t)a.n_seqs + 1) * sizeof(int32_t);
+    const size_t smem = (3 * (size_t)a.n_seqs + 1) * sizeof(int32_t);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -162,7 +168,7 @@ cudaError_t launch_page_tables(const PageTablesArgs &a, cudaStream_t stream) {
     const int64_t per_cta = kThreads * kTokensPerThread;
     const int64_t want = std::max<int64_t>((a.max_tokens + per_cta - 1) / per_cta,
                                            (a.n_seqs + kThreads / 32 - 1) / (kThreads / 32));
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, sm_count() * 4));
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, sm_count() * 8));
     const cudaError_t e = launch_dependent(page_tables_kernel, dim3(grid), dim3(kThreads), smem, stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
