@@ -16,6 +16,20 @@ __device__ __forceinline__ float exp2_sfu(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Nonzero if one of eight bf16 is infinite or NaN: an exponent of ones carries into the sign's place.
+__device__ __forceinline__ uint32_t exponent_of_ones(const uint4 &u) {
+    return (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+            ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
+           0x80008000u;
+}
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t two_bf16) {
+    return ((two_bf16 & 0x7f80u) == 0x7f80u ? 0u : two_bf16 & 0xffffu) |
+           ((two_bf16 & 0x7f800000u) == 0x7f800000u ? 0u : two_bf16 & 0xffff0000u);
+}
+__device__ __forceinline__ uint4 finite_or_zero(const uint4 &u) {
+    return make_uint4(finite_or_zero(u.x), finite_or_zero(u.y), finite_or_zero(u.z), finite_or_zero(u.w));
+}
+
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));

@@ -57,24 +57,31 @@ namespace {
 constexpr int kCopy = 16;   // tokens per copy
 constexpr int kCopies = 3;  // copies per tile
 constexpr int kTile = kCopies * kCopy;
-constexpr int kSlots = 3;   // tiles in the ring
-constexpr int kRows = 32;   // query rows per CTA
 constexpr int kThreads = 224;
 constexpr uint32_t kGroup = 9 * 1024;        // 8 tokens
 constexpr uint32_t kCopyBytes = 2 * kGroup;
 constexpr uint32_t kTileBytes = kCopies * kCopyBytes;
 constexpr float kRaise = 8.0f;  // log2 by which a score may pass its row's reference
 
-// shared memory (from a 1024-byte boundary); the ring comes first, so that the
-// 16 rows which a first product reads past its tile are inside
-constexpr uint32_t kSmTile = 0;
-constexpr uint32_t kSmQ = kSlots * kTileBytes;     // [9][32 rows][128 B]
-constexpr uint32_t kSmP = kSmQ + 9 * kRows * 128;  // 2 x [64 tokens][64 B]
-constexpr uint32_t kSmemBytes = kSmP + 2 * 64 * 64 + 1024;  // + alignment of the base
-static_assert(9 * kRows * 128 >= (8 - 2 * kCopies) * kGroup, "rows past the last tile");
-
-constexpr uint32_t kTmemCols = 256;  // O^T: 4 x 32 columns, X^T: 2 x 32
-constexpr uint32_t kTmemX = 128;
+// What depends on the query rows per CTA, 32 or 64.
+template <int ROWS>
+struct Cfg {
+    static constexpr int kSlots = ROWS == 32 ? 3 : 2;  // tiles in the ring
+    // shared memory (from a 1024-byte boundary); the ring comes first, so that the
+    // 16 rows which a first product reads past its tile are inside
+    static constexpr uint32_t kPBytes = 64 * ROWS * 2;              // [64 tokens][ROWS]
+    static constexpr uint32_t kSmQ = kSlots * kTileBytes;           // [9][ROWS][128 B]
+    static constexpr uint32_t kSmP = kSmQ + 9 * ROWS * 128;         // two P
+    static constexpr uint32_t kSmemBytes = kSmP + 2 * kPBytes + 1024;  // + alignment of the base
+    static_assert(9 * ROWS * 128 >= 2 * kGroup, "rows past the last tile");
+    static constexpr uint32_t kTmemX = 4 * ROWS;  // O^T: 4 x ROWS columns, then X^T: 2 x ROWS
+    static constexpr uint32_t kTmemCols = 8 * ROWS;
+    // P as B operand, MN-major: rows of 64 bytes (64-byte swizzle) or 128 bytes (128-byte swizzle)
+    static constexpr uint64_t kPDesc = ((uint64_t)(ROWS == 32 ? kDescHiSw64 : kDescHi) << 32);
+    static __device__ __forceinline__ uint32_t p_off(int token, int row) {
+        return ROWS == 32 ? sw64_off(token, row) : sw128_off(token, row, 64);
+    }
+};
 
 // Operand descriptors of a tile (128-byte swizzle, 8-token groups kGroup apart):
 // K-major for block b (64 columns) and step k of 16 columns; MN-major for
@@ -87,8 +94,9 @@ __device__ __forceinline__ uint64_t tile_desc_mn(uint32_t tile, int b, int k) {
     return ((uint64_t)kTileDescHi << 32) | (((tile & 0x3FFFFu) >> 4) + b * 128 + k * (kCopyBytes >> 4)) | (64u << 16);
 }
 
+template <int ROWS>
 struct Part {  // of a request that crosses ranges
-    float o[kRows][kLatent];
+    float o[ROWS][kLatent];
 };
 struct Stat {  // and its rows' reference and sum
     float m, l;
@@ -111,9 +119,9 @@ struct Cut {
 struct Grid {
     int row_blocks, ranges;
 };
-inline Grid decode_grid(int S, int H) {
+inline Grid decode_grid(int S, int H, int rows) {
     Grid g;
-    g.row_blocks = (S * H + kRows - 1) / kRows;
+    g.row_blocks = (S * H + rows - 1) / rows;
     g.ranges = std::max(1, sm_count() / g.row_blocks);
     return g;
 }
@@ -121,7 +129,7 @@ inline Grid decode_grid(int S, int H) {
 struct DecodeParams {
     LatentDecodeArgs a;
     int row_blocks, ranges;
-    Part *parts;  // [range][row block][2]: begun before the range / begun in it
+    void *parts;  // Part [range][row block][2]: begun before the range / begun in it
     Stat *stats;  // [row][2][range]: what a joining warp reads lies together
     Join *joins;  // [ranges]: a request is joined by entry n if there are no more requests than ranges, else
                   // by the entry of the range that it begins in (at most one leaves a range)
@@ -163,15 +171,20 @@ struct Walk {
     }
 };
 
+template <int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_c, const DecodeParams p) {
+    using C = Cfg<kRows>;
+    constexpr int kSlots = C::kSlots, kCols = kRows / 4;  // score columns of a softmax thread
+    constexpr uint32_t kSmTile = 0, kSmQ = C::kSmQ, kSmP = C::kSmP, kTmemX = C::kTmemX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     __shared__ uint64_t full[kSlots], empty[kSlots][kCopies], full_q, empty_q, x_full[2], p_full[2], pv_done[2], o_empty;
     __shared__ uint32_t tmem_base;
     __shared__ int piece[kThreads / 32], start_n, start_off, start_len;
     __shared__ float sh_col[4][kRows], sh_row[kRows];
+    __shared__ __align__(16) float sh_inv[kRows];
     __shared__ volatile int dead, lost;
 
     const LatentDecodeArgs &a = p.a;
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         dead = lost = 0;
     }
-    if (wid == 5) tmem_alloc(&tmem_base, kTmemCols);
+    if (wid == 5) tmem_alloc(&tmem_base, C::kTmemCols);
     // (the join is not let in early: its CTAs would settle on the SMs that finish
     // first and run there one after the other)
     griddep_wait();
@@ -325,13 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(&p_full[t & 1], (t >> 1) & 1);
                     if (i == 0 && seg > 0) wait(&o_empty, (seg - 1) & 1);
                     tc_fence_after();
-                    const uint32_t tile = tile_0 + slot * kTileBytes, pt = p0 + (t & 1) * 64 * 64;
+                    const uint32_t tile = tile_0 + slot * kTileBytes, pt = p0 + (t & 1) * C::kPBytes;
 #pragma unroll
                     for (int k = 0; k < kCopies; ++k) {
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
                             mma_bf16(tmem + b * kRows, tile_desc_mn(tile, b, k),
-                                     ((uint64_t)kDescHiSw64 << 32) | (((pt & 0x3FFFFu) >> 4) + k * 64), idesc,
+                                     C::kPDesc | (((pt & 0x3FFFFu) >> 4) + k * (16 * kRows * 2 >> 4)), idesc,
                                      i > 0 || k > 0);
                         mma_commit(&empty[slot][k]);
                     }
@@ -342,22 +355,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- softmax: a thread holds 16 scores, tokens 16 w + lane / 4 (+ 8) of the tile by
+        // ---- softmax: a thread holds scores of tokens 16 w + lane / 4 (+ 8) of the tile by
         // rows 8 j + 2 (lane % 4) + {0, 1}; warp 3 has no tokens (its scores are hidden)
         const Walk again = walk;
         const uint32_t lanes = (uint32_t)(wid * 32) << 16;
         const float scale2 = a.scale * kLog2e;
         const int rows = min(kRows, a.S * a.H - rb * kRows);
         const int tok = 16 * wid + (lane >> 2), col = 2 * (lane & 3);
-        int limit[8];  // of the thread's rows: new token r / H sees positions below len - S + 1 + r / H
+        int limit[kCols];  // of the thread's rows: new token r / H sees positions below len - S + 1 + r / H
 #pragma unroll
-        for (int c = 0; c < 8; ++c) limit[c] = (rb * kRows + 8 * (c >> 1) + col + (c & 1)) / a.H - a.S + 1;
+        for (int c = 0; c < kCols; ++c) limit[c] = (rb * kRows + 8 * (c >> 1) + col + (c & 1)) / a.H - a.S + 1;
         int at = range_begin, slot = 0, t = 0;
         bool gave_up = false;  // the same in all four warps: decided by their votes
         while (!gave_up && walk.next(s)) {
-            float m[8], l[8];
+            float m[kCols], l[kCols];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) m[c] = -INFINITY, l[c] = 0.0f;
+            for (int c = 0; c < kCols; ++c) m[c] = -INFINITY, l[c] = 0.0f;
             bool bad = !s.ok;
             for (int i = 0; i < s.tiles; ++i, ++t) {
                 const int64_t pos0 = (int64_t)(s.tile0 + i) * kTile;
@@ -368,31 +381,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 wait(&x_full[t & 1], (t >> 1) & 1);
                 tc_fence_after();
-                float x[16];
-                tmem_ld_16x32(tmem + kTmemX + (t & 1) * kRows + lanes, x);
+                float x[2 * kCols];
+#pragma unroll
+                for (int k = 0; k < kRows / 32; ++k)
+                    tmem_ld_16x32(tmem + kTmemX + (t & 1) * kRows + 32 * k + lanes,
+                                  *reinterpret_cast<float(*)[16]>(x + 16 * k));
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] *= scale2;
+                for (int j = 0; j < 2 * kCols; ++j) x[j] *= scale2;
                 if (pos0 + kTile > s.len - a.S + 1 || wid >= kCopies) {
                     // the last tiles: what a row does not see, and rows of the tile that hold no token
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 2 * kCols; ++j) {
                         const int64_t pos = pos0 + tok + ((j >> 1) & 1) * 8;
                         if (wid >= kCopies || pos >= (int64_t)s.len + limit[(j >> 2) * 2 + (j & 1)]) x[j] = -INFINITY;
                     }
-                    if (tid < 2 * kTile && pos0 + (tid >> 1) >= s.len) {
-                        // shared memory may hold anything there, and 0 times that has to be 0
-                        uint8_t *r = sm + kSmTile + slot * kTileBytes + (tid >> 4) * kGroup + ((tid >> 1) & 7) * 128 +
-                                     (tid & 1) * 4096;
-                        for (int b = 0; b < 4; ++b)
+                    if (tid < 2 * kTile && pos0 + (tid >> 1) >= s.len - a.S + 1) {
+                        // A place that some row does not see gets p = 0 there, and 0 times its values has to be 0:
+                        // rows without a token (shared memory may hold anything) become 0, and so do values of
+                        // a new token that are not finite (rows that see it are NaN by their scores).
+                        const bool none = pos0 + (tid >> 1) >= s.len;
+                        uint4 *r = (uint4 *)(sm + kSmTile + slot * kTileBytes + (tid >> 4) * kGroup +
+                                             ((tid >> 1) & 7) * 128 + (tid & 1) * 4096);
+                        for (int b = 0; b < 4; ++b, r += 64) {
+                            if (none) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) *(uint4 *)(r + b * 1024 + j * 16) = make_uint4(0, 0, 0, 0);
+                                for (int j = 0; j < 8; ++j) r[j] = make_uint4(0, 0, 0, 0);
+                            } else {
+                                uint32_t ones = 0;
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) ones |= exponent_of_ones(r[j]);
+                                for (int j = 0; ones && j < 8; ++j) r[j] = finite_or_zero(r[j]);
+                            }
+                        }
                     }
                 }
                 if (++slot == kSlots) slot = 0;
                 float over = -INFINITY;  // fmaxf skips the NaN of -inf - -inf
 #pragma unroll
-                for (int j = 0; j < 16; ++j) over = fmaxf(over, x[j] - m[(j >> 2) * 2 + (j & 1)]);
+                for (int j = 0; j < 2 * kCols; ++j) over = fmaxf(over, x[j] - m[(j >> 2) * 2 + (j & 1)]);
                 const bool given = dead;
                 if (given) lost = 1;
                 if (!named_bar_and(1, 128, !(over > kRaise) && !given)) {
@@ -402,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // raise every row's reference to its maximum so far
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < kCols; ++c) {
                         const int j = (c >> 1) * 4 + (c & 1);
                         float top = fmaxf(x[j], x[j + 2]);
 #pragma unroll
@@ -411,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     named_bar_sync(1, 128);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < kCols; ++c) {
                         const int r = 8 * (c >> 1) + col + (c & 1);
                         const float top = fmaxf(fmaxf(fmaxf(sh_col[0][r], sh_col[1][r]), fmaxf(sh_col[2][r], sh_col[3][r])), m[c]);
                         const float f = top == -INFINITY ? 1.0f : exp2_sfu(m[c] - top);
@@ -423,13 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
                         tc_fence_after();
                         named_bar_sync(1, 128);
-                        for (int k = 0; k < 4; ++k) {
-                            float o[kRows];
+                        for (int k = 0; k < 4 * kRows / 32; ++k) {
+                            float o[32];
                             tmem_ld32(tmem + k * 32 + lanes, o);
                             tmem_ld_wait();
-                            uint32_t u[kRows];
+                            uint32_t u[32];
 #pragma unroll
-                            for (int c = 0; c < kRows; ++c) u[c] = __float_as_uint(o[c] * sh_row[c]);
+                            for (int c = 0; c < 32; ++c)
+                                u[c] = __float_as_uint(o[c] * sh_row[(32 * k) % kRows + c]);
                             tmem_st32(tmem + k * 32 + lanes, u);
                         }
                         tmem_st_wait();
@@ -437,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     named_bar_sync(1, 128);  // sh_col and sh_row are read before they are written again
                 }
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < kCols; ++c) {
                     const int j = (c >> 1) * 4 + (c & 1);
                     const float ref = m[c] == -INFINITY ? 0.0f : m[c];
                     x[j] = exp2_sfu(x[j] - ref);
@@ -446,11 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // this buffer's p was read by the second product of two tiles ago
                 if (t >= 2) wait(&pv_done[t & 1], ((t >> 1) & 1) ^ 1);
-                uint8_t *ps = sm + kSmP + (t & 1) * 64 * 64;
+                uint8_t *ps = sm + kSmP + (t & 1) * C::kPBytes;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    *(uint32_t *)(ps + sw64_off(tok, 8 * j + col)) = pack2(x[4 * j], x[4 * j + 1]);
-                    *(uint32_t *)(ps + sw64_off(tok + 8, 8 * j + col)) = pack2(x[4 * j + 2], x[4 * j + 3]);
+                for (int j = 0; j < kRows / 8; ++j) {
+                    *(uint32_t *)(ps + C::p_off(tok, 8 * j + col)) = pack2(x[4 * j], x[4 * j + 1]);
+                    *(uint32_t *)(ps + C::p_off(tok + 8, 8 * j + col)) = pack2(x[4 * j + 2], x[4 * j + 3]);
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -459,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (gave_up) break;
             // ---- the request's part of this range is done
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < kCols; ++c) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
                 if (lane < 4) {
@@ -468,19 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (wid == 0) sh_row[r] = m[c];
                 }
             }
+            // (what follows the vote is done while the last second product runs)
             const bool fine = named_bar_and(1, 128, !bad);
-            wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
-            tc_fence_after();
             const int64_t row0 = (int64_t)s.n * a.S * a.H + rb * kRows;
-            Part *part = p.parts + ((int64_t)range * p.row_blocks + rb) * 2 + (s.tile0 == 0 ? 1 : 0);
-            Stat *stat = p.stats + ((int64_t)2 * rb * kRows + (s.tile0 == 0 ? 1 : 0)) * p.ranges + range;  // row 0's
-            auto sum = [&](int c) {
-                const float l = (sh_col[0][c] + sh_col[1][c]) + (sh_col[2][c] + sh_col[3][c]);
-                return fine ? l : NAN;
-            };
             if (tid < rows) {
-                const float mt = sh_row[tid], lt = sum(tid);
-                if (!s.whole()) stat[2 * p.ranges * tid] = {mt, lt};
+                float lt = (sh_col[0][tid] + sh_col[1][tid]) + (sh_col[2][tid] + sh_col[3][tid]);
+                if (!fine) lt = NAN;
+                const float mt = sh_row[tid];
+                // what the row's sums are divided by; a row that saw nothing has zeros
+                sh_inv[tid] = lt == 0.0f ? 1.0f : 1.0f / lt;
+                if (!s.whole()) p.stats[(2 * (rb * kRows + tid) + (s.tile0 == 0 ? 1 : 0)) * p.ranges + range] = {mt, lt};
                 else if (a.lse) a.lse[row0 + tid] = lt == 0.0f ? -INFINITY : (mt + log2_sfu(lt)) * kLn2;
             }
             if (tid == 0 && rb == 0 && s.tile0 == 0) {
@@ -490,27 +515,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (by_request) p.joins[s.n] = j;
                 else if (!s.whole()) p.joins[range] = j;
             }
-            if (s.whole()) {
-                float inv[kRows];
+            Part<kRows> *part = (Part<kRows> *)p.parts + ((int64_t)range * p.row_blocks + rb) * 2 + (s.tile0 == 0 ? 1 : 0);
+            wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
+            tc_fence_after();
+            named_bar_sync(1, 128);
+            // O^T columns 32 k .. are rows c0 .. of 128 values; a row half at a time, so that its divisors stay
+            // in registers and the loop is short (a long one misses the instruction cache: it runs rarely)
+            for (int c0 = 0; c0 < kRows; c0 += 32) {
+                float inv[32];
 #pragma unroll
-                for (int c = 0; c < kRows; ++c) inv[c] = sum(c), inv[c] = inv[c] == 0.0f ? 1.0f : 1.0f / inv[c];
-                for (int k = 0; k < 4; ++k) {
-                    float o[kRows];
-                    tmem_ld32(tmem + k * 32 + lanes, o);
-                    tmem_ld_wait();
-                    __nv_bfloat16 *dst = a.o + row0 * kLatent + k * 128 + tid;
+                for (int c = 0; c < 32; c += 4) *(float4 *)(inv + c) = *(const float4 *)(sh_inv + c0 + c);
+                if (s.whole()) {
+#pragma unroll 4
+                    for (int k = 0; k < 4; ++k) {
+                        float o[32];
+                        tmem_ld32(tmem + k * kRows + c0 + lanes, o);
+                        tmem_ld_wait32(o);
+                        __nv_bfloat16 *dst = a.o + (row0 + c0) * kLatent + k * 128 + tid;
 #pragma unroll
-                    for (int c = 0; c < kRows; ++c)
-                        if (c < rows) dst[c * kLatent] = __float2bfloat16_rn(o[c] * inv[c]);
-                }
-            } else {
-                for (int k = 0; k < 4; ++k) {
-                    float o[kRows];
-                    tmem_ld32(tmem + k * 32 + lanes, o);
-                    tmem_ld_wait();
+                        for (int c = 0; c < 32; ++c)
+                            if (c0 + c < rows) dst[c * kLatent] = __float2bfloat16_rn(o[c] * inv[c]);
+                    }
+                } else {
+#pragma unroll 4
+                    for (int k = 0; k < 4; ++k) {
+                        float o[32];
+                        tmem_ld32(tmem + k * kRows + c0 + lanes, o);
+                        tmem_ld_wait32(o);
+                        float *dst = &part->o[c0][k * 128 + tid];
 #pragma unroll
-                    for (int c = 0; c < kRows; ++c)
-                        if (c < rows) part->o[c][k * 128 + tid] = o[c];
+                        for (int c = 0; c < 32; ++c)
+                            if (c0 + c < rows) dst[c * kLatent] = o[c];
+                    }
                 }
             }
             tc_fence_before();
@@ -542,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long t0 = clock64();
         while (clock64() - t0 < 100000000LL) __nanosleep(1000);
     }
-    if (wid == 5) tmem_dealloc(tmem, kTmemCols);
+    if (wid == 5) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 // Joins the parts of a request that crosses ranges.  With many rows a warp takes
@@ -550,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // CTA takes a quarter of a row's 512 values, each of its eight warps every
 // eighth part, and their sums are added in order.
 constexpr int kJoinThreads = 256;
-template <bool MANY>
+template <int kRows, bool MANY>
 __global__ void __launch_bounds__(kJoinThreads) latent_decode_join_kernel(const DecodeParams p) {
     extern __shared__ float weights[];  // [8 warps][ranges]
     constexpr int kVec = MANY ? 1 : 4, kStep = MANY ? 8 : 1, kBatch = MANY ? 10 : 4;
@@ -566,7 +602,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_decode_join_kernel(const 
     const int d0 = (MANY ? blockIdx.z * 128 : 0) + 4 * lane;
     const int rb = row / kRows, c = row % kRows, parts = j.last - j.first + 1;
     auto part = [&](int i) {  // the first range began the request
-        return p.parts + ((int64_t)(j.first + i) * p.row_blocks + rb) * 2 + (i == 0 ? 1 : 0);
+        return (const Part<kRows> *)p.parts + ((int64_t)(j.first + i) * p.row_blocks + rb) * 2 + (i == 0 ? 1 : 0);
     };
     // values are requested in batches, the first one before the weights that it waits for
     float4 v[kBatch][kVec];
@@ -654,43 +690,57 @@ inline bool encode_cache(CUtensorMap *m, const void *base, int64_t rows) {
 }
 
 inline size_t joins_bytes(const Grid &g) { return align_up((size_t)g.ranges * sizeof(Join), 256); }
-inline size_t stats_bytes(const Grid &g) {
-    return align_up((size_t)g.ranges * g.row_blocks * kRows * 2 * sizeof(Stat), 256);
+template <int ROWS>
+size_t stats_bytes(const Grid &g) {
+    return align_up((size_t)g.ranges * g.row_blocks * ROWS * 2 * sizeof(Stat), 256);
+}
+template <int ROWS>
+size_t workspace_bytes(int S, int H) {
+    const Grid g = decode_grid(S, H, ROWS);
+    return joins_bytes(g) + stats_bytes<ROWS>(g) + (size_t)g.ranges * g.row_blocks * 2 * sizeof(Part<ROWS>);
+}
+
+template <int ROWS>
+cudaError_t launch(const LatentDecodeArgs &a, cudaStream_t stream) {
+    const Grid g = decode_grid(a.S, a.H, ROWS);
+    DecodeParams p{a, g.row_blocks, g.ranges};
+    uint8_t *ws = (uint8_t *)a.workspace;
+    p.joins = (Join *)ws;
+    p.stats = (Stat *)(ws + joins_bytes(g));
+    p.parts = ws + joins_bytes(g) + stats_bytes<ROWS>(g);
+    CUtensorMap map_q, map_c;
+    if (!encode_rows64(&map_q, a.q, kLatentRow, (int64_t)a.n_seqs * a.S * a.H, kLatentRow, ROWS) ||
+        !encode_cache(&map_c, a.cache, a.n_pages << a.page_shift))
+        return cudaErrorUnknown;
+    cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Cfg<ROWS>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(latent_decode_kernel<ROWS>, dim3(g.ranges * g.row_blocks), dim3(kThreads),
+                         Cfg<ROWS>::kSmemBytes, stream, map_q, map_c, p);
+    if (e != cudaSuccess) return e;
+    const size_t weights = (size_t)8 * g.ranges * sizeof(float);
+    const int joins = std::min(a.n_seqs, g.ranges), rows = a.S * a.H;
+    if (joins * rows <= 128)
+        e = launch_dependent(latent_decode_join_kernel<ROWS, true>, dim3(joins, rows, 4), dim3(kJoinThreads), weights,
+                             stream, p);
+    else
+        e = launch_dependent(latent_decode_join_kernel<ROWS, false>, dim3(joins, (rows + 7) / 8), dim3(kJoinThreads),
+                             weights, stream, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 size_t latent_decode_workspace_bytes(int n_seqs, int S, int H) {
-    const Grid g = decode_grid(S, H);
-    return joins_bytes(g) + stats_bytes(g) + (size_t)g.ranges * g.row_blocks * 2 * sizeof(Part);
+    return std::max(workspace_bytes<32>(S, H), workspace_bytes<64>(S, H));
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
-    const Grid g = decode_grid(a.S, a.H);
-    DecodeParams p{a, g.row_blocks, g.ranges};
-    uint8_t *ws = (uint8_t *)a.workspace;
-    p.joins = (Join *)ws;
-    p.stats = (Stat *)(ws + joins_bytes(g));
-    p.parts = (Part *)(ws + joins_bytes(g) + stats_bytes(g));
-    CUtensorMap map_q, map_c;
-    if (!encode_rows64(&map_q, a.q, kLatentRow, (int64_t)a.n_seqs * a.S * a.H, kLatentRow, kRows) ||
-        !encode_cache(&map_c, a.cache, a.n_pages << a.page_shift))
-        return cudaErrorUnknown;
-    cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemBytes);
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(latent_decode_kernel, dim3(g.ranges * g.row_blocks), dim3(kThreads), kSmemBytes,
-                         stream, map_q, map_c, p);
-    if (e != cudaSuccess) return e;
-    const size_t weights = (size_t)8 * g.ranges * sizeof(float);
-    const int joins = std::min(a.n_seqs, g.ranges), rows = a.S * a.H;
-    if (joins * rows <= 128)
-        e = launch_dependent(latent_decode_join_kernel<true>, dim3(joins, rows, 4), dim3(kJoinThreads), weights, stream,
-                             p);
-    else
-        e = launch_dependent(latent_decode_join_kernel<false>, dim3(joins, (rows + 7) / 8), dim3(kJoinThreads), weights,
-                             stream, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    // 64 query rows a CTA read the cache half as often (64 requests of 2304 tokens, 128 rows each: 96 us
+    // against 108 us), but take longer over a single tile (4 requests of up to 700 tokens, 128 rows each:
+    // 16.6 us against 14.5 us), which is all there is when the block table holds few tokens.
+    const int64_t most = ((int64_t)a.n_seqs * a.max_pages) << a.page_shift;
+    return a.S * a.H > 32 && most > 16384 ? launch<64>(a, stream) : launch<32>(a, stream);
 }
 
 }  // namespace kda

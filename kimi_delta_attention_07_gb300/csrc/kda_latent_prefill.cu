@@ -97,11 +97,6 @@ __device__ __forceinline__ int blocks_of(const LatentPrefillArgs &a, int n) {
     return ok ? (qb - qa + kItem - 1) / kItem : 0;
 }
 
-__device__ __forceinline__ uint32_t not_finite(uint32_t two_bf16) {
-    return ((two_bf16 & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
-           ((two_bf16 & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
-}
-
 // POSITIVE: scale > 0, so that the largest product is the largest score
 template <bool POSITIVE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -134,6 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dead = 0;
     }
     if (wid == 17) tmem_alloc(&sh.tmem_base, 512);
+    griddep_wait();
+    griddep_launch_dependents();
     // the blocks of 256 queries of the sequences before each thread's piece
     const int per = (a.n_seqs + kPieces - 1) / kPieces;
     int upto = 0, own = 0;
@@ -395,21 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rows = min(s.lk - i * kTile, kTile);  // keys of the sequence in this tile
                 uint4 *v = (uint4 *)(sm + kSmRing + slot * kBlock) + lane;  // rows lane / 8 + 4 j
                 for (int j = (rows - (lane >> 3) + 3) >> 2; j < kTile / 4; ++j) v[32 * j] = make_uint4(0, 0, 0, 0);
-                // an exponent of ones carries into the sign's place
                 uint32_t ones = 0;
 #pragma unroll 8
-                for (int j = 0; j < kTile / 4; ++j) {
-                    const uint4 u = v[32 * j];
-                    ones |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
-                            ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
-                }
-                if (ones & 0x80008000u) {
+                for (int j = 0; j < kTile / 4; ++j) ones |= exponent_of_ones(v[32 * j]);
+                if (ones) {
                     odd[it & 1] = 1;
-                    for (int j = 0; j < kTile / 4; ++j) {
-                        const uint4 u = v[32 * j];
-                        v[32 * j] = make_uint4(u.x & ~not_finite(u.x), u.y & ~not_finite(u.y), u.z & ~not_finite(u.z),
-                                               u.w & ~not_finite(u.w));
-                    }
+                    for (int j = 0; j < kTile / 4; ++j) v[32 * j] = finite_or_zero(v[32 * j]);
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -601,8 +589,9 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t strea
     // every sequence adds at most one incomplete block
     const int64_t blocks = a.total_q / kItem + std::min<int64_t>(a.n_seqs, a.total_q);
     if (blocks * a.H > INT32_MAX) return cudaErrorInvalidValue;
-    kernel<<<dim3((unsigned)(blocks * a.H)), kThreads, kSmemBytes, stream>>>(map_q, map_kv, map_r, PrefillParams{a});
-    return cudaGetLastError();
+    e = launch_dependent(kernel, dim3((unsigned)(blocks * a.H)), dim3(kThreads), kSmemBytes, stream, map_q, map_kv, map_r,
+                         PrefillParams{a});
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace kda

@@ -408,6 +408,22 @@ def test_decode_nan_and_inf_in_the_cache_stay_in_their_request(kda):
     assert o[0].isnan().all() and torch.equal(o[1], clean[1])
 
 
+def test_decode_nan_in_a_new_token_stays_with_the_rows_that_see_it(kda):
+    q, cache, table, lens = decode_case([200, 97], 3, 16, 64, 95)
+    clean = kda.kda_latent_decode(q, cache, table, lens)
+    cache[table[0, 3].long(), 199 - 192, 7] = NAN                        # the last of request 0's three tokens
+    cache[table[1, 1].long(), 95 - 64, 300] = INF                        # the second of request 1's
+    o = kda.kda_latent_decode(q, cache, table, lens)
+    assert torch.equal(o[0, :2], clean[0, :2]) and o[0, 2].isnan().all()
+    assert torch.equal(o[1, 0], clean[1, 0])
+
+
+def test_decode_many_rows_and_tokens(kda):
+    # more rows than one CTA takes, over a table that holds many tokens
+    check_decode(kda, decode_case([9000, 5, 0, 7777, 300], 2, 48, 64, 96))
+    check_decode(kda, decode_case([20000], 1, 33, 16, 97))
+
+
 def test_decode_past_32_bits(kda):
     page, n_pages = 64, 2 ** 31 // (576 * 64) + 200
     cache = torch.empty((n_pages, page, 576), dtype=torch.bfloat16, device="cuda")
