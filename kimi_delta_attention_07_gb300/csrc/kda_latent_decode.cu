@@ -273,6 +273,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return (id << a.page_shift) + (int)(pos & ((1 << a.page_shift) - 1));
             };
             int next_row = row_of(s.tile0);
+            auto queries = [&] {
+                // the queries of the request before have been read by its last first product
+                wait(&empty_q, (seg & 1) ^ 1);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full_q, 9 * kRows * 128);
+                    tma_load_3d(sm + kSmQ, &map_q, 0, s.n * (a.S * a.H) + rb * kRows, 0, &full_q);
+                }
+                __syncwarp();
+            };
+            if (seg == 0) queries();  // while the table entries come
             for (int i = 0; i < s.tiles && !dead; ++i) {
                 const int row = next_row;
                 if (i + 1 < s.tiles) next_row = row_of(s.tile0 + i + 1);
@@ -285,17 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_4d(sm + kSmTile + slot * kTileBytes + j * kCopyBytes, &map_c, 0, 0, 0, row >> 3,
                                     &full[slot]);
                 }
-                if (i == 0) {
-                    // the queries of the request before have been read by its last first product
-                    wait(&empty_q, (seg & 1) ^ 1);
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&full_q, 9 * kRows * 128);
-                        for (int b = 0; b < 9; ++b)
-                            tma_load_2d(sm + kSmQ + b * kRows * 128, &map_q, b * 64, s.n * (a.S * a.H) + rb * kRows,
-                                        &full_q);
-                    }
-                    __syncwarp();
-                }
+                if (i == 0 && seg > 0) queries();
                 if (++slot == kSlots) slot = 0, phase ^= 1;
             }
         }
@@ -676,6 +676,19 @@ __global__ void __launch_bounds__(kJoinThreads) latent_decode_join_kernel(const 
     if (a.lse && lane == 0 && d0 == 0) a.lse[out] = l == 0.0f ? -INFINITY : (top + log2_sfu(l)) * kLn2;
 }
 
+// Rows of 576 as {64 columns, rows, 9 blocks}: a box is the K-major operand of `box_rows` rows.
+inline bool encode_blocks(CUtensorMap *m, const void *base, int64_t rows, int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, 9};
+    const cuuint64_t strides[2] = {kLatentRow * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 9};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The cache as {64 columns, 8 rows, 9 blocks, groups of 8 rows}, a copy being two groups.
 inline bool encode_cache(CUtensorMap *m, const void *base, int64_t rows) {
     auto enc = tensor_map_encoder();
@@ -709,7 +722,7 @@ cudaError_t launch(const LatentDecodeArgs &a, cudaStream_t stream) {
     p.stats = (Stat *)(ws + joins_bytes(g));
     p.parts = ws + joins_bytes(g) + stats_bytes<ROWS>(g);
     CUtensorMap map_q, map_c;
-    if (!encode_rows64(&map_q, a.q, kLatentRow, (int64_t)a.n_seqs * a.S * a.H, kLatentRow, ROWS) ||
+    if (!encode_blocks(&map_q, a.q, (int64_t)a.n_seqs * a.S * a.H, ROWS) ||
         !encode_cache(&map_c, a.cache, a.n_pages << a.page_shift))
         return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
