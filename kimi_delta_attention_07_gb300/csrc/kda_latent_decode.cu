@@ -28,7 +28,9 @@
 // Tiles of 48 tokens: a tile stays in shared memory until its second product is
 // done, which is about 1.2 us after it has arrived (at 44 bytes a ns); three
 // tiles of 48 keep more in flight (90 KB) than two of 64 (68 KB).  The first
-// product's M is 64: its last 16 rows are whatever follows in the ring.
+// product's M is 64: its last 16 rows are whatever follows in the ring.  256
+// requests of 512 to 4096 tokens, 32 heads (697 MB): 125 us, 5.6 TB/s; with the
+// products cut to a ninth, so that little but the loads is left, 122 us.
 //
 // Running maximum: rows keep a reference that is only raised (and O^T in TMEM
 // rescaled) when some score passes it by 2^8, which is decided by one vote a
@@ -36,14 +38,14 @@
 // that the quotient is unchanged.  Sums are fp32 per thread, joined at the end.
 //
 // Work split: the tiles of all requests, in order, are cut evenly into one
-// range per CTA (a persistent CTA per SM; rows beyond 32 take further CTAs over
-// the same tiles).  A request inside one range is finished there; one that
+// range per CTA (a persistent CTA per SM; query rows beyond 32, or 64 where the
+// requests are long, take further CTAs over the same tiles).  A request inside one range is finished there; one that
 // crosses ranges leaves (O, max, sum) parts in the workspace, which a second,
 // dependent kernel joins in range order.
 //
-// Warps: 0..2 softmax (16 tokens each), 0..3 rescaling and epilogue, 4 TMA, 5
-// first products, 6 second products (one warp that polled for both took 135 us
-// where two take 129).
+// Warps: 0 TMA, 1 first products, 2 second products (one warp that polled for both
+// took 135 us where two take 129), 4..6 softmax (16 tokens each), 4..7 rescaling
+// and epilogue.
 #include <algorithm>
 
 #include "kda_attn.cuh"
@@ -57,7 +59,7 @@ namespace {
 constexpr int kCopy = 16;   // tokens per copy
 constexpr int kCopies = 3;  // copies per tile
 constexpr int kTile = kCopies * kCopy;
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr uint32_t kGroup = 9 * 1024;        // 8 tokens
 constexpr uint32_t kCopyBytes = 2 * kGroup;
 constexpr uint32_t kTileBytes = kCopies * kCopyBytes;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         dead = lost = 0;
     }
-    if (wid == 5) tmem_alloc(&tmem_base, C::kTmemCols);
+    if (wid == 1) tmem_alloc(&tmem_base, C::kTmemCols);
     // (the join is not let in early: its CTAs would settle on the SMs that finish
     // first and run there one after the other)
     griddep_wait();
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_base;
     Segment s;
 
-    if (wid == 4) {
+    if (wid == 0) {
         // ---- TMA: the queries of a request, then its tiles
         int slot = 0, phase = 0, seg = 0;
         for (; !dead && walk.next(s); ++seg) {
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++slot == kSlots) slot = 0, phase ^= 1;
             }
         }
-    } else if (wid == 5) {
+    } else if (wid == 1) {
         // ---- first products, one tile ahead of the softmax (two accumulators)
         if (elect_one()) {
             const uint32_t q0 = smem_u32(sm + kSmQ), tile_0 = smem_u32(sm + kSmTile);
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (wid == 6) {
+    } else if (wid == 2) {
         // ---- second products
         if (elect_one()) {
             const uint32_t tile_0 = smem_u32(sm + kSmTile), p0 = smem_u32(sm + kSmP);
@@ -354,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else {
+    } else if (wid >= 4) {
+        const int tid = threadIdx.x - 128, wid = tid >> 5;  // of the four softmax warps
         // ---- softmax: a thread holds scores of tokens 16 w + lane / 4 (+ 8) of the tile by
         // rows 8 j + 2 (lane % 4) + {0, 1}; warp 3 has no tokens (its scores are hidden)
         const Walk again = walk;
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long t0 = clock64();
         while (clock64() - t0 < 100000000LL) __nanosleep(1000);
     }
-    if (wid == 5) tmem_dealloc(tmem, C::kTmemCols);
+    if (wid == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 // Joins the parts of a request that crosses ranges.  With many rows a warp takes

@@ -7,23 +7,28 @@
 // over the keys in tiles of 128:
 //   X_t [128 x 128] = Q_t [128 x 192] . K^T    operands in shared memory
 //   O_t [128 x 128] += P_t [128 x 128] . V     P from TMEM, over X_t's columns
-// X_0, X_1, O_0, O_1 fill the 512 TMEM columns.  With two tiles the tensor core works on
-// one while the softmax of the other runs: the order is
+// X_0, X_1, O_0, O_1 fill the 512 TMEM columns.  With two tiles the tensor core
+// works on one while the softmax of the other runs: one thread issues
 //   P_0 V(i), X_0(i+1), P_1 V(i), X_1(i+1), ...
-// 768 + 512 clocks a tile and step at the tensor core's 4096 products a clock.
+// (its MMAs execute in that order, so that X_t(i+1) overwrites P_t(i) after it was
+// read), 768 + 512 clocks a tile and step at the tensor core's 4096 products a clock.
 //
-// What bounds a step is the chain X_t(i), softmax, P_t V(i), X_t(i+1) of a tile, whose
-// scores and P share columns; with one thread a row it took 4650 clocks against
-// the 2560 that the tensor core needs for both tiles.  So two threads own a query
-// row (TMEM lane), 64 keys of a step each: they exchange their maxima in a step
-// and their sums at the end, and hand P over in two parts, the first of which is
-// multiplied while the second is computed.  The reference that p is taken against is raised (and the
-// row of O rescaled) only where the row's maximum passes it by 2^8; p, its sum
-// and O share it, so that the quotient is unchanged.
+// What bounded a step was the chain X_t(i), softmax, P_t V(i), X_t(i+1) of a tile
+// (4650 clocks with one thread a row, against the 2560 that the tensor core needs
+// for both tiles) and the issuing thread's own instructions.  So two threads own a
+// query row (TMEM lane), 64 keys of a step each; they exchange their maxima in a
+// step and their sums at the end, and hand P over in two parts, the first of which
+// is multiplied while the second is computed.  A step takes about 3250 clocks: 1550
+// TFLOP/s on 8192 queries and keys without a mask, where shared memory, which
+// X_t's operands alone read at its full 128 bytes a clock, leaves little room.
 //
-// K and V tiles come as blocks of 64 columns (16 KB) through a ring of eight,
-// K(i) three, V(i) two.  The positional key's block is
-// read for every head from the one shared copy.
+// The reference that p is taken against is raised (and the row of O rescaled) only
+// where the row's maximum passes it by 2^8; p, its sum and O share it, so that the
+// quotient is unchanged.
+//
+// K and V tiles come as blocks of 64 columns (16 KB) through a ring of eight, K(i)
+// three, V(i) two; the positional key's block is read for every head from the one
+// shared copy.
 //
 // Masked places: keys that a row does not see get p = 0, and 0 times a value has
 // to be 0 whatever the value is.  In the tiles where some key is not seen by
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&o_empty[t]);
             }
             // Eight lanes exchange their units, so that a store writes whole 128-byte lines of four rows
-            // (16 bytes of 32 rows a store kept the load/store unit busy for 4000 clocks a tile pair).
+            // (as against 16 bytes of 32 rows: 128.3 instead of 126.0 us for 4096 tokens, 32 heads).
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) {
                 const bool up = lane & o;

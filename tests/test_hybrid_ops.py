@@ -579,6 +579,65 @@ def test_prefill_other_stream_and_repeats(kda):
     assert torch.equal(o, other)
 
 
+def test_prefill_past_32_bits(kda):
+    # the second sequence's keys lie past 2^31 elements of kv, its queries behind an empty sequence
+    H, first, lk = 32, 2 ** 31 // (32 * 256) + 500, 300
+    kv = torch.empty((first + lk, H, 256), dtype=torch.bfloat16, device="cuda")
+    rope = torch.empty((first + lk, 64), dtype=torch.bfloat16, device="cuda")
+    kv[first:], rope[first:] = normal((lk, H, 256), 1), normal((lk, 64), 2)
+    q = normal((5, H, 192), 3)
+    a = kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=i32([0, 0, 5]), cu_seqlens_k=i32([0, first, first + lk]))
+    b = kda.kda_latent_prefill(q, kv[first:].clone(), rope[first:].clone(), cu_seqlens_q=i32([0, 5]),
+                               cu_seqlens_k=i32([0, lk]))
+    assert torch.equal(a, b) and a.isfinite().all()
+
+
+def test_a_step_in_a_graph(kda):
+    """All operators in one captured graph, replayed on other lengths and data."""
+    H, N, page, pages = 4, 3, 32, 40
+    g = torch.Generator().manual_seed(1)
+    new, ctx = i32([5, 1, 40]), i32([0, 0, 0])
+    free, table = torch.randperm(pages, generator=g).to(torch.int32).cuda(), i32([[-1] * 8] * N)
+    x, w = normal((64, 576), 2), torch.rand(512, generator=gen(3), device="cuda") + 0.5
+    cache = torch.zeros((pages, page, 576), dtype=torch.bfloat16, device="cuda")
+    q, kv, qa = normal((64, H, 192), 4), normal((64, H, 256), 5), normal((N, H, 576), 6)
+    ws = torch.empty(kda.kda_latent_decode_workspace_bytes(N, 1, H), dtype=torch.uint8, device="cuda")
+    out = {}
+
+    def step():
+        cu, lens, slots, pos, status = kda.kda_page_tables(ctx, new, free, table, page_size=page, n_pages=pages, max_tokens=64)
+        y, _, _ = kda.kda_rms_norm(x, residual=x)
+        kda.kda_latent_cache_write(y, w, cache, slots)
+        o = kda.kda_latent_prefill(q, kv, y[:, 512:], cu_seqlens_q=cu)
+        d = kda.kda_latent_decode(qa, cache, table, lens, workspace=ws)
+        out.update(o=o, d=d, lens=lens, slots=slots)
+        return out
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    captured = dict(out)
+    for lens, seed in (([5, 1, 40], 7), ([0, 33, 2], 8), ([20, 20, 20], 9)):
+        new.copy_(i32(lens))
+        x.copy_(normal((64, 576), seed))
+        for t in (cache, captured["o"], captured["d"]):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: v.clone() for k, v in captured.items()}
+        cache.zero_()
+        want = step()
+        n = sum(lens)
+        assert torch.equal(got["o"][:n], want["o"][:n]) and (got["o"][n:] == 0).all()
+        for k in ("d", "lens", "slots"):
+            assert torch.equal(got[k], want[k]), k
+
+
 def test_prefill_agrees_with_decode(kda):
     """The two forms on the same layer: k = [U c; r], v = W c against q' = [U^T q; q_r] and W applied after."""
     H, n = 4, 90
