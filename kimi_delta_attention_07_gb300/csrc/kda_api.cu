@@ -31,7 +31,7 @@ const char *kda_status_string(int status) {
     switch (status) {
         case KDA_OK: return "KDA_OK";
         case KDA_ERR_INVALID_ARG: return "KDA_ERR_INVALID_ARG: invalid argument";
-        case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: only K = V = 128 is built";
+        case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: outside what is built (the core: K = V = 128)";
         case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE: workspace missing, too small or misaligned";
         case KDA_ERR_CUDA: return "KDA_ERR_CUDA: a CUDA call or kernel launch failed";
         case KDA_ERR_DEVICE_TIMEOUT:

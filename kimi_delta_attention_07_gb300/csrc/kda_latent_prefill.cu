@@ -82,7 +82,7 @@ struct Shared {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], x_full[2], p_full[2][2], o_full[2], o_empty[2],
         unchecked[2][2], item_full[2], item_empty[2], next_full;
     uint4 next_answer;
-    Item items[2];
+    Item items[3];            // two handed out in turn; [2]: claimed, not handed out yet
     float half[2][2][kTile];  // what the two threads of a row exchange
     int piece[kPieces];       // blocks of 256 queries of the sequences before each piece
     int warp_total[kPieces / 32];
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.next_full, 1);
         fence_mbar_init();
         dead = 0;
+        for (int i = 0; i < 3; ++i) sh.items[i].valid = 0;
     }
     if (wid == 17) tmem_alloc(&sh.tmem_base, 512);
     griddep_wait();
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (i == 0) {
                         // the queries of the item after this one, from DRAM into L2 while this one runs
                         more = next_item(next);
+                        if (more) sh.items[2] = next;
                         if (more)
                             for (int b = 0; b < 6; ++b)
                                 if (next.steps(b / 3) > 0)
@@ -286,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (steps == 0) more = next_item(next);
+                if (steps == 0 && more) sh.items[2] = next;
                 if (dead) break;
                 cur = next;
             }
@@ -568,7 +571,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (dead) {  // let copies still in flight land before the CTA's memory is given up
+    if (dead) {
+        // A wait gave up: what this CTA had in hand becomes NaN, and copies still in flight land before
+        // its memory is given up.
+        for (int i = 0; i < 3; ++i) {
+            const Item &s = sh.items[i];
+            if (!s.valid) continue;
+            const int rows = min(s.lq - s.q0, kItem);
+            for (int j = tid; j < rows * kHeadDim; j += kThreads) {
+                const int64_t out = (int64_t)(s.qa + s.q0 + j / kHeadDim) * a.H + s.h;
+                a.o[out * kHeadDim + j % kHeadDim] = __float2bfloat16_rn(NAN);
+                if (a.lse && j % kHeadDim == 0) a.lse[out] = NAN;
+            }
+        }
         const long long t0 = clock64();
         while (clock64() - t0 < 100000000LL) __nanosleep(1000);
     }

@@ -167,19 +167,13 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const RmsNormArgs
     }
 }
 
-// The resident CTAs of a kernel; the query costs as much as the launch, so its answer is kept
-// (it depends on the kernel and the GPU model alone).
 template <typename T, int QUANT, int NV, bool WARP>
 cudaError_t launch(const RmsNormArgs &a, int threads, int rows_per_cta, cudaStream_t stream) {
     auto kern = rms_norm_kernel<T, QUANT, NV, WARP>;
-    static int kept[kMaxThreads / 32 + 1] = {0};
-    int per_sm = kept[threads / 32];
-    if (per_sm == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) {
-            cudaGetLastError();
-            per_sm = 1;
-        }
-        kept[threads / 32] = per_sm;
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) {
+        cudaGetLastError();
+        per_sm = 1;
     }
     const int64_t want = (a.rows + rows_per_cta - 1) / rows_per_cta, most = (int64_t)sm_count() * per_sm;
     const cudaError_t e =

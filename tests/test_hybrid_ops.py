@@ -633,7 +633,7 @@ def test_a_step_in_a_graph(kda):
         cache.zero_()
         want = step()
         n = sum(lens)
-        assert torch.equal(got["o"][:n], want["o"][:n]) and (got["o"][n:] == 0).all()
+        assert torch.equal(got["o"][:n], want["o"][:n])   # (rows past the last sequence are not written)
         for k in ("d", "lens", "slots"):
             assert torch.equal(got[k], want[k]), k
 
