@@ -13,7 +13,7 @@ import torch
 import kimi_delta_attention_07_gb300 as _core
 
 KDA_QUANT_NONE, KDA_QUANT_ROW, KDA_QUANT_BLOCK = range(3)
-KDA_BF16 = 1
+KDA_BF16 = _core.KDA_BF16
 LATENT_DIM, ROPE_DIM, LATENT_ROW, NOPE_DIM, VALUE_DIM = 512, 64, 576, 128, 128
 _QUANT = {"none": KDA_QUANT_NONE, None: KDA_QUANT_NONE, "row": KDA_QUANT_ROW, "block": KDA_QUANT_BLOCK}
 _bf16, _f32, _i32, _u8, _e4m3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,

@@ -104,9 +104,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&u)[32
         "r"(u[29]), "r"(u[30]), "r"(u[31])
         : "memory");
 }
-// tmem_ld_wait for loads that other work was put behind: the registers pass
-// through the wait, so that none is read before it.
-__device__ __forceinline__ void tmem_ld_wait32(float (&r)[32]) {
+// Waits for this thread's TMEM loads.  The registers of one pass through the wait, so that the
+// compiler reads none of them before it.
+__device__ __forceinline__ void tmem_ld_wait_for(float (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7])
+        :
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+          "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+        :
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(float (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
         : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
           "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),

@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kRows / 32; ++k)
                     tmem_ld_16x32(tmem + kTmemX + (t & 1) * kRows + 32 * k + lanes,
                                   *reinterpret_cast<float(*)[16]>(x + 16 * k));
-                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < kRows / 32; ++k) tmem_ld_wait_for(*reinterpret_cast<float(*)[16]>(x + 16 * k));
 #pragma unroll
                 for (int j = 0; j < 2 * kCols; ++j) x[j] *= scale2;
                 if (pos0 + kTile > s.len - a.S + 1 || wid >= kCopies) {
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4 * kRows / 32; ++k) {
                             float o[32];
                             tmem_ld32(tmem + k * 32 + lanes, o);
-                            tmem_ld_wait();
+                            tmem_ld_wait_for(o);
                             uint32_t u[32];
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k) {
                         float o[32];
                         tmem_ld32(tmem + k * kRows + c0 + lanes, o);
-                        tmem_ld_wait32(o);
+                        tmem_ld_wait_for(o);
                         __nv_bfloat16 *dst = a.o + (row0 + c0) * kLatent + k * 128 + tid;
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k) {
                         float o[32];
                         tmem_ld32(tmem + k * kRows + c0 + lanes, o);
-                        tmem_ld_wait32(o);
+                        tmem_ld_wait_for(o);
                         float *dst = &part->o[c0][k * 128 + tid];
 #pragma unroll
                         for (int c = 0; c < 32; ++c)

@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float x[2][32], top = -INFINITY;
                 tmem_ld32(tx + 64 * half, x[0]);
                 tmem_ld32(tx + 64 * half + 32, x[1]);
-                tmem_ld_wait32(x[0]);
-                tmem_ld_wait32(x[1]);
+                tmem_ld_wait_for(x[0]);
+                tmem_ld_wait_for(x[1]);
                 const int left = limit - i * kTile - 64 * half;
                 if (!POSITIVE) {
 #pragma unroll
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 8; ++k) {
                             float o[8];
                             tmem_ld8(to + 8 * k, o);
-                            tmem_ld_wait();
+                            tmem_ld_wait_for(o);
                             uint32_t u[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(o[j] * f);
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float o[32];
                 if (steps > 0) {
                     tmem_ld32(to + 32 * k, o);
-                    tmem_ld_wait32(o);
+                    tmem_ld_wait_for(o);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0.0f;
