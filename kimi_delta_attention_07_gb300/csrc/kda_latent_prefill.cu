@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int n = lo * per, before = sh.piece[lo], blocks = 0;
                 for (; n < min((lo + 1) * per, a.n_seqs); ++n) {
                     blocks = blocks_of(a, n);
-                    if (rank < before + blocks) break;
+                    if ((unsigned)(rank - before) < (unsigned)blocks) break;
                     before += blocks;
                     blocks = 0;
                 }
@@ -220,8 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the next item that the answers name; false once there is none
             auto next_item = [&](Item &s) {
                 for (;;) {
-                    wait(&sh.next_full, asked++ & 1);
-                    const int cta = dead ? -1 : next_cta_answer(&sh.next_answer);
+                    // (also when another wait has given up: a CTA that was handed over is this one's to answer for)
+                    if (!mbar_wait(&sh.next_full, asked++ & 1)) {
+                        dead = 1;
+                        return false;
+                    }
+                    const int cta = next_cta_answer(&sh.next_answer);
                     fence_async_smem();
                     if (cta < 0) return false;
                     if (item_of_cta(cta, s)) return true;
@@ -236,6 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             while (more) {
                 wait(&item_empty[it & 1], ((it >> 1) & 1) ^ 1);
+                if (dead) {  // the item two before may still be in hand
+                    sh.items[2] = cur;
+                    break;
+                }
                 sh.items[it & 1] = cur;
                 odd[it & 1] = 0;
                 mbar_arrive(&item_full[it & 1]);
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 queries(0);
                 const int steps = cur.most();
-                for (int i = 0; i < steps && !dead; ++i, ++step) {
+                for (int i = 0; i < steps && (i == 0 || !dead); ++i, ++step) {  // (the first one takes the answer)
                     // ring blocks 5 step ..: K three, V two; block c takes the place of block c - 8, which
                     // for K(step) are K(step - 2)'s last and V(step - 2)'s, for V(step) K(step - 1)'s first two
                     const int row = cur.ka + i * kTile;
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 cur = next;
             }
             wait(&item_empty[it & 1], ((it >> 1) & 1) ^ 1);
-            sh.items[it & 1].valid = 0;
+            if (!dead) sh.items[it & 1].valid = 0;
             mbar_arrive(&item_full[it & 1]);
         }
         __syncwarp();
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int left = limit - i * kTile - 64 * half;
                 if (!POSITIVE) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) x[j >> 5][j & 31] = a.scale < 0.0f ? -x[j >> 5][j & 31] : 0.0f;
+                    for (int j = 0; j < 64; ++j) x[j >> 5][j & 31] = x[j >> 5][j & 31] * (a.scale < 0.0f ? -1.0f : 0.0f);
                 }
                 if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll

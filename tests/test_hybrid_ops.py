@@ -530,6 +530,19 @@ def test_prefill_large_scores(kda):
     check_prefill(kda, (q, kv, rope, cq, ck), scale=0.0, causal=False)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.4, 0.1])
+def test_prefill_nan_query_keeps_to_its_row(kda, scale):
+    # 0 times a NaN score is NaN too
+    q, kv, rope, cq, ck = prefill_case([300], [300], 2, 24)
+    plain = kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck, scale=scale)
+    q[140, 1, 3] = NAN
+    lse = torch.empty(q.shape[:2], device="cuda")
+    o = kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck, scale=scale, lse=lse)
+    assert o[140, 1].isnan().all() and lse[140, 1].isnan()
+    o[140, 1] = plain[140, 1]
+    assert torch.equal(o, plain)
+
+
 def test_prefill_strided_inputs(kda):
     H = 3
     q, kv, rope, cq, ck = prefill_case([90, 31], [150, 31], H, 10)
