@@ -44,8 +44,13 @@ int kda_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, const int3
     if (n_seqs > KDA_PAGE_TABLES_MAX_SEQS) return KDA_ERR_UNSUPPORTED;
     if (!cu_seqlens || !status || (n_free > 0 && !free_pages) ||
         (n_seqs > 0 && (!ctx_lens || !new_lens || !block_table || !seq_lens)) ||
-        (max_tokens > 0 && (!slots || !positions)) || (free_start && free_start == status))
+        (max_tokens > 0 && (!slots || !positions)))
         return KDA_ERR_INVALID_ARG;
+    // every CTA reads the inputs, while the first one writes these
+    const int32_t *written[] = {cu_seqlens, seq_lens, slots, positions, status, status + 1, block_table};
+    for (const int32_t *in : {ctx_lens, new_lens, free_pages, free_start})
+        for (const int32_t *out : written)
+            if (in && in == out) return KDA_ERR_INVALID_ARG;
     for (const void *p : {(const void *)ctx_lens, (const void *)new_lens, (const void *)free_pages,
                           (const void *)free_start, (const void *)block_table,
                           (const void *)cu_seqlens, (const void *)seq_lens, (const void *)slots,

@@ -45,7 +45,7 @@ __device__ __forceinline__ Need request_need(const PageTablesArgs &a, int n) {
     d.added = add > 0 ? add : 0;
     d.held = (ctx + r) >> a.page_shift;
     d.total = (ctx + add + r) >> a.page_shift;
-    d.fits = ctx >= 0 && add >= 0 && d.total <= a.max_pages;
+    d.fits = ctx >= 0 && add >= 0 && ctx + add <= INT32_MAX && d.total <= a.max_pages;
     return d;
 }
 

@@ -28,8 +28,8 @@ def _call(fn, order, defaults, kw):
 def _tables(lib, **kw):
     order = ("ctx", "new", "free", "n_free", "start", "table", "cu", "lens", "slots", "pos", "status", "n",
              "tokens", "max_pages", "page", "n_pages", "stream")
-    d = dict.fromkeys(order, BASE)
-    d.update(n_free=8, start=None, status=BASE + 64, n=2, tokens=8, max_pages=4, page=64, n_pages=16, stream=None)
+    d = {k: BASE + 256 * i for i, k in enumerate(order)}
+    d.update(n_free=8, start=None, n=2, tokens=8, max_pages=4, page=64, n_pages=16, stream=None)
     return _call(lib.kda_page_tables, order, d, kw)
 
 
@@ -37,10 +37,15 @@ def _tables(lib, **kw):
                                 dict(tokens=-1), dict(tokens=1 << 31), dict(n_free=-1), dict(max_pages=0),
                                 dict(n_pages=0), dict(n_pages=1 << 25), dict(ctx=None), dict(new=None),
                                 dict(free=None), dict(table=None), dict(cu=None), dict(lens=None),
-                                dict(slots=None), dict(pos=None), dict(status=None), dict(ctx=BASE + 2),
-                                dict(start=BASE + 64)])
+                                dict(slots=None), dict(pos=None), dict(status=None), dict(ctx=BASE + 2)])
 def test_page_tables_refuses(lib, kw):
     assert _tables(lib, **kw) == INVALID
+
+
+@pytest.mark.parametrize("which", ["ctx", "new", "free", "start"])
+@pytest.mark.parametrize("out", ["cu", "lens", "slots", "pos", "status", "table"])
+def test_page_tables_refuses_an_output_that_is_an_input(lib, which, out):
+    assert _tables(lib, **{which: BASE + 1024 * 1024, out: BASE + 1024 * 1024}) == INVALID
 
 
 def test_page_tables_refuses_too_many_requests(lib):

@@ -159,6 +159,17 @@ def test_page_tables_lengths_near_the_type_limit(kda):
     assert t.tolist() == [[1, 2]] and got[2].tolist() == [-1] * 4 and got[4].tolist() == [0, 1]
 
 
+def test_page_tables_sums_of_lengths_past_the_type(kda):
+    # a table row wide enough for the sum: what refuses it is the length itself
+    big = 2 ** 31 - 1
+    t = torch.full((1, 2 ** 28), 3, dtype=torch.int32, device="cuda")
+    for new, ok in ((2, False), (1, False), (0, True)):
+        cu, lens, slots, pos, status = kda.kda_page_tables(i32([big]), i32([new]), i32([3]), t, page_size=16,
+                                                           n_pages=4, max_tokens=2)
+        torch.cuda.synchronize()
+        assert lens.tolist() == [big] and slots.tolist() == pos.tolist() == [-1, -1] and status.tolist() == [0, int(not ok)]
+
+
 # ---- rms norm ---------------------------------------------------------------------
 
 
