@@ -30,7 +30,12 @@
 // tiles of 48 keep more in flight (90 KB) than two of 64 (68 KB).  The first
 // product's M is 64: its last 16 rows are whatever follows in the ring.  256
 // requests of 512 to 4096 tokens, 32 heads (697 MB): 125 us, 5.6 TB/s; with the
-// products cut to a ninth, so that little but the loads is left, 122 us.
+// products cut to a ninth, so that little but the loads is left, 122 us.  With 64
+// query rows a CTA the queries leave room for 128 tokens, as two tiles of 64 (no
+// row of the first product is wasted; four tiles of 32 are 8 to 15 % slower); p
+// then takes the place of the tile's positional block, which the first product
+// has read.  2 requests of 231k tokens in all, 64 rows: 64 us, 40 of them at 6.7
+// TB/s between the first tile's arrival and the last one's.
 //
 // Running maximum: rows keep a reference that is only raised (and O^T in TMEM
 // rescaled) when some score passes it by 2^8, which is decided by one vote a
@@ -38,14 +43,14 @@
 // that the quotient is unchanged.  Sums are fp32 per thread, joined at the end.
 //
 // Work split: the tiles of all requests, in order, are cut evenly into one
-// range per CTA (a persistent CTA per SM; query rows beyond 32, or 64 where the
-// requests are long, take further CTAs over the same tiles).  A request inside one range is finished there; one that
-// crosses ranges leaves (O, max, sum) parts in the workspace, which a second,
-// dependent kernel joins in range order.
+// range per CTA (a persistent CTA per SM; query rows beyond 32, or 64 where much
+// is read, take further CTAs over the same tiles).  A request inside one range is
+// finished there; one that crosses ranges leaves (O, max, sum) parts in the
+// workspace, which a second, dependent kernel joins in range order.
 //
 // Warps: 0 TMA, 1 first products, 2 second products (one warp that polled for both
-// took 135 us where two take 129), 4..6 softmax (16 tokens each), 4..7 rescaling
-// and epilogue.
+// took 135 us where two take 129), 4..7 softmax (16 tokens of the tile each: the
+// last one has none of 48), rescaling and epilogue.
 #include <algorithm>
 
 #include "kda_attn.cuh"
@@ -57,32 +62,28 @@ using namespace tc;
 namespace {
 
 constexpr int kCopy = 16;   // tokens per copy
-constexpr int kCopies = 3;  // copies per tile
-constexpr int kTile = kCopies * kCopy;
 constexpr int kThreads = 256;
 constexpr uint32_t kGroup = 9 * 1024;        // 8 tokens
 constexpr uint32_t kCopyBytes = 2 * kGroup;
-constexpr uint32_t kTileBytes = kCopies * kCopyBytes;
 constexpr float kRaise = 8.0f;  // log2 by which a score may pass its row's reference
 
 // What depends on the query rows per CTA, 32 or 64.
 template <int ROWS>
 struct Cfg {
+    static constexpr int kCopies = ROWS == 32 ? 3 : 4;  // copies in a tile
+    static constexpr int kTile = kCopies * kCopy;
     static constexpr int kSlots = ROWS == 32 ? 3 : 2;  // tiles in the ring
+    static constexpr bool kOwnP = ROWS == 32;  // two P of their own, else P over the tile's positional block
     // shared memory (from a 1024-byte boundary); the ring comes first, so that the
-    // 16 rows which a first product reads past its tile are inside
+    // 16 rows which a first product of 48 tokens reads past its tile are inside
+    static constexpr uint32_t kTileBytes = kCopies * kCopyBytes;
     static constexpr uint32_t kPBytes = 64 * ROWS * 2;              // [64 tokens][ROWS]
     static constexpr uint32_t kSmQ = kSlots * kTileBytes;           // [9][ROWS][128 B]
     static constexpr uint32_t kSmP = kSmQ + 9 * ROWS * 128;         // two P
-    static constexpr uint32_t kSmemBytes = kSmP + 2 * kPBytes + 1024;  // + alignment of the base
+    static constexpr uint32_t kSmemBytes = kSmP + (kOwnP ? 2 * kPBytes : 0) + 1024;  // + alignment of the base
     static_assert(9 * ROWS * 128 >= 2 * kGroup, "rows past the last tile");
     static constexpr uint32_t kTmemX = 4 * ROWS;  // O^T: 4 x ROWS columns, then X^T: 2 x ROWS
     static constexpr uint32_t kTmemCols = 8 * ROWS;
-    // P as B operand, MN-major: rows of 64 bytes (64-byte swizzle) or 128 bytes (128-byte swizzle)
-    static constexpr uint64_t kPDesc = ((uint64_t)(ROWS == 32 ? kDescHiSw64 : kDescHi) << 32);
-    static __device__ __forceinline__ uint32_t p_off(int token, int row) {
-        return ROWS == 32 ? sw64_off(token, row) : sw128_off(token, row, 64);
-    }
 };
 
 // Operand descriptors of a tile (128-byte swizzle, 8-token groups kGroup apart):
@@ -94,6 +95,18 @@ __device__ __forceinline__ uint64_t tile_desc_k(uint32_t tile, int b, int k) {
 }
 __device__ __forceinline__ uint64_t tile_desc_mn(uint32_t tile, int b, int k) {
     return ((uint64_t)kTileDescHi << 32) | (((tile & 0x3FFFFu) >> 4) + b * 128 + k * (kCopyBytes >> 4)) | (64u << 16);
+}
+
+// P as B operand, MN-major, and the place of a token's row in it: an own buffer of rows of 64 bytes
+// (64-byte swizzle), or the last block of the tile, which the second product does not read.
+__device__ __forceinline__ uint64_t own_p_desc(uint32_t p, int k) {
+    return ((uint64_t)kDescHiSw64 << 32) | (((p & 0x3FFFFu) >> 4) + k * (16 * 64 >> 4));
+}
+__device__ __forceinline__ uint64_t tile_p_desc(uint32_t tile, int k) {
+    return ((uint64_t)kTileDescHi << 32) | (((tile & 0x3FFFFu) >> 4) + 8 * 64 + k * (kCopyBytes >> 4)) | (64u << 16);
+}
+__device__ __forceinline__ uint32_t tile_p_off(int token, int row) {
+    return (token >> 3) * kGroup + 8 * 1024 + sw128_off(token & 7, row, 64);
 }
 
 template <int ROWS>
@@ -137,10 +150,11 @@ struct DecodeParams {
                   // by the entry of the range that it begins in (at most one leaves a range)
 };
 
+template <int TILE>
 __device__ __forceinline__ int tiles_of(const LatentDecodeArgs &a, int len) {
     // an empty request (or one that cannot be read) still has a tile: its outputs are written
     const bool ok = len >= 0 && (int64_t)len <= ((int64_t)a.max_pages << a.page_shift);
-    return ok && len > 0 ? (int)(((int64_t)len + kTile - 1) / kTile) : 1;
+    return ok && len > 0 ? (int)(((int64_t)len + TILE - 1) / TILE) : 1;
 }
 
 // One request's share of a range.
@@ -151,6 +165,7 @@ struct Segment {
 };
 
 // Walks the range's requests; every role keeps its own.
+template <int TILE>
 struct Walk {
     const LatentDecodeArgs &a;
     int n, off, left;
@@ -162,7 +177,7 @@ struct Walk {
         s.len = begun ? a.seq_lens[n] : len;
         begun = true;
         s.ok = s.len >= 0 && (int64_t)s.len <= ((int64_t)a.max_pages << a.page_shift);
-        s.total = tiles_of(a, s.len);
+        s.total = tiles_of<TILE>(a, s.len);
         if (!s.ok) s.len = 0;
         s.tile0 = off;
         s.tiles = min(s.total - off, left);
@@ -178,8 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_c, const DecodeParams p) {
     using C = Cfg<kRows>;
-    constexpr int kSlots = C::kSlots, kCols = kRows / 4;  // score columns of a softmax thread
-    constexpr uint32_t kSmTile = 0, kSmQ = C::kSmQ, kSmP = C::kSmP, kTmemX = C::kTmemX;
+    constexpr int kSlots = C::kSlots, kCopies = C::kCopies, kTile = C::kTile;
+    constexpr int kCols = kRows / 4;  // score columns of a softmax thread
+    constexpr uint32_t kSmTile = 0, kSmQ = C::kSmQ, kSmP = C::kSmP, kTmemX = C::kTmemX, kTileBytes = C::kTileBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     __shared__ uint64_t full[kSlots], empty[kSlots][kCopies], full_q, empty_q, x_full[2], p_full[2], pv_done[2], o_empty;
@@ -217,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int mine = 0, last_len = 0;
     for (int n = n0; n < n1; ++n) {
         last_len = a.seq_lens[n];
-        mine += tiles_of(a, last_len);
+        mine += tiles_of<kTile>(a, last_len);
     }
     int before = mine;
 #pragma unroll
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = n0, len = last_len;
         for (; n + 1 < n1; ++n) {
             len = a.seq_lens[n];
-            const int t = tiles_of(a, len);
+            const int t = tiles_of<kTile>(a, len);
             if (range_begin < before + t) break;
             before += t;
             len = last_len;
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         start_off = range_begin - before;
     }
     __syncthreads();
-    Walk walk{a, start_n, start_off, range_end - range_begin, start_len, false};
+    Walk<kTile> walk{a, start_n, start_off, range_end - range_begin, start_len, false};
     // a bounded wait; once one has given up, none waits any more
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (!dead && !mbar_wait(bar, parity)) dead = 1;
@@ -346,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
                             mma_bf16(tmem + b * kRows, tile_desc_mn(tile, b, k),
-                                     C::kPDesc | (((pt & 0x3FFFFu) >> 4) + k * (16 * kRows * 2 >> 4)), idesc,
+                                     C::kOwnP ? own_p_desc(pt, k) : tile_p_desc(tile, k), idesc,
                                      i > 0 || k > 0);
                         mma_commit(&empty[slot][k]);
                     }
@@ -360,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tid = threadIdx.x - 128, wid = tid >> 5;  // of the four softmax warps
         // ---- softmax: a thread holds scores of tokens 16 w + lane / 4 (+ 8) of the tile by
         // rows 8 j + 2 (lane % 4) + {0, 1}; warp 3 has no tokens (its scores are hidden)
-        const Walk again = walk;
+        const Walk<kTile> again = walk;
         const uint32_t lanes = (uint32_t)(wid * 32) << 16;
         const float scale2 = a.scale * kLog2e;
         const int rows = min(kRows, a.S * a.H - rb * kRows);
@@ -420,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                uint8_t *const held = sm + kSmTile + slot * kTileBytes;
                 if (++slot == kSlots) slot = 0;
                 float over = -INFINITY;  // fmaxf skips the NaN of -inf - -inf
 #pragma unroll
@@ -476,13 +493,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x[j + 2] = exp2_sfu(x[j + 2] - ref);
                     l[c] += x[j] + x[j + 2];
                 }
-                // this buffer's p was read by the second product of two tiles ago
-                if (t >= 2) wait(&pv_done[t & 1], ((t >> 1) & 1) ^ 1);
-                uint8_t *ps = sm + kSmP + (t & 1) * C::kPBytes;
+                auto put = [&](int token, int row, uint32_t two) {
+                    uint8_t *at = C::kOwnP ? sm + kSmP + (t & 1) * C::kPBytes + sw64_off(token, row) : held + tile_p_off(token, row);
+                    *(uint32_t *)at = two;
+                };
+                // an own buffer's p was read by the second product of two tiles ago (a tile's positional
+                // block by its first product)
+                if (C::kOwnP && t >= 2) wait(&pv_done[t & 1], ((t >> 1) & 1) ^ 1);
 #pragma unroll
                 for (int j = 0; j < kRows / 8; ++j) {
-                    *(uint32_t *)(ps + C::p_off(tok, 8 * j + col)) = pack2(x[4 * j], x[4 * j + 1]);
-                    *(uint32_t *)(ps + C::p_off(tok + 8, 8 * j + col)) = pack2(x[4 * j + 2], x[4 * j + 3]);
+                    put(tok, 8 * j + col, pack2(x[4 * j], x[4 * j + 1]));
+                    put(tok + 8, 8 * j + col, pack2(x[4 * j + 2], x[4 * j + 3]));
                 }
                 fence_async_smem();
                 tc_fence_before();
@@ -562,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.joins[range] = {-1, 0, 0, 0};
         if (!named_bar_and(1, 128, !dead)) {
             // a wait gave up: the range's outputs are NaN, and requests that cross it are left unjoined
-            Walk w = again;
+            Walk<kTile> w = again;
             while (w.next(s)) {
                 const int64_t row0 = (int64_t)s.n * a.S * a.H + rb * kRows;
                 for (int c = 0; c < rows; ++c) {
@@ -753,11 +774,13 @@ size_t latent_decode_workspace_bytes(int n_seqs, int S, int H) {
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
-    // 64 query rows a CTA read the cache half as often (64 requests of 2304 tokens, 128 rows each: 96 us
-    // against 108 us), but take longer over a single tile (4 requests of up to 700 tokens, 128 rows each:
-    // 16.6 us against 14.5 us), which is all there is when the block table holds few tokens.
-    const int64_t most = ((int64_t)a.n_seqs * a.max_pages) << a.page_shift;
-    return a.S * a.H > 32 && most > 16384 ? launch<64>(a, stream) : launch<32>(a, stream);
+    // 64 query rows a CTA read the cache half as often, but take 3 us longer over a first tile, and their
+    // ring holds 128 tokens against 144.  What counts is how often 32 rows a CTA would read the tokens that
+    // the block table can hold: 128k tokens (4 requests, 128 rows each) 30.4 us with 32 rows and 31.6 us with
+    // 64, 180k (7 requests, 64 rows) 35.5 and 37.2, 187k (183 requests, 128 rows) 56.4 and 52.1, 256k
+    // (16 requests, 48 rows) 46.6 and 41.8, 640k (4 requests, 128 rows) 87.6 and 68.4.
+    const int64_t read = (((int64_t)a.n_seqs * a.max_pages) << a.page_shift) * ((a.S * a.H + 31) / 32);
+    return a.S * a.H > 32 && read > 184320 ? launch<64>(a, stream) : launch<32>(a, stream);
 }
 
 }  // namespace kda

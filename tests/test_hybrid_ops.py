@@ -435,6 +435,40 @@ def test_decode_many_rows_and_tokens(kda):
     check_decode(kda, decode_case([20000], 1, 33, 16, 97))
 
 
+def widened(case):
+    """The same requests with a table that could hold many more tokens."""
+    q, cache, table, lens = case
+    more = 200000 // (table.shape[0] * cache.shape[1]) + 1
+    return q, cache, torch.cat([table, table.new_full((table.shape[0], more), -1)], 1), lens
+
+
+@pytest.mark.parametrize("S,H,page", [(1, 33, 16), (1, 64, 64), (2, 32, 256), (4, 32, 32), (3, 48, 128), (16, 8, 64)])
+def test_decode_many_rows_over_a_wide_table(kda, S, H, page):
+    check_decode(kda, widened(decode_case([0, S - 1, S, 48, 49, *EDGES, 700], S, H, page, 98)))
+
+
+def test_decode_many_rows_over_a_wide_table_large_scores(kda):
+    q, cache, table, lens = decode_case([1500, 129, 64], 2, 32, 64, 71)
+    ramp = torch.linspace(0.2, 6.0, 1500, device="cuda")
+    rows = cache[table[0, :24].long()].reshape(-1, 576)
+    rows[:1500] *= ramp[:, None].to(torch.bfloat16)
+    cache[table[0, :24].long()] = rows.view(24, 64, 576)
+    check_decode(kda, widened((q * 4, cache, table, lens)))
+    check_decode(kda, widened((q, cache, table, lens)), scale=-0.3)
+
+
+def test_decode_many_rows_over_a_wide_table_not_finite(kda):
+    q, cache, table, lens = widened(decode_case([200, 97, 90, 300], 3, 16, 64, 99))
+    clean = kda.kda_latent_decode(q, cache, table, lens)
+    cache[table[0, 3].long(), 199 - 192, 7] = NAN                        # the last of request 0's three tokens
+    cache[table[1, 1].long(), 95 - 64, 530] = INF                        # the key of the second of request 1's
+    table[2, 1] = cache.shape[0]
+    o = kda.kda_latent_decode(q, cache, table, lens)
+    assert torch.equal(o[0, :2], clean[0, :2]) and o[0, 2].isnan().all()
+    assert torch.equal(o[1, 0], clean[1, 0])
+    assert o[2].isnan().all() and torch.equal(o[3], clean[3])
+
+
 def test_decode_past_32_bits(kda):
     page, n_pages = 64, 2 ** 31 // (576 * 64) + 200
     cache = torch.empty((n_pages, page, 576), dtype=torch.bfloat16, device="cuda")
