@@ -154,6 +154,15 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
                       int64_t n_pages, int page_size, int max_pages, float scale, void *workspace,
                       size_t workspace_bytes, void *stream);
 
+/* Device workspace (256-byte aligned) of kda_latent_prefill: partial results,
+ * where there are too few queries to fill the GPU and so many keys that they are
+ * split (for queries that see KDA_LATENT_PREFILL_SPLIT_KEYS of them; the split,
+ * and with it the rounding, follows from the arguments n_seqs, total_q, total_k, H
+ * and the lengths).  0: none is needed, as always where total_k is less than
+ * KDA_LATENT_PREFILL_SPLIT_KEYS; 0 on invalid sizes. */
+#define KDA_LATENT_PREFILL_SPLIT_KEYS 1024
+size_t kda_latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t total_k, int H);
+
 /*
  * Expanded latent attention over packed sequences (prefill).
  *
@@ -172,13 +181,14 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
  *
  * A query that sees no key gives o = 0 and lse = -inf.  Tokens of a sequence
  * whose offsets are decreasing or out of range are not written.  Pointers are
- * 16-byte aligned.  Tq = 0 is a no-op.
+ * 16-byte aligned.  Tq = 0 is a no-op.  Results do not depend on timing: parts
+ * are joined in a fixed order.
  */
 int kda_latent_prefill(const void *q, int64_t q_stride, const void *kv, int64_t kv_stride,
                        const void *k_rope, int64_t rope_stride, void *o, float *lse,
                        const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int n_seqs,
                        int64_t total_q, int64_t total_k, int H, int causal, float scale,
-                       void *stream);
+                       void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

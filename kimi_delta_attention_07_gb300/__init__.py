@@ -46,7 +46,7 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_workspace_bytes", "kda
            "kda_short_conv_update", "kda_short_conv_multi_update", "kda_recurrent_multi_step_gated",
            "kda_status_from_workspace_flags", "kda_page_tables", "kda_rms_norm",
            "kda_latent_cache_write", "kda_latent_decode_workspace_bytes", "kda_latent_decode",
-           "kda_latent_prefill")
+           "kda_latent_prefill_workspace_bytes", "kda_latent_prefill")
 NOALLOC_WORKSPACE_BYTES = 64 * 1024 * 1024
 
 _lib = None
@@ -128,7 +128,9 @@ def load(path: str | None = None):
         L.kda_latent_decode.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, f32, vp,
                                         sz, vp]
         L.kda_latent_prefill.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i64, i64, i32,
-                                         i32, f32, vp]
+                                         i32, f32, vp, sz, vp]
+        L.kda_latent_prefill_workspace_bytes.argtypes = [i32, i64, i64, i32]
+        L.kda_latent_prefill_workspace_bytes.restype = sz
         for name in ("kda_page_tables", "kda_rms_norm", "kda_latent_cache_write", "kda_latent_decode",
                      "kda_latent_prefill"):
             getattr(L, name).restype = i32
@@ -590,4 +592,4 @@ def kda_chunk_fwd_noalloc(q, k, v, g, beta, *, o, final_state=None, cu_seqlens=N
 
 from ._hybrid import (KDA_QUANT_BLOCK, KDA_QUANT_NONE, KDA_QUANT_ROW, kda_latent_cache_write,  # noqa: E402,F401
                       kda_latent_decode, kda_latent_decode_workspace_bytes, kda_latent_prefill,
-                      kda_page_tables, kda_rms_norm)
+                      kda_latent_prefill_workspace_bytes, kda_page_tables, kda_rms_norm, PREFILL_SPLIT_KEYS)

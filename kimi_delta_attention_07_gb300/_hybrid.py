@@ -15,6 +15,7 @@ import kimi_delta_attention_07_gb300 as _core
 KDA_QUANT_NONE, KDA_QUANT_ROW, KDA_QUANT_BLOCK = range(3)
 KDA_BF16 = _core.KDA_BF16
 LATENT_DIM, ROPE_DIM, LATENT_ROW, NOPE_DIM, VALUE_DIM = 512, 64, 576, 128, 128
+PREFILL_SPLIT_KEYS = 1024  # KDA_LATENT_PREFILL_SPLIT_KEYS
 _QUANT = {"none": KDA_QUANT_NONE, None: KDA_QUANT_NONE, "row": KDA_QUANT_ROW, "block": KDA_QUANT_BLOCK}
 _bf16, _f32, _i32, _u8, _e4m3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
                                  torch.float8_e4m3fn)
@@ -236,15 +237,20 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, scale=None, o=None, ls
     return o
 
 
+def kda_latent_prefill_workspace_bytes(n_seqs: int, total_q: int, total_k: int, H: int) -> int:
+    return int((_lib or _library()).kda_latent_prefill_workspace_bytes(n_seqs, total_q, total_k, H))
+
+
 def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal=True, scale=None, o=None,
-                       lse=None, stream=None):
+                       lse=None, workspace=None, stream=None):
     """Expanded latent attention over packed sequences.
 
     q [Tq, H, 192] bf16; kv [Tk, H, 256] bf16 (a head's key part, then its
     value); k_rope [Tk, 64] bf16, shared by the heads; the token strides of the
     three are free.  cu_seqlens_q / cu_seqlens_k int32 [N+1] (k None: the same
     as q).  causal: query i of lq sees keys j <= i + lk - lq.  scale defaults to
-    192 ** -0.5.  lse, if given, is fp32 [Tq, H].  Returns o [Tq, H, 128].
+    192 ** -0.5.  lse, if given, is fp32 [Tq, H].  workspace is allocated where one
+    is needed, unless given (kda_latent_prefill_workspace_bytes).  Returns o [Tq, H, 128].
     """
     dev = q.get_device()
     if q.dim() != 3 or kv.dim() != 3:
@@ -264,10 +270,20 @@ def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal
         o = new_o = torch.empty((Tq, H, VALUE_DIM), dtype=_bf16, device=q.device)
     po = _need(o, "o", _bf16, (Tq, H, VALUE_DIM), dev)
     ple = None if lse is None else _need(lse, "lse", _f32, (Tq, H), dev)
-    st = (_lib or _library()).kda_latent_prefill(
+    lib = _lib or _library()
+    pw, ws, new_w = None, 0, None
+    if workspace is not None:
+        ws = workspace.numel()
+        pw = _need(workspace, "workspace", _u8, (ws,), dev)
+    elif Tk >= PREFILL_SPLIT_KEYS:
+        ws = lib.kda_latent_prefill_workspace_bytes(n, Tq, Tk, H)
+        if ws:
+            new_w = torch.empty(ws, dtype=_u8, device=q.device)
+            pw = new_w.data_ptr()
+    st = lib.kda_latent_prefill(
         pq, sq, pk, sk, pr, sr, po, ple, pcq, pck, n, Tq, Tk, H, 1 if causal else 0,
-        192 ** -0.5 if scale is None else scale,
-        _current_stream(dev) if stream is None else _stream_of(stream, new_o))
+        192 ** -0.5 if scale is None else scale, pw, ws,
+        _current_stream(dev) if stream is None else _stream_of(stream, new_o, new_w))
     if st:
         raise _core.KdaError(st, "kda_latent_prefill")
     return o

@@ -100,7 +100,9 @@ struct LatentPrefillArgs {
     int64_t total_q, total_k;
     int H, causal;
     float scale;
+    void *workspace;
 };
+size_t latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t total_k, int H);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t stream);
 
 }  // namespace kda

@@ -126,11 +126,18 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
     return launched([&] { return launch_latent_decode(a, (cudaStream_t)stream); });
 }
 
+size_t kda_latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t total_k, int H) {
+    if (n_seqs <= 0 || H <= 0 || H > 65535 || n_seqs > 65535 || total_q < 0 || total_q > INT32_MAX || total_k < 0 ||
+        total_k > INT32_MAX)
+        return 0;
+    return latent_prefill_workspace_bytes(n_seqs, total_q, total_k, H);
+}
+
 int kda_latent_prefill(const void *q, int64_t q_stride, const void *kv, int64_t kv_stride,
                        const void *k_rope, int64_t rope_stride, void *o, float *lse,
                        const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int n_seqs,
-                       int64_t total_q, int64_t total_k, int H, int causal, float scale,
-                       void *stream) {
+                       int64_t total_q, int64_t total_k, int H, int causal, float scale, void *workspace,
+                       size_t workspace_bytes, void *stream) {
     if (n_seqs <= 0 || H <= 0 || total_q < 0 || total_q > INT32_MAX || total_k < 0 ||
         total_k > INT32_MAX || !isfinite(scale) || q_stride < (int64_t)kQk * H || q_stride % 8 != 0 ||
         kv_stride < (int64_t)kKvRow * H || kv_stride % 8 != 0 || rope_stride < kRope ||
@@ -143,11 +150,13 @@ int kda_latent_prefill(const void *q, int64_t q_stride, const void *kv, int64_t 
         !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4))
         return KDA_ERR_INVALID_ARG;
     if (!cu_seqlens_k && total_k != total_q) return KDA_ERR_INVALID_ARG;
+    const size_t need = latent_prefill_workspace_bytes(n_seqs, total_q, total_k, H);
+    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     const LatentPrefillArgs a{(const __nv_bfloat16 *)q, (const __nv_bfloat16 *)kv,
                               (const __nv_bfloat16 *)k_rope, q_stride, kv_stride, rope_stride,
                               (__nv_bfloat16 *)o, lse, cu_seqlens_q,
                               cu_seqlens_k ? cu_seqlens_k : cu_seqlens_q, n_seqs, total_q, total_k,
-                              H, causal != 0, scale};
+                              H, causal != 0, scale, workspace};
     return launched([&] { return launch_latent_prefill(a, (cudaStream_t)stream); });
 }
 

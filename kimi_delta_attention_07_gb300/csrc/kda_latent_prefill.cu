@@ -36,6 +36,11 @@
 // sequence's end become 0, and so do values that are not finite; the epilogue
 // then adds those to the rows that see them.
 //
+// Few queries behind many keys (a chunk of a prompt behind its cached part) would leave
+// most SMs idle: the keys of a block of queries are then split into parts of whole
+// steps, each an item whose (O, max, sum) goes to the workspace, and a second,
+// dependent kernel joins them in order.
+//
 // CTAs ask for work with cluster launch control: the grid has a CTA per 256
 // queries and head, heaviest first within a sequence, and a running CTA takes
 // over the next unlaunched one, so that its loads overlap the last epilogue.
@@ -58,6 +63,8 @@ constexpr int kItem = 2 * kTile;     // queries per CTA
 constexpr int kThreads = 640;
 constexpr int kRing = 8;             // 16 KB blocks
 constexpr uint32_t kBlock = kTile * 128;
+constexpr int kSplitSteps = KDA_LATENT_PREFILL_SPLIT_KEYS / kTile;  // items of fewer are not split
+constexpr int kMinSteps = 2;         // of a part, where an item's keys are split
 constexpr float kRaise = 8.0f;       // log2 by which a score may pass its row's reference
 
 // shared memory (from a 1024-byte boundary)
@@ -78,22 +85,43 @@ struct Item {
     __device__ __forceinline__ int most() const { return max(steps0, steps1); }
 };
 
+struct SplitItem : Item {
+    int part;  // of an item whose keys are split: its place in the workspace; else -1
+};
+
+template <typename ITEM>
 struct Shared {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[2], q_empty[2], x_full[2], p_full[2][2], o_full[2], o_empty[2],
         unchecked[2][2], item_full[2], item_empty[2], next_full;
     uint4 next_answer;
-    Item items[3];            // two handed out in turn; [2]: claimed, not handed out yet
+    ITEM items[3];            // two handed out in turn; [2]: claimed, not handed out yet
     float half[2][2][kTile];  // what the two threads of a row exchange
     int piece[kPieces];       // blocks of 256 queries of the sequences before each piece
     int warp_total[kPieces / 32];
     volatile int dead, odd[2];
     uint32_t tmem_base;
 };
-constexpr uint32_t kSmemBytes = kSmShared + sizeof(Shared);
+constexpr uint32_t kSmemBytes = kSmShared + sizeof(Shared<SplitItem>);
 static_assert(kSmemBytes <= 232448, "shared memory");
+
+struct Stat {  // of a row's part: reference (log2), sum
+    float m, l;
+};
+struct Join {  // an item whose keys are split: first token, rows, parts (0: nothing to join)
+    int32_t q, rows, parts, pad;
+};
+struct Part {
+    float o[kItem][kHeadDim];  // not divided by the sum
+};
 
 struct PrefillParams {
     LatentPrefillArgs a;
+};
+struct SplitParams : PrefillParams {
+    int splits;   // most parts of an item
+    Part *parts;  // [CTA of the grid]
+    Stat *stats;  // [CTA of the grid][kItem]
+    Join *joins;  // [block of queries][H]
 };
 
 __device__ __forceinline__ int blocks_of(const LatentPrefillArgs &a, int n) {
@@ -102,14 +130,18 @@ __device__ __forceinline__ int blocks_of(const LatentPrefillArgs &a, int n) {
     return ok ? (qb - qa + kItem - 1) / kItem : 0;
 }
 
-// POSITIVE: scale > 0, so that the largest product is the largest score
-template <bool POSITIVE>
+// POSITIVE: scale > 0, so that the largest product is the largest score.  SPLIT: the keys of an item
+// may be split (types of its own, because the other kernel's registers are so short that a
+// member more in its item takes it from 123 to 139 us).
+template <bool POSITIVE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv,
-                          const __grid_constant__ CUtensorMap map_r, const PrefillParams p) {
+                          const __grid_constant__ CUtensorMap map_r,
+                          const std::conditional_t<SPLIT, SplitParams, PrefillParams> p) {
+    using ITEM = std::conditional_t<SPLIT, SplitItem, Item>;
     // all shared memory is dynamic, so that it begins on a 1024-byte boundary
     extern __shared__ __align__(1024) uint8_t sm[];
-    Shared &sh = *reinterpret_cast<Shared *>(sm + kSmShared);
+    auto &sh = *reinterpret_cast<Shared<ITEM> *>(sm + kSmShared);
     auto &k_full = sh.k_full, &k_empty = sh.k_empty, &v_full = sh.v_full, &v_empty = sh.v_empty;
     auto &q_full = sh.q_full, &q_empty = sh.q_empty, &x_full = sh.x_full, &o_full = sh.o_full, &o_empty = sh.o_empty,
          &item_full = sh.item_full, &item_empty = sh.item_empty;
@@ -136,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (wid == 17) tmem_alloc(&sh.tmem_base, 512);
     griddep_wait();
-    griddep_launch_dependents();
+    if (!SPLIT) griddep_launch_dependents();  // (a join's CTAs would take registers that ours need)
     // the blocks of 256 queries of the sequences before each thread's piece
     const int per = (a.n_seqs + kPieces - 1) / kPieces;
     int upto = 0, own = 0;
@@ -166,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!dead && !mbar_wait(bar, parity)) dead = 1;
     };
     // the it-th item of this CTA, as the scheduling thread published it
-    auto item_of = [&](int it) -> const Item & {
+    auto item_of = [&](int it) -> const ITEM & {
         wait(&item_full[it & 1], (it >> 1) & 1);
         return sh.items[it & 1];
     };
@@ -178,8 +210,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0, qn[2] = {0, 0};  // items published; queries' tiles loaded
             uint32_t step = 0, checks = 0, asked = 0;  // steps loaded; those whose values are checked
             // the item of a CTA of the grid; false if there is none (the grid is an upper bound)
-            auto item_of_cta = [&](int cta, Item &s) {
-                const int rank = cta / a.H;
+            auto item_of_cta = [&](int cta, ITEM &s) {
+                int rank = cta / a.H, split = 0;
+                s.h = cta - rank * a.H;
+                Join *join = nullptr;
+                if constexpr (SPLIT) {
+                    split = rank % p.splits, rank /= p.splits;
+                    if (split == 0) join = p.joins + rank * a.H + s.h;
+                }
                 // the piece that holds block `rank`, then the sequence in it
                 int lo = 0, hi = kPieces;
                 while (lo + 1 < hi) {
@@ -193,8 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     before += blocks;
                     blocks = 0;
                 }
-                if (blocks == 0) return false;
-                s.h = cta - rank * a.H;
+                if (blocks == 0) {
+                    if (join) join->parts = 0;
+                    return false;
+                }
                 s.qa = a.cu_q[n];
                 s.ka = a.cu_k[n];
                 s.lq = a.cu_q[n + 1] - s.qa;
@@ -211,6 +251,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 s.masked = first / kTile;
                 s.valid = 1;
+                if constexpr (SPLIT) {
+                    // parts of equal length, each a sequence of its own whose keys begin at its first step
+                    const int most = s.most(), parts = most < kSplitSteps ? 1 : min(p.splits, (most + kMinSteps - 1) / kMinSteps);
+                    if (join) *join = {s.qa + s.q0, min(s.lq - s.q0, kItem), parts > 1 ? parts : 0, 0};
+                    if (split >= parts) return false;
+                    const int base = most / parts, rem = most - base * parts;
+                    const int k0 = split * base + min(split, rem), len = base + (split < rem);
+                    s.ka += k0 * kTile, s.lk -= k0 * kTile, s.off -= k0 * kTile;
+                    s.steps0 = min(max(s.steps0 - k0, 0), len), s.steps1 = min(max(s.steps1 - k0, 0), len);
+                    s.masked = max(s.masked - k0, 0);
+                    s.part = parts > 1 ? cta : -1;
+                }
                 return true;
             };
             auto ask = [&] {
@@ -218,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next_cta_request(&sh.next_answer, &sh.next_full);
             };
             // the next item that the answers name; false once there is none
-            auto next_item = [&](Item &s) {
+            auto next_item = [&](ITEM &s) {
                 for (;;) {
                     // (also when another wait has given up: a CTA that was handed over is this one's to answer for)
                     if (!mbar_wait(&sh.next_full, asked++ & 1)) {
@@ -232,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ask();
                 }
             };
-            Item cur, next;
+            ITEM cur, next;
             bool more = item_of_cta(blockIdx.x, cur);
             if (!more) {
                 ask();
@@ -432,7 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *mine = &sh.half[t][half][quad * 32 + lane], *other = &sh.half[t][half ^ 1][quad * 32 + lane];
         int xn = 0, on = 0;
         for (int it = 0;; ++it) {
-            const Item s = item_of(it);
+            std::conditional_t<SPLIT, const ITEM &, const ITEM> s = item_of(it);
+            bool split = false;
+            if constexpr (SPLIT) split = s.part >= 0;
             if (!named_bar_and(1 + t, 256, !dead && s.valid)) break;
             const int row = s.q0 + t * kTile + quad * 32 + lane;
             const bool real = row < s.lq;
@@ -530,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (__any_sync(0xffffffffu, add)) {
                     // values that were taken out of V because they are not finite
-                    for (int key = s.masked * kTile; key < limit; ++key) {
+                    for (int key = s.masked * kTile; key < (SPLIT ? min(limit, steps * kTile) : limit); ++key) {
                         const __nv_bfloat16 *v = a.kv + (int64_t)(s.ka + key) * a.kv_stride +
                                                  (int64_t)s.h * kKvRow + kNope + 64 * half + 32 * k;
 #pragma unroll
@@ -540,6 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     __syncwarp();
+                }
+                if constexpr (SPLIT) {
+                    if (split && real) {
+                        const int place = t * kTile + quad * 32 + lane;
+                        float4 *dst = (float4 *)(p.parts[s.part].o[place] + 64 * half + 32 * k);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        if (half == 0 && k == 0)
+                            p.stats[(int64_t)s.part * kItem + place] = {gave_up ? NAN : m * scale2, gave_up ? NAN : l};
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 16; ++j) w[4 * k + (j >> 2)][j & 3] = pack2(o[2 * j] * inv, o[2 * j + 1] * inv);
@@ -562,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (up) w[u][j] = got; else w[u | o][j] = got;
                         }
             }
-            {
+            if (!split) {
                 const int first = s.q0 + t * kTile + quad * 32 + (lane & ~7);
                 __nv_bfloat16 *dst = a.o + ((int64_t)(s.qa + first) * a.H + s.h) * kHeadDim + 64 * half + 8 * (lane & 7);
 #pragma unroll
@@ -570,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (first + r < s.lq)
                         *(uint4 *)(dst + (int64_t)r * a.H * kHeadDim) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
             }
-            if (real && a.lse && half == 0)
+            if (real && a.lse && half == 0 && !split)
                 a.lse[out] = gave_up ? NAN : l == 0.0f ? -INFINITY : (m * scale2 + log2_sfu(l)) * kLn2;
             __syncwarp();
             if (lane == 0) item_done(it);
@@ -583,13 +647,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A wait gave up: what this CTA had in hand becomes NaN, and copies still in flight land before
         // its memory is given up.
         for (int i = 0; i < 3; ++i) {
-            const Item &s = sh.items[i];
+            const ITEM &s = sh.items[i];
             if (!s.valid) continue;
             const int rows = min(s.lq - s.q0, kItem);
             for (int j = tid; j < rows * kHeadDim; j += kThreads) {
                 const int64_t out = (int64_t)(s.qa + s.q0 + j / kHeadDim) * a.H + s.h;
                 a.o[out * kHeadDim + j % kHeadDim] = __float2bfloat16_rn(NAN);
                 if (a.lse && j % kHeadDim == 0) a.lse[out] = NAN;
+                if constexpr (SPLIT)
+                    if (s.part >= 0 && j % kHeadDim == 0) p.stats[(int64_t)s.part * kItem + j / kHeadDim] = {NAN, NAN};
             }
         }
         const long long t0 = clock64();
@@ -598,7 +664,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (wid == 17) tmem_dealloc(tmem, 512);
 }
 
+// Joins the parts of an item whose keys were split, in their order: a warp per query row, four channels a lane.
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32, kMaxSplits = 160;
+__global__ void __launch_bounds__(kJoinThreads) latent_prefill_join_kernel(const SplitParams p) {
+    __shared__ float weights[kJoinRows][kMaxSplits];
+    griddep_wait();
+    griddep_launch_dependents();
+    const LatentPrefillArgs &a = p.a;
+    const Join j = p.joins[blockIdx.y];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, row = blockIdx.x * kJoinRows + wid;
+    const int rank = blockIdx.y / a.H, h = blockIdx.y - rank * a.H;
+    if (row >= j.rows || j.parts <= 0) return;
+    // (the record of an item that no CTA could take is whatever the workspace held)
+    if (j.rows > kItem || j.parts > p.splits || j.q < 0 || j.q >= a.total_q - row) return;
+    auto slot = [&](int i) { return ((int64_t)rank * p.splits + i) * a.H + h; };
+    // a part that saw nothing has no reference, and its sum is 0; NaN (which fmaxf skips) has a weight of NaN
+    float top = -INFINITY, l = 0.0f;
+    for (int i = lane; i < j.parts; i += 32) top = fmaxf(top, p.stats[slot(i) * kItem + row].m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = lane; i < j.parts; i += 32) {
+        const Stat s = p.stats[slot(i) * kItem + row];
+        const float w = s.m == -INFINITY ? 0.0f : exp2_sfu(s.m - top);
+        weights[wid][i] = w;
+        l += w * s.l;
+    }
+    l = warp_sum(l);
+    __syncwarp();
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = 0; i < j.parts; ++i) {
+        const float4 u = *(const float4 *)(p.parts[slot(i)].o[row] + 4 * lane);
+        const float w = weights[wid][i];
+        o.x += w * u.x, o.y += w * u.y, o.z += w * u.z, o.w += w * u.w;
+    }
+    const float inv = l == 0.0f ? 1.0f : 1.0f / l;
+    const int64_t out = (int64_t)(j.q + row) * a.H + h;
+    *(uint2 *)(a.o + out * kHeadDim + 4 * lane) = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (top + log2_sfu(l)) * kLn2;
+}
+
+// Blocks of queries at most: a sequence's last one may hold a single query.
+inline int64_t block_bound(int n_seqs, int64_t total_q) {
+    return (total_q + (kItem - 1) * std::min<int64_t>(n_seqs, total_q)) / kItem;
+}
+
+// Parts that an item's keys are split into at most, from what the host knows: the waves of parts times
+// their steps, to which a part's start and outputs add about three and the join five.  8 heads, 64
+// queries and 2112 keys: 36 us whole, 15 us split; 16 heads, 512 queries behind 32768 keys: 421 and
+// 139 us; 1 head, 512 behind 65536: 820 and 42 us.  1024 queries and keys of 8 heads, which the
+// rule leaves whole: 20.8 and 21.9 us.
+inline int splits_for(int n_seqs, int64_t total_q, int64_t total_k, int H) {
+    const int64_t items = block_bound(n_seqs, total_q) * H, steps = (total_k / n_seqs + kTile - 1) / kTile;
+    const int sms = sm_count();
+    if (items == 0 || items > 2 * sms || steps < kSplitSteps) return 1;
+    const int64_t most = std::min<int64_t>({4 * sms / items, (steps + kMinSteps - 1) / kMinSteps, kMaxSplits});
+    int best = 1;
+    double least = 0.85 * ((items + sms - 1) / sms) * (steps + 3.0);
+    for (int n = 2; n <= most; ++n) {
+        const double cost = (double)((items * n + sms - 1) / sms) * ((double)steps / n + 3.0) + 5.0;
+        if (cost < least) best = n, least = cost;
+    }
+    return best;
+}
+
+struct Layout {
+    size_t joins, stats, parts, total;
+};
+inline Layout layout(int64_t items, int splits) {
+    Layout l;
+    l.joins = 0;
+    l.stats = align_up((size_t)items * sizeof(Join), 256);
+    l.parts = l.stats + align_up((size_t)items * splits * kItem * sizeof(Stat), 256);
+    l.total = l.parts + (size_t)items * splits * sizeof(Part);
+    return l;
+}
+
 }  // namespace
+
+size_t latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t total_k, int H) {
+    const int splits = splits_for(n_seqs, total_q, total_k, H);
+    return splits == 1 ? 0 : layout(block_bound(n_seqs, total_q) * H, splits).total;
+}
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t stream) {
     CUtensorMap map_q, map_kv, map_r;
@@ -610,15 +757,28 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t strea
     } else {
         map_kv = map_r = map_q;  // no key: not used
     }
-    auto kernel = a.scale > 0.0f ? latent_prefill_kernel<true> : latent_prefill_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemBytes);
-    if (e != cudaSuccess) return e;
-    // every sequence adds at most one incomplete block
-    const int64_t blocks = a.total_q / kItem + std::min<int64_t>(a.n_seqs, a.total_q);
-    if (blocks * a.H > INT32_MAX) return cudaErrorInvalidValue;
-    e = launch_dependent(kernel, dim3((unsigned)(blocks * a.H)), dim3(kThreads), kSmemBytes, stream, map_q, map_kv, map_r,
-                         PrefillParams{a});
+    const int64_t items = block_bound(a.n_seqs, a.total_q) * a.H;
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    const int splits = splits_for(a.n_seqs, a.total_q, a.total_k, a.H);
+    auto launch = [&](auto kernel, const auto &p) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        return e != cudaSuccess ? e
+                                : launch_dependent(kernel, dim3((unsigned)(items * splits)), dim3(kThreads), kSmemBytes, stream,
+                                                   map_q, map_kv, map_r, p);
+    };
+    cudaError_t e;
+    if (splits == 1) {
+        const PrefillParams p{a};
+        e = a.scale > 0.0f ? launch(latent_prefill_kernel<true, false>, p) : launch(latent_prefill_kernel<false, false>, p);
+    } else {
+        const Layout l = layout(items, splits);
+        uint8_t *ws = (uint8_t *)a.workspace;
+        const SplitParams p{{a}, splits, (Part *)(ws + l.parts), (Stat *)(ws + l.stats), (Join *)(ws + l.joins)};
+        e = a.scale > 0.0f ? launch(latent_prefill_kernel<true, true>, p) : launch(latent_prefill_kernel<false, true>, p);
+        if (e == cudaSuccess)
+            e = launch_dependent(latent_prefill_join_kernel, dim3(kItem / kJoinRows, (unsigned)items), dim3(kJoinThreads), 0,
+                                 stream, p);
+    }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -122,9 +122,9 @@ def test_decode_other_statuses(lib):
 
 def _prefill(lib, **kw):
     order = ("q", "sq", "kv", "sk", "rope", "sr", "o", "lse", "cq", "ck", "n", "Tq", "Tk", "H", "causal", "scale",
-             "stream")
+             "ws", "ws_bytes", "stream")
     d = dict.fromkeys(order, BASE)
-    d.update(sq=768, sk=1024, sr=64, lse=None, n=2, Tq=16, Tk=32, H=4, causal=1, scale=0.1, stream=None)
+    d.update(ws=None, ws_bytes=0, sq=768, sk=1024, sr=64, lse=None, n=2, Tq=16, Tk=32, H=4, causal=1, scale=0.1, stream=None)
     return _call(lib.kda_latent_prefill, order, d, kw)
 
 
@@ -135,6 +135,19 @@ def _prefill(lib, **kw):
                                 dict(o=BASE + 8), dict(lse=BASE + 1)])
 def test_prefill_refuses(lib, kw):
     assert _prefill(lib, **kw) == INVALID
+
+
+def test_prefill_workspace(lib):
+    # few queries behind many keys: the keys are split; enough queries, or few keys: they are not
+    need = kda.kda_latent_prefill_workspace_bytes(1, 64, 65536, 4)
+    assert need > 4 * 64 * 132 * 4
+    assert kda.kda_latent_prefill_workspace_bytes(1, 64, kda.PREFILL_SPLIT_KEYS - 1, 4) == 0
+    assert kda.kda_latent_prefill_workspace_bytes(1, 65536, 65536, 32) == 0
+    for bad in ((0, 64, 65536, 4), (1, -1, 65536, 4), (1, 64, -1, 4), (1, 64, 65536, 0), (1, 64, 65536, 65536)):
+        assert kda.kda_latent_prefill_workspace_bytes(*bad) == 0
+    few = dict(n=1, Tq=64, Tk=65536)
+    for ws, size in ((None, need), (BASE, need - 1), (BASE + 128, need)):
+        assert _prefill(lib, ws=ws, ws_bytes=size, **few) == WORKSPACE
 
 
 def test_prefill_nothing_to_do(lib):

@@ -637,6 +637,59 @@ def test_prefill_other_stream_and_repeats(kda):
     assert torch.equal(o, other)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens_q,lens_k,H", [([64], [1500], 3), ([1], [2049], 1), ([300], [5000], 2), ([100, 1, 260], [1400, 2000, 1100], 2),
+                                             ([5, 0, 9], [4000, 3000, 3], 4), ([700], [1100], 1), ([400], [65], 1)])
+def test_prefill_few_queries_split_their_keys(kda, lens_q, lens_k, H, causal):
+    case = prefill_case(lens_q, lens_k, H, 31, slack=sum(lens_k) % 7 + 1)
+    need = kda.kda_latent_prefill_workspace_bytes(len(lens_q), case[0].shape[0], case[1].shape[0], H)
+    assert (need > 0) == (sum(lens_k) > 1000)
+    o, lse = check_prefill(kda, case, causal)
+    ws = torch.full((need + 8,), 255, dtype=torch.uint8, device="cuda")   # NaN wherever it is read before it is written
+    again, lse2 = check_prefill(kda, case, causal, workspace=ws)
+    assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
+def test_prefill_split_keys_not_finite(kda):
+    q, kv, rope, cq, ck = prefill_case([200, 30], [2000, 1700], 2, 33)
+    run = lambda: kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck)  # noqa: E731
+    assert kda.kda_latent_prefill_workspace_bytes(2, 230, 3700, 2) > 0
+    clean = run()
+    kv[1900, 1, 130] = INF                                               # seen by query 100 of sequence 0 and later ones
+    kv[1999, 0, 128] = NAN                                               # by its last one
+    kv[2000 + 1690, 0, 140] = NAN                                        # by query 20 of sequence 1 and later ones
+    q[50, 1, 3] = NAN
+    o = run()
+    want = clean.clone()
+    want[100:200, 1, 2] = INF
+    want[199, 0, 0] = NAN
+    want[220:, 0, 12] = NAN
+    want[50, 1] = NAN
+    assert torch.equal(o.nan_to_num(7.0, 8.0), want.nan_to_num(7.0, 8.0))
+    q[199] = INF                                                         # scores of +-inf and NaN: one row of either head
+    o2 = run()
+    assert torch.equal(o2[:199].nan_to_num(7.0, 8.0), o[:199].nan_to_num(7.0, 8.0))
+
+
+def test_prefill_split_keys_in_a_graph_and_on_another_stream(kda):
+    q, kv, rope, cq, ck = prefill_case([90], [3000], 2, 35)
+    eager = kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck, stream=s)
+    s.synchronize()
+    assert torch.equal(other, eager)
+    o = torch.empty_like(eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck, o=o)
+    for keys in (3000, 1, 700):
+        ck[1] = keys
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck))
+
+
 def test_prefill_past_32_bits(kda):
     # the second sequence's keys lie past 2^31 elements of kv, its queries behind an empty sequence
     H, first, lk = 32, 2 ** 31 // (32 * 256) + 500, 300
