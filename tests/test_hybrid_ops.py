@@ -638,6 +638,30 @@ def test_prefill_other_stream_and_repeats(kda):
 
 
 @pytest.mark.parametrize("causal", [True, False])
+def test_prefill_many_short_sequences(kda, causal):
+    # more blocks of queries than the GPU runs at once, most of at most 128 queries (which take either half of a block)
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 129, (90,), generator=g).tolist()
+    lens[7], lens[40], lens[41] = 257, 128, 129
+    keys = [n + int(p) for n, p in zip(lens, torch.randint(0, 200, (90,), generator=g))]
+    keys[3], keys[4] = 0, 1
+    case = prefill_case(lens, keys, 8, 41, slack=3)
+    o, _ = check_prefill(kda, case, causal)
+    q, kv, rope, cq, ck = case
+    starts = cq.tolist()
+    b = next(i for i in range(50, 90) if lens[i] > 3 and keys[i] >= lens[i])
+    kv[ck[b + 1] - 2, 5, 200] = INF                                      # seen by the last two queries (or all)
+    cq = cq.clone()
+    cq[20] = -1                                                          # sequences 19 and 20: not written
+    again = torch.full_like(o, 7.0)
+    kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck, causal=causal, o=again)
+    want = o.clone()
+    want[starts[19]:starts[21]] = 7.0
+    want[starts[b + 1] - 2 if causal else starts[b]:starts[b + 1], 5, 72] = INF
+    assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("lens_q,lens_k,H", [([64], [1500], 3), ([1], [2049], 1), ([300], [5000], 2), ([100, 1, 260], [1400, 2000, 1100], 2),
                                              ([5, 0, 9], [4000, 3000, 3], 4), ([700], [1100], 1), ([400], [65], 1)])
 def test_prefill_few_queries_split_their_keys(kda, lens_q, lens_k, H, causal):
