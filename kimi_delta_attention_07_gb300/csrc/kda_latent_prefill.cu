@@ -119,7 +119,7 @@ struct PrefillParams {
     LatentPrefillArgs a;
 };
 struct SplitParams : PrefillParams {
-    int splits;   // most parts of an item
+    int splits, blocks;  // most parts of an item; blocks of queries, of which there are at most so many
     Part *parts;  // [CTA of the grid]
     Stat *stats;  // [CTA of the grid][kItem]
     Join *joins;  // [block of queries][H]
@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s.h = cta - rank * a.H;
                 Join *join = nullptr;
                 if constexpr (SPLIT) {
-                    split = rank % p.splits, rank /= p.splits;
+                    // (blocks inside parts, so that the blocks of a head read the same keys at the same time)
+                    split = rank / p.blocks, rank -= split * p.blocks;
                     if (split == 0) join = p.joins + rank * a.H + s.h;
                 }
                 // the piece that holds block `rank`, then the sequence in it
@@ -686,7 +687,8 @@ __global__ void __launch_bounds__(kJoinThreads) latent_prefill_join_kernel(const
     if (row >= j.rows || j.parts <= 0) return;
     // (the record of an item that no CTA could take is whatever the workspace held)
     if (j.rows > kItem || j.parts > p.splits || j.q < 0 || j.q >= a.total_q - row) return;
-    auto slot = [&](int i) { return ((int64_t)rank * p.splits + i) * a.H + h; };
+    const int first = rank * a.H + h, step = p.blocks * a.H;  // places of the item's parts
+    auto slot = [&](int i) { return (int64_t)(first + i * step); };
     // a part that saw nothing has no reference, and its sum is 0; NaN (which fmaxf skips) has a weight of NaN
     float top = -INFINITY, l = 0.0f;
     for (int i = lane; i < j.parts; i += 32) top = fmaxf(top, p.stats[slot(i) * kItem + row].m);
@@ -701,9 +703,10 @@ __global__ void __launch_bounds__(kJoinThreads) latent_prefill_join_kernel(const
     l = warp_sum(l);
     __syncwarp();
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float *src = p.parts[first].o[row] + 4 * lane;
 #pragma unroll 8
-    for (int i = 0; i < j.parts; ++i) {
-        const float4 u = *(const float4 *)(p.parts[slot(i)].o[row] + 4 * lane);
+    for (int i = 0; i < j.parts; ++i, src += (int64_t)step * kItem * kHeadDim) {
+        const float4 u = *(const float4 *)src;
         const float w = weights[wid][i];
         o.x += w * u.x, o.y += w * u.y, o.z += w * u.z, o.w += w * u.w;
     }
@@ -721,7 +724,7 @@ inline int64_t block_bound(int n_seqs, int64_t total_q) {
 // Parts that an item's keys are split into at most, from what the host knows: the waves of parts times
 // their steps, to which a part's start and outputs add about three and the join five.  8 heads, 64
 // queries and 2112 keys: 36 us whole, 15 us split; 16 heads, 512 queries behind 32768 keys: 421 and
-// 139 us; 1 head, 512 behind 65536: 820 and 42 us.  1024 queries and keys of 8 heads, which the
+// 134 us; 1 head, 512 behind 65536: 820 and 42 us.  1024 queries and keys of 8 heads, which the
 // rule leaves whole: 20.8 and 21.9 us.
 inline int splits_for(int n_seqs, int64_t total_q, int64_t total_k, int H) {
     const int64_t items = block_bound(n_seqs, total_q) * H, steps = (total_k / n_seqs + kTile - 1) / kTile;
@@ -782,7 +785,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t strea
     } else {
         const Layout l = layout(items, splits);
         uint8_t *ws = (uint8_t *)a.workspace;
-        const SplitParams p{{a}, splits, (Part *)(ws + l.parts), (Stat *)(ws + l.stats), (Join *)(ws + l.joins)};
+        const SplitParams p{{a}, splits, (int)(items / a.H), (Part *)(ws + l.parts), (Stat *)(ws + l.stats), (Join *)(ws + l.joins)};
         e = a.scale > 0.0f ? launch(latent_prefill_kernel<true, true>, p) : launch(latent_prefill_kernel<false, true>, p);
         if (e == cudaSuccess)
             e = launch_dependent(latent_prefill_join_kernel, dim3(kItem / kJoinRows, (unsigned)items), dim3(kJoinThreads), 0,
