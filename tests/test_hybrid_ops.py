@@ -151,6 +151,20 @@ def test_page_tables_many_requests(kda, n):
     check_tables(kda, ctx, new, ids[k:], table, 32, 40 * n, sum(new) + 3)
 
 
+@pytest.mark.parametrize("n", [1024, 1025, 4097, 16384])
+def test_page_tables_many_requests_of_few_tokens(kda, n):
+    r = torch.Generator().manual_seed(n)
+    ctx = torch.randint(-1, 40, (n,), generator=r).tolist()
+    new = torch.randint(-1, 4, (n,), generator=r).tolist()
+    ids = torch.randperm(5 * n, generator=r).tolist()
+    table, k = [], 0
+    for c in ctx:
+        h = max(0, -(-c // 16))
+        table.append(ids[k:k + h] + [-1] * (4 - h))
+        k += h
+    check_tables(kda, ctx, new, ids[k:k + n // 10], table, 16, 5 * n, sum(v for v in new if v > 0) + 3)
+
+
 def test_page_tables_lengths_near_the_type_limit(kda):
     big = 2 ** 31 - 1
     t = i32([[1, 2]])
