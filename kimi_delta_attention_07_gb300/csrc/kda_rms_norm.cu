@@ -170,12 +170,16 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const RmsNormArgs
 template <typename T, int QUANT, int NV, bool WARP>
 cudaError_t launch(const RmsNormArgs &a, int threads, int rows_per_cta, cudaStream_t stream) {
     auto kern = rms_norm_kernel<T, QUANT, NV, WARP>;
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) {
-        cudaGetLastError();
-        per_sm = 1;
+    const int64_t want = (a.rows + rows_per_cta - 1) / rows_per_cta;
+    int64_t most = sm_count();
+    if (want > most) {  // (a query that few rows do without)
+        int per_sm = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess || per_sm < 1) {
+            cudaGetLastError();
+            per_sm = 1;
+        }
+        most *= per_sm;
     }
-    const int64_t want = (a.rows + rows_per_cta - 1) / rows_per_cta, most = (int64_t)sm_count() * per_sm;
     const cudaError_t e =
         launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), dim3(threads), 0, stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
