@@ -590,6 +590,6 @@ def kda_chunk_fwd_noalloc(q, k, v, g, beta, *, o, final_state=None, cu_seqlens=N
     return o, final_state
 
 
-from ._hybrid import (KDA_QUANT_BLOCK, KDA_QUANT_NONE, KDA_QUANT_ROW, kda_latent_cache_write,  # noqa: E402,F401
-                      kda_latent_decode, kda_latent_decode_workspace_bytes, kda_latent_prefill,
-                      kda_latent_prefill_workspace_bytes, kda_page_tables, kda_rms_norm, PREFILL_SPLIT_KEYS)
+from ._hybrid import (KDA_LATENT_PREFILL_SPLIT_KEYS, KDA_QUANT_BLOCK, KDA_QUANT_NONE, KDA_QUANT_ROW,  # noqa: E402,F401
+                      kda_latent_cache_write, kda_latent_decode, kda_latent_decode_workspace_bytes,
+                      kda_latent_prefill, kda_latent_prefill_workspace_bytes, kda_page_tables, kda_rms_norm)

@@ -15,7 +15,7 @@ import kimi_delta_attention_07_gb300 as _core
 KDA_QUANT_NONE, KDA_QUANT_ROW, KDA_QUANT_BLOCK = range(3)
 KDA_BF16 = _core.KDA_BF16
 LATENT_DIM, ROPE_DIM, LATENT_ROW, NOPE_DIM, VALUE_DIM = 512, 64, 576, 128, 128
-PREFILL_SPLIT_KEYS = 1024  # KDA_LATENT_PREFILL_SPLIT_KEYS
+KDA_LATENT_PREFILL_SPLIT_KEYS = 1024
 _QUANT = {"none": KDA_QUANT_NONE, None: KDA_QUANT_NONE, "row": KDA_QUANT_ROW, "block": KDA_QUANT_BLOCK}
 _bf16, _f32, _i32, _u8, _e4m3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
                                  torch.float8_e4m3fn)
@@ -275,7 +275,7 @@ def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal
     if workspace is not None:
         ws = workspace.numel()
         pw = _need(workspace, "workspace", _u8, (ws,), dev)
-    elif Tk >= PREFILL_SPLIT_KEYS:
+    elif Tk >= KDA_LATENT_PREFILL_SPLIT_KEYS:
         ws = lib.kda_latent_prefill_workspace_bytes(n, Tq, Tk, H)
         if ws:
             new_w = torch.empty(ws, dtype=_u8, device=q.device)

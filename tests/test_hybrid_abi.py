@@ -141,7 +141,7 @@ def test_prefill_workspace(lib):
     # few queries behind many keys: the keys are split; enough queries, or few keys: they are not
     need = kda.kda_latent_prefill_workspace_bytes(1, 64, 65536, 4)
     assert need > 4 * 64 * 132 * 4
-    assert kda.kda_latent_prefill_workspace_bytes(1, 64, kda.PREFILL_SPLIT_KEYS - 1, 4) == 0
+    assert kda.kda_latent_prefill_workspace_bytes(1, 64, kda.KDA_LATENT_PREFILL_SPLIT_KEYS - 1, 4) == 0
     assert kda.kda_latent_prefill_workspace_bytes(1, 65536, 65536, 32) == 0
     for bad in ((0, 64, 65536, 4), (1, -1, 65536, 4), (1, 64, -1, 4), (1, 64, 65536, 0), (1, 64, 65536, 65536)):
         assert kda.kda_latent_prefill_workspace_bytes(*bad) == 0
