@@ -558,21 +558,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 4; ++k) tmem_ld_wait_for(o[k]);
                 if (s.whole()) {
                     __nv_bfloat16 *dst = a.o + (row0 + c0) * kLatent + tid;
+                    float inv[8];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c0 + c < rows) {
-                            const float inv = sh_inv[c0 + c];
+                    for (int c = 0; c < 8; c += 4) *(float4 *)(inv + c) = *(const float4 *)(sh_inv + c0 + c);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) dst[c * kLatent + k * 128] = __float2bfloat16_rn(o[k][c] * inv);
-                        }
-                    }
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            if (c0 + c < rows) dst[c * kLatent + k * 128] = __float2bfloat16_rn(o[k][c] * inv[c]);
                 } else {
                     float *dst = &part->o[c0][tid];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c0 + c < rows)
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) dst[c * kLatent + k * 128] = o[k][c];
+                        for (int c = 0; c < 8; ++c)
+                            if (c0 + c < rows) dst[c * kLatent + k * 128] = o[k][c];
                 }
             }
             tc_fence_before();
