@@ -12,6 +12,10 @@ rounding is off by at most half a step, eps / 2 of its type):
   lse        e + 2^-16 (1 + |lse|)
 Whole numbers are equal.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -163,6 +167,23 @@ def test_page_tables_many_requests_of_few_tokens(kda, n):
         table.append(ids[k:k + h] + [-1] * (4 - h))
         k += h
     check_tables(kda, ctx, new, ids[k:k + n // 10], table, 16, 5 * n, sum(v for v in new if v > 0) + 3)
+
+
+def test_page_tables_request_counts_around_48_kb_of_shared_memory():
+    # in a process of its own: what a call with more requests raises stays raised for the calls after it
+    code = """
+import torch
+import kimi_delta_attention_07_gb300 as kda
+i32 = lambda v: v.to(torch.int32).cuda()
+for n in (4082, 4083, 4084, 4085, 4090, 4095, 4096):
+    t = i32(torch.full((n, 1), -1))
+    got = kda.kda_page_tables(i32(torch.zeros(n)), i32(torch.ones(n)), i32(torch.arange(n)), t, page_size=16, n_pages=n, max_tokens=n)
+    assert t[:, 0].tolist() == list(range(n)) and got[2].tolist() == list(range(0, 16 * n, 16)) and got[4].tolist() == [n, 0], n
+print("all right")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.stdout.strip() == "all right", run.stderr[-2000:]
 
 
 def test_page_tables_lengths_near_the_type_limit(kda):
