@@ -37,10 +37,10 @@
 // has read.  2 requests of 231k tokens in all, 64 rows: 64 us, 40 of them at 6.7
 // TB/s between the first tile's arrival and the last one's.
 //
-// Running maximum: rows keep a reference that is only raised (and O^T in TMEM
-// rescaled) when some score passes it by 2^8, which is decided by one vote a
-// tile; p is then at most 2^8, and p, its sum and O share the reference, so
-// that the quotient is unchanged.  Sums are fp32 per thread, joined at the end.
+// Running maximum: a row keeps a reference that is only raised (and its column of
+// O^T in TMEM rescaled) when one of its scores passes it by 2^8; whether any row's
+// did is decided by one vote a tile.  p is then at most 2^8, and p, its sum and O
+// share the reference, so that the quotient is unchanged.  Sums are fp32 per thread, joined at the end.
 //
 // Work split: the tiles of all requests, in order, are cut evenly into one
 // range per CTA (a persistent CTA per SM; query rows beyond 32, or 64 where much
@@ -381,9 +381,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float scale2 = a.scale * kLog2e;
         const int rows = min(kRows, a.S * a.H - rb * kRows);
         const int tok = 16 * wid + (lane >> 2), col = 2 * (lane & 3);
-        int limit[kCols];  // of the thread's rows: new token r / H sees positions below len - S + 1 + r / H
+        // of the thread's rows: new token r / H sees positions below len - S + 1 + r / H; rows past the request's
+        // (the next request's queries, whose scores nobody reads) see none of the last tiles
+        int limit[kCols];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) limit[c] = (rb * kRows + 8 * (c >> 1) + col + (c & 1)) / a.H - a.S + 1;
+        for (int c = 0; c < kCols; ++c) {
+            const int r = 8 * (c >> 1) + col + (c & 1);
+            limit[c] = r < rows ? (rb * kRows + r) / a.H - a.S + 1 : INT32_MIN / 2;
+        }
         int at = range_begin, slot = 0, t = 0;
         bool gave_up = false;  // the same in all four warps: decided by their votes
         while (!gave_up && walk.next(s)) {
@@ -452,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         gave_up = true;
                         break;
                     }
-                    // raise every row's reference to its maximum so far
+                    // The rows that passed their reference take their maximum so far.  The others keep theirs, so that
+                    // a row's rounding follows from its own scores, whatever the rows beside it hold.
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) {
                         const int j = (c >> 1) * 4 + (c & 1);
@@ -466,8 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kCols; ++c) {
                         const int r = 8 * (c >> 1) + col + (c & 1);
                         const float top = fmaxf(fmaxf(fmaxf(sh_col[0][r], sh_col[1][r]), fmaxf(sh_col[2][r], sh_col[3][r])), m[c]);
-                        const float f = top == -INFINITY ? 1.0f : exp2_sfu(m[c] - top);
-                        m[c] = top;
+                        const bool up = top - m[c] > kRaise;  // (not where both are -inf)
+                        const float f = up ? exp2_sfu(m[c] - top) : 1.0f;
+                        if (up) m[c] = top;
                         l[c] *= f;
                         if (wid == 0 && lane < 4) sh_row[r] = f;
                     }

@@ -504,6 +504,27 @@ def test_decode_many_rows_over_a_wide_table_not_finite(kda):
     assert o[2].isnan().all() and torch.equal(o[3], clean[3])
 
 
+@pytest.mark.parametrize("S,H,wide", [(1, 1, False), (1, 5, False), (1, 8, False), (2, 3, False), (1, 40, False), (1, 40, True), (3, 16, True)])
+def test_decode_rows_do_not_depend_on_what_lies_beside_them(kda, S, H, wide):
+    """Bit for bit: not on cache rows past the length, nor on another request's or another head's query.  Enough requests
+    that a CTA takes several tiles of each, where a score far above the first tile's raises the reference."""
+    case = decode_case([97 + 7 * b % 60 for b in range(500)], S, H, 64, 120, poison=False)
+    q, cache, table, lens = widened(case) if wide else case
+    plain = kda.kda_latent_decode(q, cache, table, lens)
+    held = torch.zeros(cache.shape[:2], dtype=torch.bool)
+    for row, length in zip(table.tolist(), lens.tolist()):
+        for p in range(length):
+            held[row[p // 64], p % 64] = True
+    other = torch.where(held.cuda()[..., None], cache, cache * 3e4)
+    assert torch.equal(kda.kda_latent_decode(q, other, table, lens), plain)
+    other = q.clone()
+    other[1::2] *= 50
+    assert torch.equal(kda.kda_latent_decode(other, cache, table, lens)[::2], plain[::2])
+    other = q.clone()
+    other[:, :, 0] *= 50
+    assert torch.equal(kda.kda_latent_decode(other, cache, table, lens)[:, :, 1:], plain[:, :, 1:])
+
+
 def test_decode_past_32_bits(kda):
     page, n_pages = 64, 2 ** 31 // (576 * 64) + 200
     cache = torch.empty((n_pages, page, 576), dtype=torch.bfloat16, device="cuda")
