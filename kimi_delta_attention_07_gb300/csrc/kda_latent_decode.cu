@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int piece[kThreads / 32], start_n, start_off, start_len;
     __shared__ float sh_col[4][kRows], sh_row[kRows];
     __shared__ __align__(16) float sh_inv[kRows];
-    __shared__ volatile int dead, lost;
+    __shared__ volatile int dead, lost, odd;
 
     const LatentDecodeArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&full_q, 1), mbar_init(&empty_q, 1), mbar_init(&o_empty, 128);
         fence_mbar_init();
-        dead = lost = 0;
+        dead = lost = odd = 0;
     }
     if (wid == 1) tmem_alloc(&tmem_base, C::kTmemCols);
     // (the join is not let in early: its CTAs would settle on the SMs that finish
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tid < 2 * kTile && pos0 + (tid >> 1) >= s.len - a.S + 1) {
                         // A place that some row does not see gets p = 0 there, and 0 times its values has to be 0:
                         // rows without a token (shared memory may hold anything) become 0, and so do values of
-                        // a new token that are not finite (rows that see it are NaN by their scores).
+                        // a new token that are not finite (given back in the end to the rows that see it).
                         const bool none = pos0 + (tid >> 1) >= s.len;
                         uint4 *r = (uint4 *)(sm + kSmTile + slot * kTileBytes + (tid >> 4) * kGroup +
                                              ((tid >> 1) & 7) * 128 + (tid & 1) * 4096);
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint32_t ones = 0;
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) ones |= exponent_of_ones(r[j ^ turn]);
+                                if (ones) odd = 1;
                                 for (int j = 0; ones && j < 8; ++j) r[j] = finite_or_zero(r[j]);
                             }
                         }
@@ -589,7 +590,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (tid == 0 && rb == 0 && a.n_seqs > p.ranges && (range >= ranges || s.whole() || s.tile0 > 0))
             p.joins[range] = {-1, 0, 0, 0};
-        if (!named_bar_and(1, 128, !dead)) {
+        const bool alive = named_bar_and(1, 128, !dead);
+        if (alive && odd) {
+            // A value that is not finite is NaN in its channel for every row that sees its token: by that row's
+            // scores where one is NaN or +inf, and by 0 times the value where it is -inf.  (The tiles have lost
+            // it; a thread writes the channels that it wrote above.)
+            Walk<kTile> w = again;
+#pragma unroll 1
+            while (w.next(s)) {
+                const int64_t row0 = (int64_t)s.n * a.S * a.H + rb * kRows;
+                Part<kRows> *part = (Part<kRows> *)p.parts + ((int64_t)range * p.row_blocks + rb) * 2 + (s.tile0 == 0 ? 1 : 0);
+                const int64_t begin = max((int64_t)s.tile0 * kTile, (int64_t)s.len - a.S + 1);
+                const int64_t end = min((int64_t)(s.tile0 + s.tiles) * kTile, (int64_t)s.len);
+                for (int64_t pos = begin; pos < end; ++pos) {
+                    const int id = a.block_table[(int64_t)s.n * a.max_pages + (pos >> a.page_shift)];
+                    if (id < 0 || id >= a.n_pages) continue;  // (the whole request is NaN)
+                    const __nv_bfloat16 *token =
+                        a.cache + (((int64_t)id << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * kLatentRow;
+                    const int first = max((int)(pos - s.len + a.S) * a.H - rb * kRows, 0);  // row that sees it
+                    for (int d = tid; d < kLatent; d += 128) {
+                        if (fabsf(__bfloat162float(token[d])) < INFINITY) continue;
+                        for (int r = first; r < rows; ++r) {
+                            if (s.whole()) a.o[(row0 + r) * kLatent + d] = __float2bfloat16_rn(NAN);
+                            else part->o[r][d] = NAN;
+                        }
+                    }
+                }
+            }
+        }
+        if (!alive) {
             // a wait gave up: the range's outputs are NaN, and requests that cross it are left unjoined
             Walk<kTile> w = again;
             while (w.next(s)) {

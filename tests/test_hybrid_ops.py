@@ -464,6 +464,35 @@ def test_decode_nan_in_a_new_token_stays_with_the_rows_that_see_it(kda):
     assert torch.equal(o[1, 0], clean[1, 0])
 
 
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+@pytest.mark.parametrize("lens,S,H,wide", [([200, 97], 3, 16, False), ([200, 97], 3, 16, True), ([49, 65], 2, 8, False),
+                                           ([20011, 3], 4, 8, False), ([20011, 96], 4, 32, True)])
+def test_decode_not_finite_in_a_new_token_reaches_the_rows_that_see_it(kda, lens, S, H, wide, value):
+    """The newest but one token of the first request has a latent value that is not finite.  Rows whose query is of the
+    other sign score -inf there: p = 0, NaN in that channel (0 * inf), and the others as if the token were not there.
+    Every other row that sees it is NaN.  (49 and 65: the new tokens lie in two tiles.)"""
+    case = decode_case(lens, S, H, 64, 96)
+    q, cache, table, lens = widened(case) if wide else case
+    length, d = int(lens[0]), 300
+    q[..., d] = torch.where(q[..., d] == 0, 1.0, q[..., d])
+    clean = kda.kda_latent_decode(q, cache, table, lens)
+    at = length - 2
+    cache[table[0, at // 64].long(), at % 64, d] = value
+    lse = torch.empty((len(lens), S, H), device="cuda")
+    o = kda.kda_latent_decode(q, cache, table, lens, lse=lse)
+    assert torch.equal(o[1:], clean[1:]) and torch.equal(o[0, :S - 2], clean[0, :S - 2])
+    rows = cache[table[0, : -(-length // 64)].long()].reshape(-1, 576)[:length]
+    hidden = q[0, S - 2:, :, d].float() * value == -INF
+    assert (value != value) == (not hidden.any()) and not hidden.all()
+    assert o[0, S - 2:][~hidden].isnan().all() and lse[0, S - 2:][~hidden].isnan().all()
+    rows = torch.cat([rows[:at], rows[at + 1:]])[:, None]
+    ref, ref_lse, bound, lse_bound = attention_ref(q[0, S - 2:], rows, rows[..., :512], [at, at + 1], 192 ** -0.5)
+    got, rest = o[0, S - 2:], torch.arange(512, device="cuda") != d
+    assert got[hidden][:, d].isnan().all()
+    within(got[hidden][:, rest], ref[hidden][:, rest], bound[hidden][:, rest], "rows that score -inf")
+    within(lse[0, S - 2:][hidden], ref_lse[hidden], lse_bound[hidden], "their lse")
+
+
 def test_decode_many_rows_and_tokens(kda):
     # more rows than one CTA takes, over a table that holds many tokens
     check_decode(kda, decode_case([9000, 5, 0, 7777, 300], 2, 48, 64, 96))
