@@ -49,11 +49,12 @@
 // workspace, which a second, dependent kernel joins in range order.
 //
 // Warps: 0 TMA, 1 first products, 2 second products (one warp that polled for both
-// took 135 us where two take 129), 4..7 softmax (16 tokens of the tile each: the
+// took 135 us where two take 129), 3 the join's records, 4..7 softmax (16 tokens of the tile each: the
 // last one has none of 48), rescaling and epilogue.
 #include <algorithm>
 
 #include "kda_attn.cuh"
+#include "kda_latent_split.cuh"
 
 namespace kda {
 
@@ -116,21 +117,6 @@ struct Part {  // of a request that crosses ranges
 struct Stat {  // and its rows' reference and sum
     float m, l;
 };
-struct Join {  // ranges first..last hold request n's parts; n < 0: nothing to join
-    int32_t n, first, last, pad;
-};
-
-// Tiles [0, total) cut into `ranges` pieces that differ by at most one tile.
-struct Cut {
-    int base, rem;
-    __device__ __forceinline__ Cut(int total, int ranges) : base(total / ranges), rem(total - base * ranges) {}
-    __device__ __forceinline__ int begin(int range) const { return range * base + min(range, rem); }
-    __device__ __forceinline__ int range_of(int tile) const {
-        const int longer = rem * (base + 1);
-        return tile < longer ? tile / (base + 1) : rem + (tile - longer) / base;
-    }
-};
-
 struct Grid {
     int row_blocks, ranges;
 };
@@ -146,46 +132,7 @@ struct DecodeParams {
     int row_blocks, ranges;
     void *parts;  // Part [range][row block][2]: begun before the range / begun in it
     Stat *stats;  // [row][2][range]: what a joining warp reads lies together
-    Join *joins;  // [ranges]: a request is joined by entry n if there are no more requests than ranges, else
-                  // by the entry of the range that it begins in (at most one leaves a range)
-};
-
-template <int TILE>
-__device__ __forceinline__ int tiles_of(const LatentDecodeArgs &a, int len) {
-    // an empty request (or one that cannot be read) still has a tile: its outputs are written
-    const bool ok = len >= 0 && (int64_t)len <= ((int64_t)a.max_pages << a.page_shift);
-    return ok && len > 0 ? (int)(((int64_t)len + TILE - 1) / TILE) : 1;
-}
-
-// One request's share of a range.
-struct Segment {
-    int n, len, tile0, tiles, total;  // tiles [tile0, tile0 + tiles) of the request's `total`
-    bool ok;
-    __device__ __forceinline__ bool whole() const { return tiles == total; }
-};
-
-// Walks the range's requests; every role keeps its own.
-template <int TILE>
-struct Walk {
-    const LatentDecodeArgs &a;
-    int n, off, left;
-    int len;  // of request n if it is the first, which the setup has read
-    bool begun;
-    __device__ __forceinline__ bool next(Segment &s) {
-        if (left <= 0) return false;
-        s.n = n;
-        s.len = begun ? a.seq_lens[n] : len;
-        begun = true;
-        s.ok = s.len >= 0 && (int64_t)s.len <= ((int64_t)a.max_pages << a.page_shift);
-        s.total = tiles_of<TILE>(a, s.len);
-        if (!s.ok) s.len = 0;
-        s.tile0 = off;
-        s.tiles = min(s.total - off, left);
-        left -= s.tiles;
-        ++n;
-        off = 0;
-        return true;
-    }
+    Join *joins;  // [ranges]
 };
 
 template <int kRows>
@@ -372,6 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (wid == 3) {
+        // ---- the join's records, by the CTA that answers for the range.  They follow from the lengths alone: where
+        // a wait gives up, the parts' NaN reach the joined rows, and other rows' parts are joined as ever.
+        if (rb == 0 && lane == 0) write_joins(walk, cut, range_begin, range, a.n_seqs <= p.ranges, p.joins);
     } else if (wid >= 4) {
         const int tid = threadIdx.x - 128, wid = tid >> 5;  // of the four softmax warps
         // ---- softmax: a thread holds scores of tokens 16 w + lane / 4 (+ 8) of the tile by
@@ -389,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 8 * (c >> 1) + col + (c & 1);
             limit[c] = r < rows ? (rb * kRows + r) / a.H - a.S + 1 : INT32_MIN / 2;
         }
-        int at = range_begin, slot = 0, t = 0;
+        int slot = 0, t = 0;
         bool gave_up = false;  // the same in all four warps: decided by their votes
         while (!gave_up && walk.next(s)) {
             float m[kCols], l[kCols];
@@ -545,13 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!s.whole()) p.stats[(2 * (rb * kRows + tid) + (s.tile0 == 0 ? 1 : 0)) * p.ranges + range] = {mt, lt};
                 else if (a.lse) a.lse[row0 + tid] = lt == 0.0f ? -INFINITY : (mt + log2_sfu(lt)) * kLn2;
             }
-            if (tid == 0 && rb == 0 && s.tile0 == 0) {
-                const bool by_request = a.n_seqs <= p.ranges;
-                Join j = {-1, 0, 0, 0};
-                if (!s.whole()) j = {s.n, range, cut.range_of(at + s.total - 1), 0};
-                if (by_request) p.joins[s.n] = j;
-                else if (!s.whole()) p.joins[range] = j;
-            }
             Part<kRows> *part = (Part<kRows> *)p.parts + ((int64_t)range * p.row_blocks + rb) * 2 + (s.tile0 == 0 ? 1 : 0);
             wait(&pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1);
             tc_fence_after();
@@ -585,11 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             mbar_arrive(&o_empty);
-            at += s.tiles;
             named_bar_sync(1, 128);  // sh_col and sh_row are read before the next request writes them
         }
-        if (tid == 0 && rb == 0 && a.n_seqs > p.ranges && (range >= ranges || s.whole() || s.tile0 > 0))
-            p.joins[range] = {-1, 0, 0, 0};
         const bool alive = named_bar_and(1, 128, !dead);
         if (alive && odd) {
             // A value that is not finite is NaN in its channel for every row that sees its token: by that row's
@@ -619,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!alive) {
-            // a wait gave up: the range's outputs are NaN, and requests that cross it are left unjoined
+            // a wait gave up: the range's outputs are NaN, and so are its parts
             Walk<kTile> w = again;
             while (w.next(s)) {
                 const int64_t row0 = (int64_t)s.n * a.S * a.H + rb * kRows;
@@ -627,8 +568,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int d = tid; d < kLatent; d += 128) a.o[(row0 + c) * kLatent + d] = __float2bfloat16_rn(NAN);
                     if (a.lse && tid == 0) a.lse[row0 + c] = NAN;
                 }
-                if (tid == 0 && s.tile0 == 0 && a.n_seqs <= p.ranges) p.joins[s.n] = {-1, 0, 0, 0};
-                if (tid == 0 && a.n_seqs > p.ranges) p.joins[range] = {-1, 0, 0, 0};
                 if (!s.whole() && tid < rows)
                     p.stats[(2 * (rb * kRows + tid) + (s.tile0 == 0 ? 1 : 0)) * p.ranges + range] = {NAN, NAN};
             }
