@@ -154,11 +154,16 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_current_device = torch._C._cuda_getDevice
+
+
 def _check(t, name, dtype=None, shape=None, device=None):
     if t is None:
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _current_device():  # kernels are launched there
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:

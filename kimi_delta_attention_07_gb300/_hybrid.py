@@ -19,7 +19,7 @@ KDA_LATENT_PREFILL_SPLIT_KEYS = 1024
 _QUANT = {"none": KDA_QUANT_NONE, None: KDA_QUANT_NONE, "row": KDA_QUANT_ROW, "block": KDA_QUANT_BLOCK}
 _bf16, _f32, _i32, _u8, _e4m3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
                                  torch.float8_e4m3fn)
-_current_stream = torch._C._cuda_getCurrentRawStream
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _lib = None
 
 
@@ -29,9 +29,20 @@ def _library():
     return _lib
 
 
+def _device(t, name):
+    """The device of t, which is the current one: kernels are launched there, and their grids and
+    workspaces are sized for it."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
 def _need(t, name, dtype, shape, dev):
     """The address of t: a contiguous CUDA tensor of this dtype and shape on device `dev`."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev >= 0:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
     _core._check(t, name, dtype, shape)
     raise ValueError(f"{name} must be on the same device as the other tensors")
@@ -41,7 +52,7 @@ def _rows(t, name, dtype, shape, dev):
     """The same for a tensor whose first stride is free (a slice of a wider
     projection); returns (address, elements between rows)."""
     strides = t.stride()
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         # below the first axis the strides are those of a contiguous tensor
         inner = shape[-1] if len(shape) == 2 else shape[-1] * shape[-2]
         if strides[-1] == 1 and (len(shape) == 2 or strides[1] == shape[2] or shape[1] == 1):
@@ -81,7 +92,7 @@ def kda_page_tables(ctx_lens, new_lens, free_pages, block_table, *, page_size, n
     [max_tokens], positions [max_tokens], status [2] = (position in free_pages
     after the step, requests refused)), all int32.
     """
-    dev = ctx_lens.get_device()
+    dev = _device(ctx_lens, "ctx_lens")
     n = ctx_lens.numel()
     if slots is not None:
         max_tokens = slots.numel()
@@ -129,7 +140,7 @@ def kda_rms_norm(x, weight=None, *, residual=None, eps=1e-6, quant="none", resid
     (allocated unless given; may be residual or x).  Returns (y, residual_out
     or None, scales or None).
     """
-    dev = x.get_device()
+    dev = _device(x, "x")
     shape, dtype = x.shape, x.dtype
     D = shape[-1]
     q = _QUANT[quant]
@@ -171,7 +182,7 @@ def kda_latent_cache_write(kv, weight, cache, slots, *, eps=1e-6, stream=None):
     page_size, 576] bf16, written in place; slots int32 [T] (others than cache
     rows, such as -1, are skipped).  Returns cache.
     """
-    dev = kv.get_device()
+    dev = _device(kv, "kv")
     T = kv.shape[0]
     pk, stride = _rows(kv, "kv", _bf16, (T, LATENT_ROW), dev)
     if cache.dim() != 3:
@@ -202,7 +213,7 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, scale=None, o=None, ls
     scale defaults to 192 ** -0.5 (the expanded query's width).  lse, if given,
     is fp32 [N, S, H] (or [N, H]).  Returns o, q's shape with 512 for 576.
     """
-    dev = q.get_device()
+    dev = _device(q, "q")
     shape = q.shape
     if len(shape) == 4:
         n, S, H, _ = shape
@@ -252,7 +263,7 @@ def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal
     192 ** -0.5.  lse, if given, is fp32 [Tq, H].  workspace is allocated where one
     is needed, unless given (kda_latent_prefill_workspace_bytes).  Returns o [Tq, H, 128].
     """
-    dev = q.get_device()
+    dev = _device(q, "q")
     if q.dim() != 3 or kv.dim() != 3:
         raise ValueError("q must be [Tq, H, 192], kv [Tk, H, 256]")
     Tq, H, _ = q.shape

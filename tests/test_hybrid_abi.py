@@ -171,6 +171,87 @@ def test_binding_refuses_host_tensors(lib):
         kda.kda_latent_prefill(b[:, None, :192], b[:, None, :256], b[:, :64], cu_seqlens_q=i)
 
 
+class Fake:
+    """Stands for a CUDA tensor (default: an aligned address on device 1)."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.bfloat16, dev=1):
+        self.shape, self.dtype, self.dev, self.device = torch.Size(shape), dtype, dev, torch.device("cuda", dev)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self):
+        return torch.empty(self.shape, device="meta").stride()
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.dev
+
+    def data_ptr(self):
+        return BASE
+
+
+def ints(*shape):
+    return Fake(*shape, dtype=torch.int32)
+
+
+def calls_on_fakes():
+    """One call of each entry point, with every output given."""
+    return {
+        "page_tables": lambda: kda.kda_page_tables(
+            ints(2), ints(2), ints(8), ints(2, 4), page_size=64, n_pages=16, cu_seqlens=ints(3), seq_lens=ints(2),
+            slots=ints(8), positions=ints(8), status=ints(2)),
+        "rms_norm": lambda: kda.kda_rms_norm(Fake(4, 256), y=Fake(4, 256)),
+        "cache_write": lambda: kda.kda_latent_cache_write(Fake(2, 576), None, Fake(1, 16, 576), ints(2)),
+        "decode": lambda: kda.kda_latent_decode(Fake(2, 4, 576), Fake(8, 16, 576), ints(2, 4), ints(2), o=Fake(2, 4, 512),
+                                                workspace=Fake(1 << 28, dtype=torch.uint8)),
+        "prefill": lambda: kda.kda_latent_prefill(Fake(6, 2, 192), Fake(6, 2, 256), Fake(6, 64), cu_seqlens_q=ints(3),
+                                                  o=Fake(6, 2, 128)),
+        "recurrent_step": lambda: kda.kda_recurrent_step(
+            Fake(2, 4, 128), Fake(2, 4, 128), Fake(2, 4, 128), Fake(2, 4, 128, dtype=torch.float32),
+            Fake(2, 4, dtype=torch.float32), Fake(2, 4, 128, 128, dtype=torch.float32), o=Fake(2, 4, 128)),
+        "output_gate_norm": lambda: kda.kda_output_gate_norm(Fake(3, 128), Fake(3, 128), Fake(128, dtype=torch.float32)),
+    }
+
+
+class FakeLibrary:
+    def __init__(self):
+        self.launched = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.launched.append(name) or 0
+
+
+@pytest.fixture
+def fake_library(monkeypatch):
+    """Device 0 is current, every call of the library succeeds and is noted."""
+    from kimi_delta_attention_07_gb300 import _hybrid
+    library = FakeLibrary()
+    monkeypatch.setattr(_hybrid, "_lib", library)
+    monkeypatch.setattr(kda, "load", lambda: library)
+    for module in (kda, _hybrid):
+        monkeypatch.setattr(module, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(_hybrid, "_current_stream", lambda dev: 0)
+    monkeypatch.setattr(kda, "_stream", lambda stream: 0)
+    return library
+
+
+@pytest.mark.parametrize("name", sorted(calls_on_fakes()))
+def test_binding_refuses_tensors_of_another_device_than_the_current_one(fake_library, name):
+    with pytest.raises(ValueError, match="current device"):
+        calls_on_fakes()[name]()
+    assert not fake_library.launched
+    kda._current_device = kda._hybrid._current_device = lambda: 1     # (put back by the fixture)
+    calls_on_fakes()[name]()
+    assert fake_library.launched
+
+
 def test_every_entry_point_of_the_header_has_argument_types(lib):
     for name in ("kda_page_tables", "kda_rms_norm", "kda_latent_cache_write", "kda_latent_decode", "kda_latent_prefill"):
         fn = getattr(lib, name)
