@@ -172,6 +172,21 @@ def _check(t, name, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
 
 
+def _empty(shape, dtype, device, stream, scratch=False):
+    """Memory that a call allocates.  For a given stream it is that stream's own: what was freed on the
+    current one may still be in use there, and a workspace (scratch) that is freed on return goes to later
+    work of `stream` only.  What is returned is marked as in use on the current stream, where the caller
+    may take it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(current)
+    return t
+
+
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
@@ -243,15 +258,15 @@ def kda_chunk_fwd(q, k, v, g, beta, *, cu_seqlens=None, n_seqs=None, initial_sta
     T, H, K, V, N, dt, slots = _chunk_args(q, k, v, g, beta, cu_seqlens, n_seqs, initial_state,
                                            final_state, state_indices, n_slots, o, gdt)
     if state_indices is None and final_state is None and output_final_state:
-        final_state = torch.empty((N, H, V, K), dtype=torch.float32, device=q.device)
+        final_state = _empty((N, H, V, K), torch.float32, q.device, stream)
     if o is None:
-        o = torch.empty((T, H, V), dtype=q.dtype, device=q.device)
+        o = _empty((T, H, V), q.dtype, q.device, stream)
     flags = (KDA_CHUNK_PRECISE if precise else 0) | _SCAN_FLAGS[scan]
     if _gate is not None:
         flags |= KDA_CHUNK_GATED
     need = kda_chunk_workspace_bytes(T, N, H, K, V, dt, flags)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 256), torch.uint8, q.device, stream, scratch=True)
     _check(workspace, "workspace", torch.uint8)
     if scale is None:
         scale = K ** -0.5
@@ -339,7 +354,7 @@ def kda_recurrent_step_gated(q, k, v, raw_gate, raw_beta, a_log, dt_bias, state_
     if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (H, V, K):
         raise ValueError(f"state_pool must be [slots, {H}, {V}, {K}]")
     if o is None:
-        o = torch.empty((N, H, V), dtype=q.dtype, device=q.device)
+        o = _empty((N, H, V), q.dtype, q.device, stream)
     _check(o, "o", q.dtype, (N, H, V))
     if scale is None:
         scale = K ** -0.5
@@ -394,7 +409,7 @@ def kda_recurrent_step(q, k, v, g, beta, state_pool, *, state_indices=None, scal
     if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (H, V, K):
         raise ValueError(f"state_pool must be [slots, {H}, {V}, {K}]")
     if o is None:
-        o = torch.empty((N, H, V), dtype=q.dtype, device=q.device)
+        o = _empty((N, H, V), q.dtype, q.device, stream)
     _check(o, "o", q.dtype, (N, H, V))
     if scale is None:
         scale = K ** -0.5
@@ -429,7 +444,7 @@ def kda_recurrent_multi_step(q, k, v, g, beta, state_pool, state_indices, *, num
     if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (H, V, K):
         raise ValueError(f"state_pool must be [slots, {H}, {V}, {K}]")
     if o is None:
-        o = torch.empty((N, S, H, V), dtype=q.dtype, device=q.device)
+        o = _empty((N, S, H, V), q.dtype, q.device, stream)
     _check(o, "o", q.dtype, (N, S, H, V))
     if scale is None:
         scale = K ** -0.5
@@ -464,7 +479,7 @@ def kda_recurrent_multi_step_gated(q, k, v, raw_gate, raw_beta, a_log, dt_bias, 
     if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (H, V, K):
         raise ValueError(f"state_pool must be [slots, {H}, {V}, {K}]")
     if o is None:
-        o = torch.empty((N, S, H, V), dtype=q.dtype, device=q.device)
+        o = _empty((N, S, H, V), q.dtype, q.device, stream)
     _check(o, "o", q.dtype, (N, S, H, V))
     if scale is None:
         scale = K ** -0.5
@@ -502,7 +517,7 @@ def kda_short_conv_fwd(x, weight, *, cu_seqlens=None, n_seqs=None, activation="s
                                    ("final_states", final_states, x.dtype, None)):
         _check(t, name, dtype_, shape)
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     _check(y, "y", x.dtype, (T, D))
     pool = final_states if final_states is not None else initial_states
     slots = 0
@@ -530,7 +545,7 @@ def kda_short_conv_update(x, weight, state_pool, *, state_indices=None, activati
     if state_pool.dim() != 3 or tuple(state_pool.shape[1:]) != (ks - 1, D):
         raise ValueError(f"state_pool must be [slots, {ks - 1}, {D}]")
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     _check(y, "y", x.dtype, (N, D))
     st = load().kda_short_conv_update(_p(x), _p(weight), _p(y), _p(state_pool), _p(state_indices),
                                       state_pool.shape[0], N, D, ks, _CONV_ACT[activation], dt,
@@ -559,7 +574,7 @@ def kda_short_conv_multi_update(x, weight, state_pool, state_indices, *, num_acc
     if state_pool.dim() != 3 or tuple(state_pool.shape[1:]) != (ks - 1, D):
         raise ValueError(f"state_pool must be [slots, {ks - 1}, {D}]")
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     _check(y, "y", x.dtype, (N, S, D))
     st = load().kda_short_conv_multi_update(_p(x), _p(weight), _p(y), _p(state_pool),
                                             _p(state_indices), _p(num_accepted), state_pool.shape[0],

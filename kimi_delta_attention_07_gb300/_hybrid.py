@@ -1,8 +1,8 @@
 """Binding of the operators around the KDA core (include/kda_hybrid.h): page
 tables, residual + RMS norm, the paged latent cache and latent attention.
 
-Arguments are checked on the host, nothing is synchronised.  A call on a
-stream that is not the current one marks what it allocated as in use there.
+Arguments are checked on the host, nothing is synchronised.  What a call on a
+given stream allocates is that stream's memory.
 Small calls are dominated by the host, so the checks test all of a tensor's
 properties at once and name the property only when one of them fails.
 """
@@ -20,6 +20,7 @@ _QUANT = {"none": KDA_QUANT_NONE, None: KDA_QUANT_NONE, "row": KDA_QUANT_ROW, "b
 _bf16, _f32, _i32, _u8, _e4m3 = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
                                  torch.float8_e4m3fn)
 _current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_empty = _core._empty
 _lib = None
 
 
@@ -70,14 +71,6 @@ def _rows(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be on the same device as the other tensors")
 
 
-def _stream_of(stream, *allocated):
-    """A given stream's handle; what the call allocated is marked as in use there."""
-    for t in allocated:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
-
-
 def kda_page_tables(ctx_lens, new_lens, free_pages, block_table, *, page_size, n_pages, max_tokens=None,
                     free_start=None, cu_seqlens=None, seq_lens=None, slots=None, positions=None,
                     status=None, stream=None):
@@ -107,11 +100,9 @@ def kda_page_tables(ctx_lens, new_lens, free_pages, block_table, *, page_size, n
     pf = _need(free_pages, "free_pages", _i32, (n_free,), dev)
     pb = _need(block_table, "block_table", _i32, (n, max_pages), dev)
     ps = None if free_start is None else _need(free_start, "free_start", _i32, (1,), dev)
-    new = []
 
     def fresh(size):
-        new.append(torch.empty(size, dtype=_i32, device=ctx_lens.device))
-        return new[-1]
+        return _empty(size, _i32, ctx_lens.device, stream)
 
     cu_seqlens = fresh(n + 1) if cu_seqlens is None else cu_seqlens
     seq_lens = fresh(n) if seq_lens is None else seq_lens
@@ -123,7 +114,7 @@ def kda_page_tables(ctx_lens, new_lens, free_pages, block_table, *, page_size, n
         _need(seq_lens, "seq_lens", _i32, shape, dev), _need(slots, "slots", _i32, (max_tokens,), dev),
         _need(positions, "positions", _i32, (max_tokens,), dev), _need(status, "status", _i32, (2,), dev), n,
         max_tokens, max_pages, page_size, n_pages,
-        _current_stream(dev) if stream is None else _stream_of(stream, *new))
+        _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise _core.KdaError(st, "kda_page_tables")
     return cu_seqlens, seq_lens, slots, positions, status
@@ -145,30 +136,29 @@ def kda_rms_norm(x, weight=None, *, residual=None, eps=1e-6, quant="none", resid
     D = shape[-1]
     q = _QUANT[quant]
     px = _need(x, "x", dtype, shape, dev)
-    new_r = new_y = new_s = None
     if residual is None:
         pr = None
     else:
         pr = _need(residual, "residual", dtype, shape, dev)
         if residual_out is None:
-            residual_out = new_r = torch.empty_like(x)
+            residual_out = _empty(shape, dtype, x.device, stream)
     po = None if residual_out is None else _need(residual_out, "residual_out", dtype, shape, dev)
     pw = None if weight is None else _need(weight, "weight", _f32, (D,), dev)
     ydt = _e4m3 if q else dtype
     if y is None:
-        y = new_y = torch.empty(shape, dtype=ydt, device=x.device)
+        y = _empty(shape, ydt, x.device, stream)
     py = _need(y, "y", ydt, shape, dev)
     if q:
         groups = (*shape[:-1], 1 if q == KDA_QUANT_ROW else D // 128)
         if scales is None:
-            scales = new_s = torch.empty(groups, dtype=_f32, device=x.device)
+            scales = _empty(groups, _f32, x.device, stream)
         ps = _need(scales, "scales", _f32, groups, dev)
     else:
         scales = ps = None
     st = (_lib or _library()).kda_rms_norm(
         px, pr, pw, py, ps, po, eps, x.numel() // D if D else 0, D, q,
         KDA_BF16 if dtype is _bf16 else _core._dtype_code(x),
-        _current_stream(dev) if stream is None else _stream_of(stream, new_r, new_y, new_s))
+        _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise _core.KdaError(st, "kda_rms_norm")
     return y, residual_out, scales
@@ -193,7 +183,7 @@ def kda_latent_cache_write(kv, weight, cache, slots, *, eps=1e-6, stream=None):
     ps = _need(slots, "slots", _i32, (T,), dev)
     st = (_lib or _library()).kda_latent_cache_write(
         pk, stride, pw, eps, pc, ps, T, n_pages, page_size,
-        _current_stream(dev) if stream is None else _stream_of(stream))
+        _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise _core.KdaError(st, "kda_latent_cache_write")
     return cache
@@ -229,20 +219,18 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, scale=None, o=None, ls
     pb = _need(block_table, "block_table", _i32, (n, block_table.shape[1]), dev)
     pl = _need(seq_lens, "seq_lens", _i32, (n,), dev)
     out = (*shape[:-1], LATENT_DIM)
-    new_o = new_w = None
     if o is None:
-        o = new_o = torch.empty(out, dtype=_bf16, device=q.device)
+        o = _empty(out, _bf16, q.device, stream)
     po = _need(o, "o", _bf16, out, dev)
     ple = None if lse is None else _need(lse, "lse", _f32, shape[:-1], dev)
     lib = _lib or _library()
     if workspace is None:
-        workspace = new_w = torch.empty(max(256, lib.kda_latent_decode_workspace_bytes(n, S, H)), dtype=_u8,
-                                        device=q.device)
+        workspace = _empty(max(256, lib.kda_latent_decode_workspace_bytes(n, S, H)), _u8, q.device, stream, scratch=True)
     ws = workspace.numel()
     st = lib.kda_latent_decode(
         pq, pc, pb, pl, po, ple, n, S, H, n_pages, page_size, block_table.shape[1],
         192 ** -0.5 if scale is None else scale, _need(workspace, "workspace", _u8, (ws,), dev), ws,
-        _current_stream(dev) if stream is None else _stream_of(stream, new_o, new_w))
+        _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise _core.KdaError(st, "kda_latent_decode")
     return o
@@ -276,25 +264,24 @@ def kda_latent_prefill(q, kv, k_rope, *, cu_seqlens_q, cu_seqlens_k=None, causal
         raise ValueError("cu_seqlens_q must be int32 [N+1] with N >= 1")
     pcq = _need(cu_seqlens_q, "cu_seqlens_q", _i32, (n + 1,), dev)
     pck = None if cu_seqlens_k is None else _need(cu_seqlens_k, "cu_seqlens_k", _i32, (n + 1,), dev)
-    new_o = None
     if o is None:
-        o = new_o = torch.empty((Tq, H, VALUE_DIM), dtype=_bf16, device=q.device)
+        o = _empty((Tq, H, VALUE_DIM), _bf16, q.device, stream)
     po = _need(o, "o", _bf16, (Tq, H, VALUE_DIM), dev)
     ple = None if lse is None else _need(lse, "lse", _f32, (Tq, H), dev)
     lib = _lib or _library()
-    pw, ws, new_w = None, 0, None
+    pw, ws = None, 0
     if workspace is not None:
         ws = workspace.numel()
         pw = _need(workspace, "workspace", _u8, (ws,), dev)
     elif Tk >= KDA_LATENT_PREFILL_SPLIT_KEYS:
         ws = lib.kda_latent_prefill_workspace_bytes(n, Tq, Tk, H)
         if ws:
-            new_w = torch.empty(ws, dtype=_u8, device=q.device)
-            pw = new_w.data_ptr()
+            workspace = _empty(ws, _u8, q.device, stream, scratch=True)
+            pw = workspace.data_ptr()
     st = lib.kda_latent_prefill(
         pq, sq, pk, sk, pr, sr, po, ple, pcq, pck, n, Tq, Tk, H, 1 if causal else 0,
         192 ** -0.5 if scale is None else scale, pw, ws,
-        _current_stream(dev) if stream is None else _stream_of(stream, new_o, new_w))
+        _current_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise _core.KdaError(st, "kda_latent_prefill")
     return o
