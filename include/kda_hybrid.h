@@ -183,6 +183,9 @@ size_t kda_latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t t
  * whose offsets are decreasing or out of range are not written.  Pointers are
  * 16-byte aligned.  Tq = 0 is a no-op.  Results do not depend on timing: parts
  * are joined in a fixed order.
+ *
+ * Limits: N <= 65535, H <= 65535, H * ((Tq + 255 min(N, Tq)) / 256) < 2^31 (blocks of
+ * 256 queries of a head; beyond them KDA_ERR_UNSUPPORTED).
  */
 int kda_latent_prefill(const void *q, int64_t q_stride, const void *kv, int64_t kv_stride,
                        const void *k_rope, int64_t rope_stride, void *o, float *lse,

@@ -102,6 +102,8 @@ struct LatentPrefillArgs {
     float scale;
     void *workspace;
 };
+// Blocks of queries times heads, at most: the grid without a split.
+int64_t latent_prefill_items(int n_seqs, int64_t total_q, int H);
 size_t latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t total_k, int H);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t stream);
 

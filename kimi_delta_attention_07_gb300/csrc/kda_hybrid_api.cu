@@ -143,7 +143,7 @@ int kda_latent_prefill(const void *q, int64_t q_stride, const void *kv, int64_t 
         kv_stride < (int64_t)kKvRow * H || kv_stride % 8 != 0 || rope_stride < kRope ||
         rope_stride % 8 != 0)
         return KDA_ERR_INVALID_ARG;
-    if (H > 65535 || n_seqs > 65535) return KDA_ERR_UNSUPPORTED;
+    if (H > 65535 || n_seqs > 65535 || latent_prefill_items(n_seqs, total_q, H) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     if (total_q == 0) return KDA_OK;
     if (!q || !o || !cu_seqlens_q || (total_k > 0 && (!kv || !k_rope)) || !aligned(q, 16) ||
         !aligned(kv, 16) || !aligned(k_rope, 16) || !aligned(o, 16) || !aligned(lse, 4) ||

@@ -754,6 +754,8 @@ inline Layout layout(int64_t items, int splits) {
 
 }  // namespace
 
+int64_t latent_prefill_items(int n_seqs, int64_t total_q, int H) { return block_bound(n_seqs, total_q) * H; }
+
 size_t latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t total_k, int H) {
     const int splits = splits_for(n_seqs, total_q, total_k, H);
     return splits == 1 ? 0 : layout(block_bound(n_seqs, total_q) * H, splits).total;
@@ -769,8 +771,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t strea
     } else {
         map_kv = map_r = map_q;  // no key: not used
     }
-    const int64_t items = block_bound(a.n_seqs, a.total_q) * a.H;
-    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    const int64_t items = latent_prefill_items(a.n_seqs, a.total_q, a.H);
     const int splits = splits_for(a.n_seqs, a.total_q, a.total_k, a.H);
     auto launch = [&](auto kernel, const auto &p) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);

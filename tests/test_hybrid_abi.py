@@ -137,6 +137,15 @@ def test_prefill_refuses(lib, kw):
     assert _prefill(lib, **kw) == INVALID
 
 
+def test_prefill_unsupported(lib):
+    wide = dict(sq=192 * 65535, sk=256 * 65535)
+    assert _prefill(lib, H=65536, sq=192 * 65536, sk=256 * 65536) == UNSUPPORTED
+    assert _prefill(lib, n=65536) == UNSUPPORTED
+    # more blocks of queries and heads than a grid has
+    assert _prefill(lib, Tq=(1 << 31) - 1, n=1, H=65535, **wide) == UNSUPPORTED
+    assert _prefill(lib, Tq=40000, n=40000, H=65535, **wide) == UNSUPPORTED
+
+
 def test_prefill_workspace(lib):
     # few queries behind many keys: the keys are split; enough queries, or few keys: they are not
     need = kda.kda_latent_prefill_workspace_bytes(1, 64, 65536, 4)
