@@ -67,14 +67,14 @@ extern "C" {
  *
  * A request is refused when a length is negative, when its length would pass
  * 2^31 - 1 or need more than max_pages pages, or when its pages pass the end of
- * free_pages.  A refused
- * request takes no page (one refused by a length or by max_pages moves no
- * other request's pages), its tokens get slot and position -1, and its
+ * free_pages.  A refused request takes no page (one refused by a length or by
+ * max_pages moves no other request's pages), its tokens get slot and position -1, and its
  * seq_lens is its ctx_lens (0 if that is negative).  A token whose
  * page id is outside [0, n_pages) gets slot and position -1.
  * N = 0 or max_tokens = 0 is allowed (max_tokens less than the packed batch:
- * only the first max_tokens entries are written).  No output may be an input
- * (seq_lens is not ctx_lens: keep two and exchange them).
+ * only the first max_tokens entries are written).  No output may share memory
+ * with an input or with block_table (seq_lens is not ctx_lens: keep two and
+ * exchange them).
  */
 int kda_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *free_pages,
                     int64_t n_free, const int32_t *free_start, int32_t *block_table,

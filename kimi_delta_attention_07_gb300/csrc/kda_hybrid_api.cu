@@ -46,11 +46,26 @@ int kda_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, const int3
         (n_seqs > 0 && (!ctx_lens || !new_lens || !block_table || !seq_lens)) ||
         (max_tokens > 0 && (!slots || !positions)))
         return KDA_ERR_INVALID_ARG;
-    // every CTA reads the inputs, while the first one writes these
-    const int32_t *written[] = {cu_seqlens, seq_lens, slots, positions, status, status + 1, block_table};
-    for (const int32_t *in : {ctx_lens, new_lens, free_pages, free_start})
-        for (const int32_t *out : written)
-            if (in && in == out) return KDA_ERR_INVALID_ARG;
+    // every CTA reads the inputs (the table's held entries among them) while others write the outputs
+    struct Ints {
+        const int32_t *p;
+        int64_t n;
+        bool meets(const Ints &o) const {
+            return p && o.p && n > 0 && o.n > 0 && (uintptr_t)p < (uintptr_t)(o.p + o.n) &&
+                   (uintptr_t)o.p < (uintptr_t)(p + n);
+        }
+    };
+    const Ints table = {block_table, (int64_t)n_seqs * max_pages};
+    const Ints inputs[] = {{ctx_lens, n_seqs}, {new_lens, n_seqs}, {free_pages, n_free}, {free_start, 1}};
+    const Ints outputs[] = {{cu_seqlens, (int64_t)n_seqs + 1}, {seq_lens, n_seqs}, {slots, max_tokens},
+                            {positions, max_tokens}, {status, 2}};
+    for (const Ints &in : inputs)
+        if (in.meets(table)) return KDA_ERR_INVALID_ARG;
+    for (const Ints &out : outputs) {
+        if (out.meets(table)) return KDA_ERR_INVALID_ARG;
+        for (const Ints &in : inputs)
+            if (in.meets(out)) return KDA_ERR_INVALID_ARG;
+    }
     for (const void *p : {(const void *)ctx_lens, (const void *)new_lens, (const void *)free_pages,
                           (const void *)free_start, (const void *)block_table,
                           (const void *)cu_seqlens, (const void *)seq_lens, (const void *)slots,

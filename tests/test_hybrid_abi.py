@@ -48,6 +48,16 @@ def test_page_tables_refuses_an_output_that_is_an_input(lib, which, out):
     assert _tables(lib, **{which: BASE + 1024 * 1024, out: BASE + 1024 * 1024}) == INVALID
 
 
+@pytest.mark.parametrize("kw", [
+    dict(ctx=BASE, lens=BASE + 4), dict(lens=BASE, ctx=BASE + 4),                      # one entry apart, two requests
+    dict(new=BASE, cu=BASE + 4), dict(cu=BASE, new=BASE + 8),                          # offsets hold one entry more
+    dict(free=BASE, slots=BASE + 28), dict(pos=BASE, free=BASE + 28),                  # the last of eight
+    dict(start=BASE + 4, status=BASE), dict(table=BASE, start=BASE + 28),
+    dict(table=BASE, slots=BASE + 16), dict(pos=BASE, table=BASE + 28), dict(table=BASE, status=BASE - 4)])
+def test_page_tables_refuses_an_output_that_shares_memory_with_an_input(lib, kw):
+    assert _tables(lib, **{k: v + 1024 * 1024 for k, v in kw.items()}) == INVALID
+
+
 def test_page_tables_refuses_too_many_requests(lib):
     assert _tables(lib, n=16385) == UNSUPPORTED
 
