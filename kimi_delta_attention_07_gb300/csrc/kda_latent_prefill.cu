@@ -729,7 +729,8 @@ inline int64_t block_bound(int n_seqs, int64_t total_q) {
 inline int splits_for(int n_seqs, int64_t total_q, int64_t total_k, int H) {
     const int64_t items = block_bound(n_seqs, total_q) * H, steps = (total_k / n_seqs + kTile - 1) / kTile;
     const int sms = sm_count();
-    if (items == 0 || items > 2 * sms || steps < kSplitSteps) return 1;
+    // (below SPLIT_KEYS no caller has a workspace, whatever the costs say)
+    if (items == 0 || items > 2 * sms || steps < kSplitSteps || total_k < KDA_LATENT_PREFILL_SPLIT_KEYS) return 1;
     const int64_t most = std::min<int64_t>({4 * sms / items, (steps + kMinSteps - 1) / kMinSteps, kMaxSplits});
     int best = 1;
     double least = 0.85 * ((items + sms - 1) / sms) * (steps + 3.0);

@@ -169,6 +169,14 @@ def test_prefill_workspace(lib):
         assert _prefill(lib, ws=ws, ws_bytes=size, **few) == WORKSPACE
 
 
+def test_prefill_needs_no_workspace_below_the_documented_number_of_keys(lib):
+    below = kda.KDA_LATENT_PREFILL_SPLIT_KEYS - 1
+    for n in (1, 2, 3, 8):
+        for tq in (1, 64, 256, 257, 1024):
+            for H in (*range(1, 34), 64, 100, 128, 149, 150, 153, 200, 300, 305):
+                assert all(kda.kda_latent_prefill_workspace_bytes(n, tq, tk, H) == 0 for tk in (0, 1, 500, 896, 897, 960, below))
+
+
 def test_prefill_nothing_to_do(lib):
     assert _prefill(lib, Tq=0) == OK
     assert _prefill(lib, Tq=0, ck=None, Tk=0) == OK
