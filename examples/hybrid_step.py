@@ -58,16 +58,28 @@ class HybridDecoder:
         self.free_start = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros(requests, dtype=torch.int32, device="cuda")
         self.slots = torch.arange(requests, dtype=torch.int32, device="cuda")
+        self.begun = False
 
     def step(self, x, new_lens, prompts):
         """x [T, hidden]: the packed new tokens' embeddings (one a request when
-        `prompts` is false); new_lens int32 [N].  Returns the normed output as
-        e4m3 values and scales, and those values in fp32."""
+        `prompts` is false); new_lens int32 [N].  Prompts come first: they begin at
+        position 0 and from zero states.  Raises, and changes nothing that a later
+        step reads, if a request is refused (out of pages or of its table's row).
+        Returns the normed output as e4m3 values and scales, and those values in
+        fp32."""
         T, H = x.shape[0], self.heads
+        if prompts and self.begun:
+            raise ValueError("a prompt needs requests without cached tokens")
+        if not prompts and T != self.lens.numel():
+            raise ValueError("a decode step takes one token a request")
         cu, lens, slots, _, status = kda.kda_page_tables(
             self.lens, new_lens, self.free_pages, self.table, page_size=self.page_size, n_pages=self.n_pages,
             max_tokens=T, free_start=self.free_start)
-        self.free_start = status[:1].clone()
+        # A refused request's tokens have slot -1 and its length stays.  (A server that counts its pages on the host
+        # does not wait for the device here.)
+        if int(status[1]):
+            raise RuntimeError(f"{int(status[1])} requests refused: more pages are needed than are free or fit a row")
+        self.free_start, self.begun = status[:1].clone(), True
         # KDA layer
         y, _, _ = kda.kda_rms_norm(x, self.norms[0])
         q, k, v, gate, beta = (y @ self.kda_in).split([H * HEAD] * 4 + [H], -1)
