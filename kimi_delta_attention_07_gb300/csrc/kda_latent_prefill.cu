@@ -33,8 +33,8 @@
 // Masked places: keys that a row does not see get p = 0, and 0 times a value has
 // to be 0 whatever the value is.  In the tiles where some key is not seen by
 // some row, two warps look through V before it is used: rows past the
-// sequence's end become 0, and so do values that are not finite; the epilogue
-// then adds those to the rows that see them.
+// sequence's end become 0, and so do values that are not finite; they are added to
+// the outputs of the rows that see them.
 //
 // Few queries behind many keys (a chunk of a prompt behind its cached part) would leave
 // most SMs idle: the keys of a block of queries are then split into parts of whole
@@ -129,6 +129,15 @@ __device__ __forceinline__ int blocks_of(const LatentPrefillArgs &a, int n) {
     const int qa = a.cu_q[n], qb = a.cu_q[n + 1], ka = a.cu_k[n], kb = a.cu_k[n + 1];
     const bool ok = qa >= 0 && qb >= qa && qb <= a.total_q && ka >= 0 && kb >= ka && kb <= a.total_k;
     return ok ? (qb - qa + kItem - 1) / kItem : 0;
+}
+
+// Whether a key's 128 + 64 values are all finite.
+__device__ __forceinline__ bool finite_key(const __nv_bfloat16 *nope, const __nv_bfloat16 *rope) {
+    uint32_t ones = 0;
+#pragma unroll 1
+    for (int j = 0; j < kQk / 8; ++j)
+        ones |= exponent_of_ones(*(const uint4 *)(j < kNope / 8 ? nope + 8 * j : rope + 8 * j - kNope));
+    return ones == 0;
 }
 
 // POSITIVE: scale > 0, so that the largest product is the largest score.  SPLIT: the keys of an item
@@ -580,7 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += *other;
             }
             const float inv = gave_up ? NAN : l == 0.0f ? 1.0f : 1.0f / l;
-            const bool add = odd[it & 1] != 0;
             uint32_t w[8][4];  // the thread's 64 values of its row, eight units of 16 bytes
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -591,19 +599,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-                }
-                if (__any_sync(0xffffffffu, add)) {
-                    // values that were taken out of V because they are not finite
-                    for (int key = s.masked * kTile; key < (SPLIT ? min(limit, steps * kTile) : limit); ++key) {
-                        const __nv_bfloat16 *v = a.kv + (int64_t)(s.ka + key) * a.kv_stride +
-                                                 (int64_t)s.h * kKvRow + kNope + 64 * half + 32 * k;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float u = __bfloat162float(v[j]);
-                            if (!(fabsf(u) < INFINITY)) o[j] += u;
-                        }
-                    }
-                    __syncwarp();
                 }
                 if constexpr (SPLIT) {
                     if (split && real) {
@@ -646,6 +641,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (real && a.lse && half == 0 && !split)
                 a.lse[out] = gave_up ? NAN : l == 0.0f ? -INFINITY : (m * scale2 + log2_sfu(l)) * kLn2;
+            if (__any_sync(0xffffffffu, odd[it & 1])) {
+                // Values that were taken out of V because they are not finite, for the rows that see them.  A key that is
+                // not finite either has a score of -inf (p = 0, and 0 times the value is NaN) or makes the row NaN.
+                __syncwarp();  // (other lanes have written the row)
+                const int end = !real ? 0 : SPLIT ? min(limit, steps * kTile) : limit;
+#pragma unroll 1
+                for (int key = s.masked * kTile; key < end; ++key) {
+                    const __nv_bfloat16 *v = a.kv + (int64_t)(s.ka + key) * a.kv_stride + (int64_t)s.h * kKvRow;
+                    const bool by_zero = !finite_key(v, a.k_rope + (int64_t)(s.ka + key) * a.rope_stride);
+#pragma unroll 1
+                    for (int j = 64 * half; j < 64 * half + 64; ++j) {
+                        const float u = __bfloat162float(v[kNope + j]);
+                        if (fabsf(u) < INFINITY) continue;
+                        if constexpr (SPLIT) {
+                            if (split) {
+                                p.parts[s.part].o[t * kTile + quad * 32 + lane][j] += by_zero ? NAN : u;
+                                continue;
+                            }
+                        }
+                        __nv_bfloat16 *dst = a.o + out * kHeadDim + j;
+                        *dst = __float2bfloat16_rn(__bfloat162float(*dst) + (by_zero ? NAN : u));
+                    }
+                }
+            }
             __syncwarp();
             if (lane == 0) item_done(it);
             if (gave_up) break;

@@ -703,6 +703,29 @@ def test_prefill_not_finite_values_stay_where_they_are_seen(kda):
     assert torch.equal(o[:300], clean[:300]) and torch.equal(o[:, 1], clean[:, 1])
 
 
+@pytest.mark.parametrize("lq,lk,at", [(300, 300, 200), (300, 300, 20), (200, 2000, 1900), (129, 199, 198)])
+@pytest.mark.parametrize("value", [INF, -INF])
+def test_prefill_infinite_value_of_a_token_that_scores_minus_infinity(kda, lq, lk, at, value):
+    """p = 0 there, and 0 times the value is NaN in its channel; the other channels are as if the token were not there.
+    (In a tile with hidden places, in one without, with split keys, and as the last key.)"""
+    q, kv, rope, cq, ck = prefill_case([lq], [lk], 2, 36)
+    q[..., 7] = torch.where(q[..., 7] == 0, 1.0, q[..., 7])
+    kv[at, :, 7], kv[at, 1, 128 + 40] = INF, value
+    lse = torch.empty(q.shape[:2], device="cuda")
+    o = kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck, lse=lse)
+    sees = (torch.arange(lq, device="cuda") + lk - lq >= at)[:, None].expand(lq, 2)
+    below = sees & (q[..., 7] < 0)
+    assert o[sees & ~below].isnan().all() and o[below & (torch.arange(2, device="cuda") == 1)][:, 40].isnan().all()
+    rest = [j for j in range(lk) if j != at]
+    k = torch.cat([kv[..., :128], rope[:, None].expand(-1, 2, -1)], -1)[rest]
+    seen = [i + 1 + lk - lq - (i + lk - lq >= at) for i in range(lq)]
+    ref, ref_lse, bound, lse_bound = attention_ref(q, k, kv[rest][..., 128:], seen, 192 ** -0.5)
+    fine = (below | ~sees)[..., None].expand(lq, 2, 128).clone()
+    fine[:, 1, 40] &= ~sees[:, 1]
+    within(o[fine], ref[fine], bound[fine], "o")
+    within(lse[below | ~sees], ref_lse[below | ~sees], lse_bound[below | ~sees], "lse")
+
+
 def test_prefill_bad_offsets_write_nothing_of_their_sequence(kda):
     q, kv, rope, _, _ = prefill_case([300], [300], 2, 12)
     o = torch.full((300, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
