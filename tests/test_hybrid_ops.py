@@ -554,6 +554,20 @@ def test_decode_rows_do_not_depend_on_what_lies_beside_them(kda, S, H, wide):
     assert torch.equal(kda.kda_latent_decode(other, cache, table, lens)[:, :, 1:], plain[:, :, 1:])
 
 
+@pytest.mark.parametrize("n", [5000, 65535])
+def test_decode_thousands_of_requests(kda, n):
+    # of one tile each, so that a request's bits are the same in a call with fewer of them
+    g = torch.Generator().manual_seed(n)
+    cache, q = normal((300, 16, 576), 121), normal((n, 4, 576), 122)
+    table = torch.randint(0, 300, (n, 3), generator=g).to(torch.int32).cuda()
+    lens = torch.randint(0, 49, (n,), generator=g).to(torch.int32).cuda()
+    o = kda.kda_latent_decode(q, cache, table, lens)
+    for a in range(0, n, n // 5 - 7):
+        part = slice(a, a + 700)
+        assert torch.equal(o[part], kda.kda_latent_decode(q[part], cache, table[part], lens[part])), a
+    check_decode(kda, (q[-40:, None], cache, table[-40:], lens[-40:]))
+
+
 def test_decode_past_32_bits(kda):
     page, n_pages = 64, 2 ** 31 // (576 * 64) + 200
     cache = torch.empty((n_pages, page, 576), dtype=torch.bfloat16, device="cuda")
@@ -767,6 +781,22 @@ def test_prefill_many_short_sequences(kda, causal):
     want[starts[19]:starts[21]] = 7.0
     want[starts[b + 1] - 2 if causal else starts[b]:starts[b + 1], 5, 72] = INF
     assert torch.equal(again, want)
+
+
+def test_prefill_thousands_of_sequences(kda):
+    g = torch.Generator().manual_seed(6)
+    lens = torch.randint(0, 4, (5000,), generator=g).tolist()
+    lens[4321], lens[17] = 300, 257
+    keys = [v + int(p) for v, p in zip(lens, torch.randint(0, 5, (5000,), generator=g))]
+    q, kv, rope, cq, ck = prefill_case(lens, keys, 2, 42, slack=1)
+    o = kda.kda_latent_prefill(q, kv, rope, cu_seqlens_q=cq, cu_seqlens_k=ck)
+    aq, ak = cq.tolist(), ck.tolist()
+    for a in range(0, 5000, 500):
+        rows, cols = slice(aq[a], aq[a + 500]), slice(ak[a], ak[a + 500])
+        part = (q[rows], kv[cols], rope[cols], cq[a:a + 501] - aq[a], ck[a:a + 501] - ak[a])
+        got = kda.kda_latent_prefill(*part[:3], cu_seqlens_q=part[3], cu_seqlens_k=part[4])
+        assert torch.equal(o[rows], got), a
+    check_prefill(kda, (part[0], part[1], part[2], part[3][-61:], part[4][-61:]))
 
 
 @pytest.mark.parametrize("causal", [True, False])
