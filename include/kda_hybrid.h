@@ -158,7 +158,8 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
  * where there are too few queries to fill the GPU and so many keys that they are
  * split (for queries that see KDA_LATENT_PREFILL_SPLIT_KEYS of them; the split,
  * and with it the rounding, follows from the arguments n_seqs, total_q, total_k, H
- * and the lengths).  0: none is needed, as always where total_k is less than
+ * and the lengths).  Whether keys are split is decided by total_k / n_seqs: one long
+ * sequence among many short ones is better given a call of its own.  0: none is needed, as always where total_k is less than
  * KDA_LATENT_PREFILL_SPLIT_KEYS; 0 on invalid sizes. */
 #define KDA_LATENT_PREFILL_SPLIT_KEYS 1024
 size_t kda_latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t total_k, int H);
@@ -179,10 +180,11 @@ size_t kda_latent_prefill_workspace_bytes(int n_seqs, int64_t total_q, int64_t t
  *   *_stride  elements between tokens (multiples of 8): q at least 192 H,
  *           kv at least 256 H, k_rope at least 64
  *
- * A query that sees no key gives o = 0 and lse = -inf.  Tokens of a sequence
- * whose offsets are decreasing or out of range are not written.  Pointers are
- * 16-byte aligned.  Tq = 0 is a no-op.  Results do not depend on timing: parts
- * are joined in a fixed order.
+ * A query that sees no key gives o = 0 and lse = -inf.  The probabilities enter
+ * the second product as bf16; their sum is taken in fp32 before that rounding.
+ * Tokens of a sequence whose offsets are decreasing or out of range are not
+ * written.  Pointers are 16-byte aligned.  Tq = 0 is a no-op.  Results do not
+ * depend on timing: parts are joined in a fixed order.
  *
  * Limits: N <= 65535, H <= 65535, H * ((Tq + 255 min(N, Tq)) / 256) < 2^31 (blocks of
  * 256 queries of a head; beyond them KDA_ERR_UNSUPPORTED).

@@ -29,12 +29,12 @@
 // done, which is about 1.2 us after it has arrived (at 44 bytes a ns); three
 // tiles of 48 keep more in flight (90 KB) than two of 64 (68 KB).  The first
 // product's M is 64: its last 16 rows are whatever follows in the ring.  256
-// requests of 512 to 4096 tokens, 32 heads (697 MB): 125 us, 5.6 TB/s; with the
-// products cut to a ninth, so that little but the loads is left, 122 us.  With 64
+// requests of 512 to 4096 tokens, 32 heads (697 MB): 123 us, 5.7 TB/s; with the
+// products cut to a ninth and a quarter, so that little but the loads is left, 118 us.  With 64
 // query rows a CTA the queries leave room for 128 tokens, as two tiles of 64 (no
 // row of the first product is wasted; four tiles of 32 are 8 to 15 % slower); p
 // then takes the place of the tile's positional block, which the first product
-// has read.  2 requests of 231k tokens in all, 64 rows: 64 us, 40 of them at 6.7
+// has read.  2 requests of 231k tokens in all, 64 rows: 65 us, 40 of them at 6.7
 // TB/s between the first tile's arrival and the last one's.
 //
 // Running maximum: a row keeps a reference that is only raised (and its column of
@@ -752,9 +752,9 @@ size_t latent_decode_workspace_bytes(int n_seqs, int S, int H) {
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
     // 64 query rows a CTA read the cache half as often, but take 3 us longer over a first tile, and their
     // ring holds 128 tokens against 144.  What counts is how often 32 rows a CTA would read the tokens that
-    // the block table can hold: 128k tokens (4 requests, 128 rows each) 30.4 us with 32 rows and 31.6 us with
-    // 64, 180k (7 requests, 64 rows) 35.5 and 37.2, 187k (183 requests, 128 rows) 56.4 and 52.1, 256k
-    // (16 requests, 48 rows) 46.6 and 41.8, 640k (4 requests, 128 rows) 87.6 and 68.4.
+    // the block table can hold: 128k tokens (4 requests, 128 rows each) 29.1 us with 32 rows and 30.2 us with
+    // 64, 180k (7 requests, 64 rows) 34.8 and 37.3, 187k (183 requests, 128 rows) 47.6 and 46.2, 256k
+    // (16 requests, 48 rows) 44.6 and 40.0, 640k (4 requests, 128 rows) 85.6 and 68.9.
     const int64_t read = (((int64_t)a.n_seqs * a.max_pages) << a.page_shift) * ((a.S * a.H + 31) / 32);
     return a.S * a.H > 32 && read > 184320 ? launch<64>(a, stream) : launch<32>(a, stream);
 }

@@ -18,7 +18,7 @@
 // for both tiles) and the issuing thread's own instructions.  So two threads own a
 // query row (TMEM lane), 64 keys of a step each; they exchange their maxima in a
 // step and their sums at the end, and hand P over in two parts, the first of which
-// is multiplied while the second is computed.  A step takes about 3250 clocks: 1550
+// is multiplied while the second is computed.  A step takes about 3200 clocks: 1580
 // TFLOP/s on 8192 queries and keys without a mask, where shared memory, which
 // X_t's operands alone read at its full 128 bytes a clock, leaves little room.
 //
@@ -44,7 +44,7 @@
 // CTAs ask for work with cluster launch control: the grid has a CTA per 256
 // queries and head, heaviest first within a sequence, and a running CTA takes
 // over the next unlaunched one, so that its loads overlap the last epilogue.
-// 4096 queries and keys of 32 heads: 119 us, 1440 TFLOP/s of the visible pairs.
+// 4096 queries and keys of 32 heads: 117 us a call in a graph of calls, 1470 TFLOP/s of the visible pairs.
 //
 // Warps: 0..7 and 8..15 softmax and epilogue of the two tiles, 16 TMA and
 // scheduling, 17 MMA, 18 and 19 the value blocks' check.
@@ -743,8 +743,10 @@ inline int64_t block_bound(int n_seqs, int64_t total_q) {
 // Parts that an item's keys are split into at most, from what the host knows: the waves of parts times
 // their steps, to which a part's start and outputs add about three and the join five.  8 heads, 64
 // queries and 2112 keys: 36 us whole, 15 us split; 16 heads, 512 queries behind 32768 keys: 421 and
-// 134 us; 1 head, 512 behind 65536: 820 and 42 us.  1024 queries and keys of 8 heads, which the
-// rule leaves whole: 20.8 and 21.9 us.
+// 131 us; 1 head, 512 behind 65536: 820 and 41 us.  1024 queries and keys of 8 heads, which the
+// rule leaves whole: 20.8 and 21.9 us.  The host has no lengths, so that a long sequence among short
+// ones is left whole: 16 queries behind 131072 keys, 8 heads, 112 us alone and 1780 us beside 15 sequences
+// of 256 keys.
 inline int splits_for(int n_seqs, int64_t total_q, int64_t total_k, int H) {
     const int64_t items = block_bound(n_seqs, total_q) * H, steps = (total_k / n_seqs + kTile - 1) / kTile;
     const int sms = sm_count();
