@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- the join's records, by the CTA that answers for the range.  They follow from the lengths alone: where
         // a wait gives up, the parts' NaN reach the joined rows, and other rows' parts are joined as ever.
         if (rb == 0 && lane == 0) write_joins(walk, cut, range_begin, range, a.n_seqs <= p.ranges, p.joins);
+        __syncwarp();
     } else if (wid >= 4) {
         const int tid = threadIdx.x - 128, wid = tid >> 5;  // of the four softmax warps
         // ---- softmax: a thread holds scores of tokens 16 w + lane / 4 (+ 8) of the tile by

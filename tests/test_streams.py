@@ -162,3 +162,24 @@ def test_work_of_the_current_stream_does_not_reach_a_call_on_another(name):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     del held
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["rms_norm", "decode", "prefill", "chunk_fwd"])
+def test_a_call_on_a_stream_of_a_captured_graph(name):
+    kda.load()
+    call = gpu_cases()[name]
+    want = [v.clone() for v in call(None)]
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+        after = [v * 1 for v in got]
+    for _ in range(2):
+        for v in (*got, *after):
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(after, want)) and all(torch.equal(a, b) for a, b in zip(got, want))
