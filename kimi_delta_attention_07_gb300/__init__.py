@@ -12,6 +12,9 @@ Entry points (same names as the C ABI):
   kda_page_tables, kda_rms_norm, kda_latent_cache_write, kda_latent_decode,
   kda_latent_prefill   the operators around the core in a hybrid decoder's
                        serving step (include/kda_hybrid.h, _hybrid.py)
+  kda_head_norm_rope, kda_linear_chunk_fwd, kda_linear_step,
+  kda_linear_multi_step  a linear-attention layer with one decay a head
+                       (include/kda_linear.h, _linear.py)
 """
 from __future__ import annotations
 
@@ -46,7 +49,9 @@ EXPORTS = ("kda_status_string", "kda_version", "kda_chunk_workspace_bytes", "kda
            "kda_short_conv_update", "kda_short_conv_multi_update", "kda_recurrent_multi_step_gated",
            "kda_status_from_workspace_flags", "kda_page_tables", "kda_rms_norm",
            "kda_latent_cache_write", "kda_latent_decode_workspace_bytes", "kda_latent_decode",
-           "kda_latent_prefill_workspace_bytes", "kda_latent_prefill")
+           "kda_latent_prefill_workspace_bytes", "kda_latent_prefill", "kda_head_norm_rope",
+           "kda_linear_chunk_workspace_bytes", "kda_linear_chunk_fwd", "kda_linear_step",
+           "kda_linear_multi_step")
 NOALLOC_WORKSPACE_BYTES = 64 * 1024 * 1024
 
 _lib = None
@@ -133,6 +138,17 @@ def load(path: str | None = None):
         L.kda_latent_prefill_workspace_bytes.restype = sz
         for name in ("kda_page_tables", "kda_rms_norm", "kda_latent_cache_write", "kda_latent_decode",
                      "kda_latent_prefill"):
+            getattr(L, name).restype = i32
+        L.kda_head_norm_rope.argtypes = [vp, i64, vp, i64, vp, vp, f32, i32, vp, vp, i32, vp, i32, i32, i32, vp,
+                                         i64, vp, i64, i64, i32, i32, i32, i32, vp]
+        L.kda_linear_chunk_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.kda_linear_chunk_workspace_bytes.restype = sz
+        layer = [vp, i64, vp, i64, vp, i64, vp, i64]
+        L.kda_linear_chunk_fwd.argtypes = layer + [vp, vp, vp, i64, vp, vp, i32, i64, i32, i32, i32, i32, f32, i32, vp,
+                                                   sz, vp]
+        L.kda_linear_step.argtypes = layer + [vp, vp, i64, vp, i32, i32, i32, i32, i32, f32, i32, vp]
+        L.kda_linear_multi_step.argtypes = layer + [vp, vp, vp, i64, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp]
+        for name in ("kda_head_norm_rope", "kda_linear_chunk_fwd", "kda_linear_step", "kda_linear_multi_step"):
             getattr(L, name).restype = i32
         _lib = L
         return L
@@ -613,3 +629,5 @@ def kda_chunk_fwd_noalloc(q, k, v, g, beta, *, o, final_state=None, cu_seqlens=N
 from ._hybrid import (KDA_LATENT_PREFILL_SPLIT_KEYS, KDA_QUANT_BLOCK, KDA_QUANT_NONE, KDA_QUANT_ROW,  # noqa: E402,F401
                       kda_latent_cache_write, kda_latent_decode, kda_latent_decode_workspace_bytes,
                       kda_latent_prefill, kda_latent_prefill_workspace_bytes, kda_page_tables, kda_rms_norm)
+from ._linear import (kda_head_norm_rope, kda_linear_chunk_fwd, kda_linear_chunk_workspace_bytes,  # noqa: E402,F401
+                      kda_linear_multi_step, kda_linear_step)

@@ -1,0 +1,78 @@
+// Launchers of the linear-attention layer with one decay a head (kda_linear.h).
+#pragma once
+
+#include "kda_hybrid.cuh"
+#include "kda_linear.h"
+
+namespace kda {
+
+struct HeadRopeArgs {
+    const void *x[2];  // q, k
+    void *y[2];
+    int64_t x_stride[2], y_stride[2];
+    const float *weight[2];
+    int heads[2];
+    float eps;
+    const int32_t *positions;
+    const float *inv_freq;
+    int section_end[KDA_ROPE_MAX_AXES];  // pairs below it turn by this axis or one before
+    int rot_offset, rot_dim, D;
+    int64_t n_tokens;
+};
+cudaError_t launch_head_norm_rope(const HeadRopeArgs &a, bool norm, bool interleaved, int dtype, cudaStream_t stream);
+
+struct LinearChunkArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g;
+    int64_t g_stride;
+    const float *initial_state;
+    float *final_state;
+    const int32_t *state_indices;
+    int64_t n_slots;
+    void *o;
+    const int32_t *cu_seqlens;
+    int n_seqs;
+    int64_t total_tokens;
+    int H, group;  // group: heads that share q and k
+    float scale;
+    void *workspace;
+};
+size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H);
+cudaError_t launch_linear_chunk_serial(const LinearChunkArgs &a, int dtype, cudaStream_t stream);
+
+struct LinearStepArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g;
+    int64_t g_stride;
+    float *pool;
+    const int32_t *state_indices, *num_accepted;
+    int64_t n_slots;
+    void *o;
+    int N, S, H, group;
+    float scale;
+};
+cudaError_t launch_linear_step(const LinearStepArgs &a, int dtype, cudaStream_t stream);
+
+// Sequence n's tokens [first, first + len); len < 0 where its offsets are decreasing or out of range.
+struct Span {
+    int first, len;
+};
+__device__ __forceinline__ Span span_of(const LinearChunkArgs &a, int n) {
+    if (!a.cu_seqlens) {
+        const int len = (int)(a.total_tokens / a.n_seqs);
+        return {n * len, len};
+    }
+    const int from = a.cu_seqlens[n], to = a.cu_seqlens[n + 1];
+    const bool ok = from >= 0 && to >= from && to <= a.total_tokens;
+    return {from, ok ? to - from : -1};
+}
+// The slot of sequence n's states, -1 where it lies outside the pool.
+__device__ __forceinline__ int64_t slot_of(const LinearChunkArgs &a, int n) {
+    if (!a.state_indices) return n;
+    const int s = a.state_indices[n];
+    return s >= 0 && s < a.n_slots ? s : -1;
+}
+
+}  // namespace kda
