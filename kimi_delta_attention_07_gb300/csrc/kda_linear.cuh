@@ -39,7 +39,9 @@ struct LinearChunkArgs {
     void *workspace;
 };
 size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H);
-cudaError_t launch_linear_chunk_serial(const LinearChunkArgs &a, int dtype, cudaStream_t stream);
+// bf16 on the tensor cores; fp32 on the CUDA cores (no workspace)
+cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream);
+cudaError_t launch_linear_chunk_f32(const LinearChunkArgs &a, cudaStream_t stream);
 
 struct LinearStepArgs {
     const void *q, *k, *v;

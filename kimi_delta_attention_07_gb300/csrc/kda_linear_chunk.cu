@@ -17,8 +17,7 @@ constexpr int kThreads = kRows * kLanes;
 constexpr int kPer = kHeadDim / kLanes;  // key channels of a lane: four times four, 32 apart
 constexpr int kBlock = 16;               // tokens in shared memory at a time
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) linear_chunk_serial_kernel(const LinearChunkArgs a) {
+__global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const LinearChunkArgs a) {
     __shared__ __align__(16) float sq[kBlock][kHeadDim], sk[kBlock][kHeadDim];
     __shared__ float sv[kBlock][kRows], sg[kBlock];
     griddep_wait();
@@ -29,10 +28,10 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_serial_kernel(const Lin
     if (span.len < 0) return;
     const int64_t slot = slot_of(a, n);
     const int64_t first = span.first;
-    T *o = (T *)a.o + h * kHeadDim + row0;
+    float *o = (float *)a.o + h * kHeadDim + row0;
     if (slot < 0) {
         for (int64_t i = tid; i < (int64_t)span.len * kRows; i += kThreads)
-            o[(first + i / kRows) * a.H * kHeadDim + i % kRows] = from_f32<T>(__int_as_float(0x7fc00000));
+            o[(first + i / kRows) * a.H * kHeadDim + i % kRows] = (__int_as_float(0x7fc00000));
         return;
     }
     const int64_t state_at = (slot * a.H + h) * (int64_t)(kHeadDim * kHeadDim) + (int64_t)(row0 + row) * kHeadDim + 4 * l;
@@ -40,8 +39,8 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_serial_kernel(const Lin
 #pragma unroll
     for (int i = 0; i < kPer / 4; ++i)
         s[i] = a.initial_state ? *(const float4 *)(a.initial_state + state_at + 32 * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const T *q = (const T *)a.q + h / a.group * kHeadDim, *k = (const T *)a.k + h / a.group * kHeadDim,
-            *v = (const T *)a.v + h * kHeadDim + row0;
+    const float *q = (const float *)a.q + h / a.group * kHeadDim, *k = (const float *)a.k + h / a.group * kHeadDim,
+            *v = (const float *)a.v + h * kHeadDim + row0;
     constexpr int kVecs = kBlock * kHeadDim / 4 / kThreads;  // of four channels, of q (and of k) a thread
     float4 rq[kVecs], rk[kVecs];
     float rv[kBlock * kRows / kThreads], rg = 0.0f;
@@ -56,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_serial_kernel(const Lin
 #pragma unroll
         for (int i = 0; i < kBlock * kRows / kThreads; ++i) {
             const int t = t0 + (tid + i * kThreads) / kRows;
-            if (t < span.len) rv[i] = to_f32(v[(first + t) * a.v_stride + tid % kRows]);
+            if (t < span.len) rv[i] = (v[(first + t) * a.v_stride + tid % kRows]);
         }
         if (tid < kBlock && t0 + tid < span.len) rg = a.g[(first + t0 + tid) * a.g_stride + h];
     };
@@ -87,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_serial_kernel(const Lin
             float x = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
             for (int m = 1; m < kLanes; m <<= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-            if (l == 0) o[(first + t0 + t) * a.H * kHeadDim + row] = from_f32<T>(a.scale * x);
+            if (l == 0) o[(first + t0 + t) * a.H * kHeadDim + row] = (a.scale * x);
         }
     }
     if (a.final_state)
@@ -97,12 +96,9 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_serial_kernel(const Lin
 
 }  // namespace
 
-size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H) { return 0; }
-
-cudaError_t launch_linear_chunk_serial(const LinearChunkArgs &a, int dtype, cudaStream_t stream) {
-    const dim3 grid((unsigned)(a.n_seqs * a.H), kHeadDim / kRows);
-    const cudaError_t e = launch_dependent(dtype == KDA_BF16 ? linear_chunk_serial_kernel<__nv_bfloat16> : linear_chunk_serial_kernel<float>,
-                                           grid, dim3(kThreads), 0, stream, a);
+cudaError_t launch_linear_chunk_f32(const LinearChunkArgs &a, cudaStream_t stream) {
+    const cudaError_t e = launch_dependent(linear_chunk_f32_kernel, dim3((unsigned)(a.n_seqs * a.H), kHeadDim / kRows),
+                                           dim3(kThreads), 0, stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
