@@ -32,8 +32,15 @@
 // value that is not finite would reach rows before it as 0 times it: V is looked through,
 // such values become 0 and their channel NaN from their row on, in o and in S.
 //
-// Warps: 0 TMA, 1 MMA of X and O, 2 MMA of D, 3 decays, 4..7 Kt, 8..11 check of V and P,
-// 12..19 the state and the outputs, 64 value channels each half.
+// What bounds a chunk: not its products (3072 clocks of the tensor core; taking them out changes nothing) but
+// the chain of instructions of a warp, each some seven clocks behind the last. So the work is spread over
+// as many warps as there are registers for.  With outputs, eight warps look through V and make Kt and
+// run ahead, sixteen make P and hold the state, 32 value channels each, and take a chunk's outputs while the
+// next one's scores are computed; without outputs, sixteen warps make a quarter of Kt each and update a
+// quarter of the state while the next chunk's D runs.
+//
+// Warps: 0 TMA, 1 MMA of X and O, 2 MMA of D, 3 decays, 4..11 check of V and Kt, 12..27 P, the state
+// and the outputs; without outputs 4..19 all of it.
 #include <algorithm>
 
 #include "kda_attn.cuh"
@@ -46,7 +53,6 @@ using namespace tc;
 namespace {
 
 constexpr int kTok = 128;  // tokens of a chunk
-constexpr int kThreads = 640;
 constexpr uint32_t kTile = 32768;        // 128 tokens x 128 channels: two blocks of 64 channels
 constexpr uint32_t kHalf = kTile / 2;
 constexpr int kState = kHeadDim * kHeadDim;
@@ -54,17 +60,18 @@ constexpr int kState = kHeadDim * kHeadDim;
 // shared memory (from a 1024-byte boundary): two stages of K, Q, V; the copy of S
 constexpr uint32_t kSmK = 0, kSmQ = 2 * kTile, kSmV = 4 * kTile, kSmS = 6 * kTile, kSmShared = 7 * kTile;
 
-// TMEM columns: X and P, O, D, two buffers of 32 tokens of Kt in three terms of 16 columns
-constexpr uint32_t kTmO = 128, kTmD = 256, kTmK = 384, kTmTerm = 16, kTmBuf = 48;
+// TMEM columns: X and P (block b of P over the first 16 columns of its scores), O, D, buffers of 32 tokens of Kt in three
+// terms of 16 columns.  Without outputs eight buffers, over X and O as well.
+constexpr uint32_t kTmO = 128, kTmD = 384, kTmK = 256, kTmTerm = 16, kTmBuf = 48;
 
 struct Shared {
-    uint64_t kq_full[2], v_full[2], k_empty[2], q_empty[2], v_empty[2], gates_full[2], gates_empty[2], v_ready[2],
-        kt_full[2], kt_empty[2], x_full, p_full, qs_full, o_scaled, o_full, o_empty, s_full, d_full, d_empty;
+    uint64_t full[2], k_empty[2], q_empty[2], v_empty[2], gates_full[2], gates_empty[2], v_ready[2], kt_full[2], kt_empty[2],
+        x_full, qs_full, pv_ready, o_full, o_empty, d_full, d_empty;
     alignas(16) float lower[2][kTok];  // log2 decay of a token's block up to and with it
-    float upper[2][kTok];   // decay of a token's block behind it
-    float block[2][4];      // log2 decay of each block
-    uint8_t odd[2][kTok];   // a value channel's first row that is not finite, if any_odd; else kTok
-    volatile int any_odd[2], dead;
+    float upper[2][kTok];              // decay of a token's block behind it
+    float block[2][4];                 // log2 decay of each block
+    uint8_t odd[4][kTok];              // a value channel's first row that is not finite (kTok: none), if any_odd
+    volatile int any_odd[4][4], dead;  // of a group of channels
     uint32_t tmem_base;
 };
 constexpr uint32_t kSmemBytes = kSmShared + sizeof(Shared);
@@ -80,6 +87,54 @@ struct ChunkParams {
     float *decay;    // [entries][H]
 };
 
+// Two fp32 as one operand of the packed instructions.
+typedef uint64_t F2;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unf2(F2 x, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Two bf16 of a register as fp32.
+__device__ __forceinline__ F2 wide(uint32_t two) {
+    return f2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t narrow(F2 x) {
+    float lo, hi;
+    unf2(x, lo, hi);
+    return pack2(lo, hi);
+}
+
+// Four 8 x 8 matrices of bf16, transposed: matrix m's rows are the 16 bytes that lanes 8 m .. 8 m + 7 point at;
+// r[m] holds the elements (row 2 (lane % 4), 2 (lane % 4) + 1; column lane / 4).
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t *r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 columns of 16 TMEM lanes: u[2 j + h] goes to lane 8 h + lane / 4, column 4 j + lane % 4.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t *u) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+// The larger magnitude of two pairs of bf16, NaN if either is.
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ int offset_of(const LinearChunkArgs &a, int n) {
     return a.cu_seqlens ? a.cu_seqlens[n] : n * (int)(a.total_tokens / a.n_seqs);
 }
@@ -108,7 +163,7 @@ struct Item {
 
 // Segment (and head) `i` of the kernel with outputs.  Sequence n's segments are numbered from
 // floor(offset / segment) + n on, which leaves room for all of them whatever the lengths; false: no such segment.
-__device__ __forceinline__ bool output_item(const ChunkParams &p, int64_t i, Item &s) {
+__device__ __noinline__ bool output_item(const ChunkParams &p, int64_t i, Item &s) {
     const LinearChunkArgs &a = p.a;
     const int64_t rank = i / a.H;
     s.h = (int)(i - rank * a.H);
@@ -127,7 +182,7 @@ __device__ __forceinline__ bool output_item(const ChunkParams &p, int64_t i, Ite
 
 // Segment of entry m, if it is one that others follow in its sequence: the one that token
 // (m + 1) segment - 1 lies in, or ends with.
-__device__ __forceinline__ bool state_item(const ChunkParams &p, int m, Item &s) {
+__device__ __noinline__ bool state_item(const ChunkParams &p, int m, Item &s) {
     const LinearChunkArgs &a = p.a;
     const int64_t x = (int64_t)(m + 1) * p.segment;
     s.n = last_below(a.n_seqs, x, [&](int n) { return (int64_t)offset_of(a, n); });
@@ -145,7 +200,7 @@ __device__ __forceinline__ bool state_item(const ChunkParams &p, int m, Item &s)
 
 // OUTPUT: o and final states, from the states in front of the segments; else a segment's own state.
 template <bool OUTPUT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const ChunkParams p) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -155,14 +210,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.kq_full[i], 1), mbar_init(&sh.v_full[i], 1);
-            mbar_init(&sh.k_empty[i], OUTPUT ? 2 : 1), mbar_init(&sh.q_empty[i], 1), mbar_init(&sh.v_empty[i], OUTPUT ? 2 : 1);
-            mbar_init(&sh.gates_full[i], 1), mbar_init(&sh.gates_empty[i], 16);
-            mbar_init(&sh.v_ready[i], 128), mbar_init(&sh.kt_full[i], 128), mbar_init(&sh.kt_empty[i], 1);
+            mbar_init(&sh.full[i], 1), mbar_init(&sh.k_empty[i], OUTPUT ? 9 : 16), mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.v_empty[i], OUTPUT ? 2 : 1), mbar_init(&sh.v_ready[i], OUTPUT ? 8 : 16);
+            mbar_init(&sh.gates_full[i], 1), mbar_init(&sh.gates_empty[i], OUTPUT ? 24 : 16);
+            mbar_init(&sh.kt_full[i], OUTPUT ? 4 : 16), mbar_init(&sh.kt_empty[i], 1);
         }
-        mbar_init(&sh.x_full, 1), mbar_init(&sh.p_full, 128), mbar_init(&sh.qs_full, 1), mbar_init(&sh.o_scaled, 256);
-        mbar_init(&sh.o_full, 1), mbar_init(&sh.o_empty, 256), mbar_init(&sh.s_full, 256);
-        mbar_init(&sh.d_full, 1), mbar_init(&sh.d_empty, 256);
+        mbar_init(&sh.x_full, 1), mbar_init(&sh.qs_full, 1), mbar_init(&sh.pv_ready, 16);
+        mbar_init(&sh.o_full, 1), mbar_init(&sh.o_empty, 16), mbar_init(&sh.d_full, 1), mbar_init(&sh.d_empty, 16);
         fence_mbar_init();
         dead = 0;
     }
@@ -179,6 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_try_wait(bar, parity) && !dead && !mbar_wait(bar, parity)) dead = 1;
         __syncwarp();
     };
+    // one arrival a warp
+    auto arrive = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
     auto gave_up = [&] { return __any_sync(0xffffffffu, dead); };
     // f(item, chunks) for each of this CTA's items, in the same order by every warp
     auto for_items = [&](auto f) {
@@ -192,32 +251,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s.h = (int)(i - (int64_t)m * a.H);
                 if (!state_item(p, m, s)) continue;
             }
-            f(s, s.slot < 0 ? 0 : (s.rows + kTok - 1) / kTok);
+            // a segment whose states serve o alone does without the third term
+            f(s, s.slot < 0 ? 0 : (s.rows + kTok - 1) / kTok, OUTPUT && s.cut && !s.ends ? 2 : 3);
         }
     };
 
     if (wid == 0) {
         // ---- TMA
         uint32_t c = 0;
-        for_items([&](const Item &s, int chunks) {
+        for_items([&](const Item &s, int chunks, int terms) {
             const int hk = s.h / a.group;
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
                 const uint32_t st = c & 1, before = ((c >> 1) & 1) ^ 1;
                 const int row = s.first + i * kTok;
                 wait(&sh.k_empty[st], before);
                 if (OUTPUT) wait(&sh.q_empty[st], before);
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sh.kq_full[st], OUTPUT ? 2 * kTile : kTile);
-                    for (int b = 0; b < 2; ++b) {
-                        tma_load_3d(sm + kSmK + st * kTile + b * kHalf, &map_k, 64 * b, hk, row, &sh.kq_full[st]);
-                        if (OUTPUT) tma_load_3d(sm + kSmQ + st * kTile + b * kHalf, &map_q, 64 * b, hk, row, &sh.kq_full[st]);
-                    }
-                }
                 wait(&sh.v_empty[st], before);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&sh.v_full[st], kTile);
-                    for (int b = 0; b < 2; ++b)
-                        tma_load_3d(sm + kSmV + st * kTile + b * kHalf, &map_v, 64 * b, s.h, row, &sh.v_full[st]);
+                    uint64_t *bar = &sh.full[st];
+                    mbar_arrive_expect_tx(bar, OUTPUT ? 3 * kTile : 2 * kTile);
+#pragma unroll 1
+                    for (int b = 0; b < 2; ++b) {
+                        uint8_t *to = sm + st * kTile + b * kHalf;
+                        tma_load_3d(to + kSmK, &map_k, 64 * b, hk, row, bar);
+                        if (OUTPUT) tma_load_3d(to + kSmQ, &map_q, 64 * b, hk, row, bar);
+                        tma_load_3d(to + kSmV, &map_v, 64 * b, s.h, row, bar);
+                    }
                 }
                 __syncwarp();
             }
@@ -227,10 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t c = 0;
         const uint32_t q0 = smem_u32(sm + kSmQ), k0 = smem_u32(sm + kSmK), s0 = smem_u32(sm + kSmS);
         const uint32_t v_lo = (smem_u32(sm + kSmV) >> 4) | ((kHalf >> 4) << 16);
-        for_items([&](const Item &s, int chunks) {
+        for_items([&](const Item &s, int chunks, int terms) {
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
                 const uint32_t st = c & 1, full = (c >> 1) & 1;
-                wait(&sh.kq_full[st], full);
+                wait(&sh.full[st], full);
                 if (c > 0) wait(&sh.o_full, (c - 1) & 1);  // P of the chunk before is read
                 tc_fence_after();
                 if (elect_one()) {
@@ -239,8 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&sh.x_full);
                 }
                 __syncwarp();
-                wait(&sh.s_full, c & 1);
-                if (c > 0) wait(&sh.o_empty, (c - 1) & 1);
+                wait(&sh.o_empty, c & 1);  // O is taken, and the copy of S is there
                 tc_fence_after();
                 if (elect_one()) {
                     mma_tile<kTok, kTok, kHeadDim, kTok, kTok, false, true>(tmem + kTmO, q0 + st * kTile, s0, false);
@@ -248,15 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&sh.qs_full);
                 }
                 __syncwarp();
-                wait(&sh.v_ready[st], full);
-                wait(&sh.p_full, c & 1);
-                wait(&sh.o_scaled, c & 1);
+                wait(&sh.pv_ready, c & 1);  // (behind v_ready)
                 tc_fence_after();
                 if (elect_one()) {
                     constexpr uint32_t idesc = idesc_bf16(kTok, kTok) | (1u << 16);
 #pragma unroll
                     for (int j = 0; j < kTok / 16; ++j)
-                        mma_bf16_ts(tmem + kTmO, tmem + 8 * j,
+                        mma_bf16_ts(tmem + kTmO, tmem + 32 * (j >> 1) + 8 * (j & 1),
                                     ((uint64_t)kDescHi << 32) | (uint64_t)(v_lo + st * (kTile >> 4) + 128 * j), idesc, 1);
                     mma_commit(&sh.v_empty[st]);
                     mma_commit(&sh.o_full);
@@ -266,29 +322,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
     } else if (wid == 2) {
         // ---- MMA of D
-        uint32_t c = 0, kt = 0;  // chunks and quarters of Kt so far
+        // Kt comes in quarters through two buffers, or (without outputs) in whole chunks, likewise
+        uint32_t c = 0, kt = 0;
         const uint32_t v_lo = (smem_u32(sm + kSmV) >> 4) | ((kHalf >> 4) << 16);
-        constexpr uint32_t idesc = idesc_bf16(kTok, kTok) | (1u << 16);
-        for_items([&](const Item &s, int chunks) {
+        constexpr int kParts = OUTPUT ? 4 : 1;
+        for_items([&](const Item &s, int chunks, int terms) {
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
-                const uint32_t st = c & 1, full = (c >> 1) & 1;
-                const int quarters = (min(kTok, s.rows - i * kTok) + 31) / 32;
-                wait(&sh.v_ready[st], full);
+                const uint32_t st = c & 1;
+                const int steps = (min(kTok, s.rows - i * kTok) + 15) / 16;
+                wait(&sh.v_ready[st], (c >> 1) & 1);
                 if (c > 0) wait(&sh.d_empty, (c - 1) & 1);
-                for (int b = 0; b < quarters; ++b, ++kt) {
+#pragma unroll 1
+                for (int b = 0; b < kParts; ++b, ++kt) {
                     wait(&sh.kt_full[kt & 1], (kt >> 1) & 1);
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t k_at = tmem + kTmK + (kt & 1) * kTmBuf, v_at = v_lo + st * (kTile >> 4) + 256 * b;
-#pragma unroll
-                        for (int term = 0; term < 3; ++term)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                mma_bf16_ts(tmem + kTmD, k_at + term * kTmTerm + 8 * j,
-                                            ((uint64_t)kDescHi << 32) | (uint64_t)(v_at + 128 * j), idesc, b + term + j > 0);
+                        constexpr uint32_t idesc = idesc_bf16(kTok, kTok) | (1u << 16);
+                        constexpr int kSteps = 8 / kParts;
+                        const uint32_t k_at = tmem + (OUTPUT ? kTmK : 0) + (kt & 1) * (kTmBuf * (4 / kParts));
+                        const uint32_t v_at = v_lo + st * (kTile >> 4) + 256 * b;
+#pragma unroll 1
+                        for (int j = 0; j < kSteps && kSteps * b + j < steps; ++j)
+#pragma unroll 1
+                            for (int t = 0; t < terms; ++t)
+                                mma_bf16_ts(tmem + kTmD, k_at + (j >> 1) * kTmBuf + t * kTmTerm + 8 * (j & 1),
+                                            ((uint64_t)kDescHi << 32) | (uint64_t)(v_at + 128 * j), idesc, b + t + j > 0);
                         mma_commit(&sh.kt_empty[kt & 1]);
-                        if (b == quarters - 1) {
-                            mma_commit(&sh.k_empty[st]);
+                        if (b == kParts - 1) {
                             mma_commit(&sh.v_empty[st]);
                             mma_commit(&sh.d_full);
                         }
@@ -300,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (wid == 3) {
         // ---- decays
         uint32_t c = 0;
-        for_items([&](const Item &s, int chunks) {
+        for_items([&](const Item &s, int chunks, int terms) {
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
                 const uint32_t st = c & 1;
                 float g[4];
@@ -309,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int t = i * kTok + 32 * b + lane;
                     g[b] = t < s.rows ? a.g[(int64_t)(s.first + t) * a.g_stride + s.h] * kLog2e : 0.0f;
                 }
-                wait(&sh.gates_empty[st], ((c >> 1) & 1) ^ 1);
+                float lower[4], upper[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     // (2^-160 is 0; -inf would leave no difference of two sums)
@@ -322,299 +382,372 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane + o < 32) down += z;
                     }
                     down = __shfl_down_sync(0xffffffffu, down, 1);
-                    sh.lower[st][32 * b + lane] = up;
-                    sh.upper[st][32 * b + lane] = lane < 31 ? exp2f(down) : 1.0f;
-                    if (lane == 31) sh.block[st][b] = up;
+                    lower[b] = up;
+                    upper[b] = lane < 31 ? exp2f(down) : 1.0f;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.gates_full[st]);
+                wait(&sh.gates_empty[st], ((c >> 1) & 1) ^ 1);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    sh.lower[st][32 * b + lane] = lower[b];
+                    sh.upper[st][32 * b + lane] = upper[b];
+                    if (lane == 31) sh.block[st][b] = lower[b];
+                }
+                arrive(&sh.gates_full[st]);
             }
         });
-    } else if (wid >= 4 && wid < 8) {
-        // ---- Kt: a thread takes a key channel, 32 tokens at a time
-        uint32_t c = 0, kt = 0;
-        const int d = tid - 128;
-        const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
-        const uint32_t at = (d >> 6) * kHalf + (d & 7) * 2, chunk16 = (d & 63) >> 3;
-        for_items([&](const Item &s, int chunks) {
-            for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
-                const uint32_t st = c & 1, full = (c >> 1) & 1;
-                const int rows = min(kTok, s.rows - i * kTok), quarters = (rows + 31) / 32;
-                wait(&sh.gates_full[st], full);
-                wait(&sh.kq_full[st], full);
-                const uint8_t *k = sm + kSmK + st * kTile + at;
-                float behind = 0.0f;  // log2 decay of the blocks behind
-                for (int b = 1; b < 4; ++b) behind += sh.block[st][b];
-                for (int b = 0; b < quarters; ++b, ++kt) {
-                    const float f = exp2f(behind);
-                    if (b < 3) behind = b == 0 ? sh.block[st][2] + sh.block[st][3] : b == 1 ? sh.block[st][3] : 0.0f;
-                    wait(&sh.kt_empty[kt & 1], ((kt >> 1) & 1) ^ 1);
-                    tc_fence_after();
-                    uint32_t term[3][16];
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) {
-                        float y[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int j = 2 * m + e;
-                            const uint32_t u = *(const uint16_t *)(k + (32 * b + j) * 128 + ((chunk16 ^ (j & 7)) << 4));
-                            y[e] = __uint_as_float(u << 16) * (f * sh.upper[st][32 * b + j]);
-                            if (32 * b + j >= rows) y[e] = 0.0f;
-                        }
-#pragma unroll
-                        for (int t = 0; t < 3; ++t) {
-                            const uint32_t w = pack2(y[0], y[1]);
-                            term[t][m] = w;
-                            y[0] -= __uint_as_float(w << 16), y[1] -= __uint_as_float(w & 0xffff0000u);
-                        }
-                    }
-                    const uint32_t to = tmem + kTmK + (kt & 1) * kTmBuf + lanes;
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) tmem_st16(to + t * kTmTerm, term[t]);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive(&sh.kt_full[kt & 1]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.gates_empty[st]);
-            }
-        });
-    } else if (wid >= 8 && wid < 12) {
-        // ---- check of V; P: a thread takes a row (token i of the chunk)
-        uint32_t c = 0;
-        const int row = tid - 256, w = wid & 3;
+    } else if (wid >= 4) {
+        constexpr int kGroups = OUTPUT ? 2 : 4;  // of four warps that look through V and make Kt
+        constexpr int kWidth = kHeadDim / kGroups;
+        const bool maker = !OUTPUT || wid < 12;
+        const int g = (wid >> 2) - 1, u = OUTPUT ? g - 2 : g, w = wid & 3, row = 32 * w + lane;
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
-        for_items([&](const Item &s, int chunks) {
-            for (int i = 0; i < chunks; ++i, ++c) {  // (not left early: its four warps meet at a barrier)
-                const uint32_t st = c & 1, full = (c >> 1) & 1;
-                const int rows = min(kTok, s.rows - i * kTok);
-                wait(&sh.gates_full[st], full);  // (the chunk two before is done with `odd`)
-                wait(&sh.v_full[st], full);
-                uint8_t *v = sm + kSmV + st * kTile;
-                uint32_t ones = 0;
+        // Kt: this lane's address of a matrix row (matrix 2 j + h: tokens 8 j .., channels 8 h .. of 16)
+        const int token = 8 * (lane >> 4) + (lane & 7), channel = 32 * w + 8 * ((lane >> 3) & 1);
+        const uint32_t k_at = smem_u32(sm + kSmK) + (channel >> 6) * kHalf + token * 128;
+        const uint32_t unit = (channel & 63) >> 3, turn = token & 7;
+        uint32_t kt = 0;
+
+        // V: kWidth channels of this thread's row; rows past the sequence's end become zeros, as those of K
+        auto check = [&](uint32_t c, int rows) {
+            const uint32_t st = c & 1;
+            wait(&sh.full[st], (c >> 1) & 1);
+            uint8_t *v = sm + kSmV + st * kTile + (g * kWidth >> 6) * kHalf + row * 128;
+            const int first16 = (g * kWidth & 63) >> 3;
+            if (__builtin_expect(rows < kTok, 0)) {
+                if (row >= rows)
+                    for (int j = 0; j < kWidth / 8; ++j)
+                        *(uint4 *)(v + 16 * (first16 + j)) = *(uint4 *)(v - kSmV + kSmK + 16 * (first16 + j)) = make_uint4(0, 0, 0, 0);
+                __syncwarp();
+                named_bar_sync(5, 128 * kGroups);
+            }
+            uint32_t most = 0;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    uint4 *x = (uint4 *)(v + (j >> 3) * kHalf + row * 128 + (((j & 7) ^ (row & 7)) << 4));
-                    if (row < rows) ones |= exponent_of_ones(*x);
-                    else *x = make_uint4(0, 0, 0, 0);
-                }
-                if (!named_bar_and(1, 128, ones == 0)) {
-                    // this thread's channel: its first such row, and zeros in the place of all of them
-                    uint8_t *x = v + (row >> 6) * kHalf + (row & 7) * 2;
+            for (int j = 0; j < kWidth / 8; ++j) {
+                const uint4 x = *(const uint4 *)(v + (((first16 + j) ^ (row & 7)) << 4));
+                most = abs_max2(abs_max2(abs_max2(abs_max2(most, x.x), x.y), x.z), x.w);
+            }
+            if (row == 0) sh.any_odd[g][c & 3] = 0;
+            if (__builtin_expect(!named_bar_and(1 + g, 128, exponent_of_ones(make_uint4(most, 0, 0, 0)) == 0), 0)) {
+                // a channel's first such row, and zeros in the place of all of them
+                if (row < kWidth) {
                     int first = kTok;
                     for (int j = rows - 1; j >= 0; --j) {
-                        uint16_t *u = (uint16_t *)(x + j * 128 + ((((row & 63) >> 3) ^ (j & 7)) << 4));
-                        if ((*u & 0x7f80) == 0x7f80) first = j, *u = 0;
+                        const int ch = 8 * first16 + row;
+                        uint16_t *x = (uint16_t *)(v + (j - row) * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2);
+                        if ((*x & 0x7f80) == 0x7f80) first = j, *x = 0;
                     }
-                    sh.odd[st][row] = (uint8_t)first;
-                    if (row == 0) sh.any_odd[st] = 1;
-                } else if (row == 0) {
-                    sh.any_odd[st] = 0;
+                    sh.odd[c & 3][g * kWidth + row] = (uint8_t)first;
                 }
-                fence_async_smem();
-                mbar_arrive(&sh.v_ready[st]);
-                if (OUTPUT) {
+                if (row == 0) sh.any_odd[g][c & 3] = 1;
+                __syncwarp();
+                named_bar_sync(1 + g, 128);
+            }
+            fence_async_smem();
+            wait(&sh.gates_full[st], (c >> 1) & 1);  // (so that who waits for v_ready has the decays, too)
+            arrive(&sh.v_ready[st]);
+        };
+        // Kt: 32 tokens, block b, into the buffer at tk
+        auto make_kt = [&](uint32_t st, int b, int terms, uint32_t tk, uint64_t *empty, uint32_t parity) {
+            float behind = 0.0f;  // log2 decay of the blocks behind
+            for (int j = b + 1; j < 4; ++j) behind += sh.block[st][j];
+            const float f = exp2f(behind);
+            F2 weight[4];  // of tokens 8 j + 2 (lane % 4), and the one after
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = *(const float2 *)&sh.upper[st][32 * b + 8 * j + 2 * (lane & 3)];
+                weight[j] = f2(x.x * f, x.y * f);
+            }
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {  // 16 channels
+                uint32_t raw[8], term[3][8];
+                const uint32_t from = k_at + st * kTile + 32 * b * 128 + (((unit + 2 * l) ^ turn) << 4);
+                ldmatrix4_trans(raw, from);
+                ldmatrix4_trans(raw + 4, from + 16 * 128);
+                F2 y[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {  // m = 2 j + h
+                    y[m] = mul2(wide(raw[m]), weight[m >> 1]);
+                    term[0][m] = narrow(y[m]);
+                    y[m] = fma2(wide(term[0][m]), f2(-1.0f, -1.0f), y[m]);
+                    term[1][m] = narrow(y[m]);
+                }
+                if (terms == 3) {
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) term[2][m] = narrow(fma2(wide(term[1][m]), f2(-1.0f, -1.0f), y[m]));
+                }
+                if (l == 0) {
+                    wait(empty, parity);
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    if (t < terms) tmem_st_16x16(tk + ((uint32_t)(16 * l) << 16) + t * kTmTerm, term[t]);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+        };
+        if (maker && OUTPUT) {
+            // ---- check of V, Kt
+            uint32_t c = 0;
+            for_items([&](const Item &s, int chunks, int terms) {
+                for (int i = 0; i < chunks; ++i, ++c) {  // (not left early: these warps meet at barriers)
+                    const uint32_t st = c & 1;
+                    check(c, min(kTok, s.rows - i * kTok));
+#pragma unroll 1
+                    for (int e = 0; e < 2; ++e, ++kt) {
+                        make_kt(st, g + 2 * e, terms, tmem + kTmK + g * kTmBuf + lanes, &sh.kt_empty[g], (kt & 1) ^ 1);
+                        arrive(&sh.kt_full[g]);
+                    }
+                    arrive(&sh.k_empty[st]);
+                    arrive(&sh.gates_empty[st]);
+                }
+            });
+        } else if (!OUTPUT) {
+            // ---- check of V, Kt, the state (of the chunk before): a thread stands for a key channel of it
+            uint32_t c = 0;
+            const uint32_t td = tmem + kTmD + 32 * u + lanes;
+            for_items([&](const Item &s, int chunks, int terms) {
+                F2 S[16];  // value channels 32 u + 2 e, and the one after
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[e] = 0;
+                float log_decay = 0.0f, whole = 0.0f;
+                auto update = [&](uint32_t n) {  // by chunk n
+                    wait(&sh.d_full, n & 1);
+                    tc_fence_after();
+                    const float decay = exp2f(whole);
+                    log_decay += whole;
+                    float x[32];
+                    tmem_ld32(td, x);
+                    tmem_ld_wait_for(x);
+                    tc_fence_before();
+                    arrive(&sh.d_empty);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) S[e] = fma2(f2(decay, decay), S[e], f2(x[2 * e], x[2 * e + 1]));
+                    if (__builtin_expect(sh.any_odd[u][n & 3], 0)) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint8_t *from = &sh.odd[n & 3][32 * u + 2 * e];
+                            float lo, hi;
+                            unf2(S[e], lo, hi);
+                            S[e] = f2(from[0] < kTok ? NAN : lo, from[1] < kTok ? NAN : hi);
+                        }
+                    }
+                };
+                for (int i = 0; i < chunks; ++i, ++c) {
+                    const uint32_t st = c & 1;
+                    check(c, min(kTok, s.rows - i * kTok));
+                    make_kt(st, g, terms, tmem + st * (4 * kTmBuf) + g * kTmBuf + lanes, &sh.kt_empty[st], ((c >> 1) & 1) ^ 1);
+                    arrive(&sh.kt_full[st]);
+                    arrive(&sh.k_empty[st]);
+                    if (i > 0) update(c - 1);
+                    whole = sh.block[st][0] + sh.block[st][1] + sh.block[st][2] + sh.block[st][3];
+                    arrive(&sh.gates_empty[st]);
+                }
+                if (chunks > 0) update(c - 1);
+                if (gave_up()) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) S[e] = f2(NAN, NAN);
+                }
+                const int64_t at = (int64_t)s.entry * a.H + s.h;
+                float *out = p.states + at * kState + (int64_t)(32 * u) * kHeadDim + row;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
+                if (u == 0 && row == 0) p.decay[at] = exp2f(log_decay);
+            });
+        } else {
+            // ---- P, the state and the outputs: a thread stands for a row of P, a token of o and a key channel of the state
+            uint32_t c = 0;
+            const uint32_t to = tmem + kTmO + 32 * u + lanes, td = tmem + kTmD + 32 * u + lanes;
+            // outputs that are not taken yet: the last chunk's, from the first of the four rows that four lanes exchange
+            __nv_bfloat16 *o = nullptr;
+            int o_rows = 0;
+            bool o_odd = false;
+            auto take_outputs = [&] {
+                wait(&sh.o_full, (c - 1) & 1);
+                tc_fence_after();
+                uint32_t y[4][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float x[16];
+                    tmem_ld16(to + 16 * n, x);
+                    tmem_ld_wait_for(x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[2 * n + (j >> 2)][j & 3] = pack2(x[2 * j], x[2 * j + 1]);
+                }
+                tc_fence_before();
+                if (__builtin_expect(o_odd | (dead != 0), 0)) {
+                    const bool lost = dead;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (lost || sh.odd[(c - 1) & 3][32 * u + j] <= row) y[j >> 3][(j >> 1) & 3] |= j & 1 ? 0x7fff0000u : 0x7fffu;
+                }
+            // four lanes exchange their units of 16 bytes, so that a store writes 64 bytes of eight rows
+#pragma unroll
+                for (int n = 1; n < 4; n <<= 1) {
+                    const bool up = lane & n;
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        if (!(m & n))
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? y[m][j] : y[m | n][j], n);
+                                if (up) y[m][j] = got; else y[m | n][j] = got;
+                            }
+                }
+                const int64_t step = (int64_t)a.H * kHeadDim;
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if ((row & ~3) + m < o_rows) *(uint4 *)(o + m * step) = make_uint4(y[m][0], y[m][1], y[m][2], y[m][3]);
+            };
+            for_items([&](const Item &s, int chunks, int) {
+                const int64_t place = (int64_t)(32 * u) * kHeadDim + row;  // of this thread's part of a state
+                if (s.slot < 0) {
+                    for (int t = row; t < s.rows; t += kTok) {
+                        uint32_t *to_o = (uint32_t *)((__nv_bfloat16 *)a.o + ((int64_t)(s.first + t) * a.H + s.h) * kHeadDim + 32 * u);
+                        for (int j = 0; j < 16; ++j) to_o[j] = 0x7fc07fc0u;
+                    }
+                    return;
+                }
+                F2 S[16];  // value channels 32 u + 2 e, and the one after
+                const float *init = nullptr;
+                if (!s.begins) init = p.states + ((int64_t)(s.entry - 1) * a.H + s.h) * kState;
+                else if (a.initial_state)
+                    init = s.cut ? p.first + ((int64_t)s.entry * a.H + s.h) * kState : a.initial_state + (s.slot * a.H + s.h) * (int64_t)kState;
+                if (init) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) S[e] = f2(init[place + 2 * e * kHeadDim], init[place + (2 * e + 1) * kHeadDim]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) S[e] = 0;
+                }
+                auto publish = [&] {  // the copy of S that the next chunk's O is taken from
+                    uint8_t *to_s = sm + kSmS + (u >> 1) * kHalf + row * 128;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *(uint4 *)(to_s + (((4 * (u & 1) + j) ^ (row & 7)) << 4)) =
+                            make_uint4(narrow(S[4 * j]), narrow(S[4 * j + 1]), narrow(S[4 * j + 2]), narrow(S[4 * j + 3]));
+                    fence_async_smem();
+                };
+                if (chunks > 0) publish();
+                for (int i = 0; i < chunks; ++i, ++c) {
+                    const uint32_t st = c & 1, full = (c >> 1) & 1;
+                    if (c > 0) take_outputs();
+                    arrive(&sh.o_empty);
+                    wait(&sh.v_ready[st], full);
+                    const bool odd = sh.any_odd[u >> 1][c & 3];
                     const float own = sh.lower[st][row];
+                    float whole = 0.0f, upto = own, before = own;  // before: log2 decay from the end of block u to this row
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const float x = sh.block[st][b];
+                        if (b < w) upto += x;
+                        if (b < w && b > u) before += x;
+                        whole += x;
+                    }
+                    // P: columns 32 u ..
+                    const float f = exp2f(before) * a.scale;
                     wait(&sh.x_full, c & 1);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t u[16];
-                        if (b < w) {
-                            float x[32];
-                            tmem_ld32(tmem + lanes + 32 * b, x);
-                            float before = own;  // log2 decay from the end of block b to this row
-                            for (int j = b + 1; j < w; ++j) before += sh.block[st][j];
-                            const float f = exp2f(before);
-                            tmem_ld_wait_for(x);
+                    for (int e = 0; e < 2; ++e) {
+                        const int j0 = 32 * u + 16 * e;
+                        uint32_t y[8];
+                        if (u <= w) {
+                            float x[16];
+                            tmem_ld16(tmem + lanes + j0, x);
+                            if (u < w) {
+                                tmem_ld_wait_for(x);
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 y = *(const float4 *)&sh.upper[st][32 * b + j];
-                                u[j / 2] = pack2(x[j] * (f * y.x), x[j + 1] * (f * y.y));
-                                u[j / 2 + 1] = pack2(x[j + 2] * (f * y.z), x[j + 3] * (f * y.w));
-                            }
-                        } else if (b == w) {
-                            float x[32];
-                            tmem_ld32(tmem + lanes + 32 * b, x);
-                            tmem_ld_wait_for(x);
+                                for (int j = 0; j < 16; j += 4) {
+                                    const float4 z = *(const float4 *)&sh.upper[st][j0 + j];
+                                    y[j / 2] = narrow(mul2(f2(x[j], x[j + 1]), mul2(f2(z.x, z.y), f2(f, f))));
+                                    y[j / 2 + 1] = narrow(mul2(f2(x[j + 2], x[j + 3]), mul2(f2(z.z, z.w), f2(f, f))));
+                                }
+                            } else {
+                                const int seen = row - j0;  // last column that this row sees
+                                tmem_ld_wait_for(x);
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 y = *(const float4 *)&sh.lower[st][32 * b + j];
-                                x[j] = j <= lane ? x[j] * exp2_sfu(own - y.x) : 0.0f;
-                                x[j + 1] = j + 1 <= lane ? x[j + 1] * exp2_sfu(own - y.y) : 0.0f;
-                                x[j + 2] = j + 2 <= lane ? x[j + 2] * exp2_sfu(own - y.z) : 0.0f;
-                                x[j + 3] = j + 3 <= lane ? x[j + 3] * exp2_sfu(own - y.w) : 0.0f;
-                                u[j / 2] = pack2(x[j], x[j + 1]);
-                                u[j / 2 + 1] = pack2(x[j + 2], x[j + 3]);
+                                for (int j = 0; j < 16; j += 4) {
+                                    const float4 z = *(const float4 *)&sh.lower[st][j0 + j];
+                                    x[j] = j <= seen ? x[j] * (a.scale * exp2_sfu(own - z.x)) : 0.0f;
+                                    x[j + 1] = j + 1 <= seen ? x[j + 1] * (a.scale * exp2_sfu(own - z.y)) : 0.0f;
+                                    x[j + 2] = j + 2 <= seen ? x[j + 2] * (a.scale * exp2_sfu(own - z.z)) : 0.0f;
+                                    x[j + 3] = j + 3 <= seen ? x[j + 3] * (a.scale * exp2_sfu(own - z.w)) : 0.0f;
+                                    y[j / 2] = pack2(x[j], x[j + 1]);
+                                    y[j / 2 + 1] = pack2(x[j + 2], x[j + 3]);
+                                }
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) u[j] = 0;
+                            for (int j = 0; j < 8; ++j) y[j] = 0;
                         }
-                        tmem_st16(tmem + lanes + 16 * b, u);
+                        tmem_st8(tmem + lanes + 32 * u + 8 * e, y);  // over scores of the block that are read
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive(&sh.p_full);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.gates_empty[st]);
-            }
-        });
-    } else if (wid >= 12) {
-        // ---- the state (a thread takes a key channel) and the outputs (a token), 64 value channels each
-        uint32_t c = 0;
-        const int half = (wid - 12) >> 2, w = wid & 3, row = 32 * w + lane;
-        const uint32_t lanes = (uint32_t)(w * 32) << 16;
-        const uint32_t to = tmem + kTmO + 64 * half + lanes, td = tmem + kTmD + 64 * half + lanes;
-        for_items([&](const Item &s, int chunks) {
-            const int64_t place = (int64_t)(64 * half) * kHeadDim + row;  // of this thread's part of a state
-            if (s.slot < 0) {
-                for (int t = row; t < s.rows; t += kTok) {
-                    uint32_t *o = (uint32_t *)((__nv_bfloat16 *)a.o + ((int64_t)(s.first + t) * a.H + s.h) * kHeadDim + 64 * half);
-                    for (int j = 0; j < 32; ++j) o[j] = 0x7fc07fc0u;
-                }
-                return;
-            }
-            float S[64];
-            const float *init = nullptr;
-            if (OUTPUT) {
-                const int64_t in_pool = (s.slot * a.H + s.h) * (int64_t)kState;
-                if (!s.begins) init = p.states + ((int64_t)(s.entry - 1) * a.H + s.h) * kState;
-                else if (a.initial_state) init = s.cut ? p.first + ((int64_t)s.entry * a.H + s.h) * kState : a.initial_state + in_pool;
-            }
-            if (init) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e) S[e] = init[place + e * kHeadDim];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 64; ++e) S[e] = 0.0f;
-            }
-            float log_decay = 0.0f;
-            auto publish = [&] {  // the copy of S that the next chunk's O is taken from
-                uint8_t *to_s = sm + kSmS + half * kHalf + row * 128;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *(uint4 *)(to_s + ((j ^ (row & 7)) << 4)) =
-                        make_uint4(pack2(S[8 * j], S[8 * j + 1]), pack2(S[8 * j + 2], S[8 * j + 3]),
-                                   pack2(S[8 * j + 4], S[8 * j + 5]), pack2(S[8 * j + 6], S[8 * j + 7]));
-                fence_async_smem();
-                mbar_arrive(&sh.s_full);
-            };
-            if (OUTPUT && chunks > 0) publish();
-            for (int i = 0; i < chunks; ++i, ++c) {
-                const uint32_t st = c & 1, full = (c >> 1) & 1;
-                const int rows = min(kTok, s.rows - i * kTok);
-                wait(&sh.gates_full[st], full);
-                wait(&sh.v_ready[st], full);
-                float whole = 0.0f, upto = sh.lower[st][row];
-                for (int b = 0; b < 4; ++b) {
-                    if (b < w) upto += sh.block[st][b];
-                    whole += sh.block[st][b];
-                }
-                if (OUTPUT) {
-                    const float f = exp2f(upto);
+                    arrive(&sh.gates_empty[st]);
+                    // O so far, Q . S, times the row's decay
+                    const float to_row = exp2f(upto) * a.scale;
                     wait(&sh.qs_full, c & 1);
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         float x[16];
                         tmem_ld16(to + 16 * k, x);
                         tmem_ld_wait_for(x);
-                        uint32_t u[16];
+                        uint32_t y[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(x[j] * f);
-                        tmem_st16(to + 16 * k, u);
+                        for (int j = 0; j < 16; j += 2) {
+                            float lo, hi;
+                            unf2(mul2(f2(x[j], x[j + 1]), f2(to_row, to_row)), lo, hi);
+                            y[j] = __float_as_uint(lo), y[j + 1] = __float_as_uint(hi);
+                        }
+                        tmem_st16(to + 16 * k, y);
                     }
                     tmem_st_wait();
                     tc_fence_before();
-                    mbar_arrive(&sh.o_scaled);
-                } else {
-                    log_decay += whole;
-                }
-                const float decay = exp2f(whole);
-                wait(&sh.d_full, c & 1);
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float x[16];
-                    tmem_ld16(td + 16 * k, x);
-                    tmem_ld_wait_for(x);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) S[16 * k + j] = fmaf(decay, S[16 * k + j], x[j]);
-                }
-                tc_fence_before();
-                mbar_arrive(&sh.d_empty);
-                const bool odd = sh.any_odd[st];
-                if (odd) {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (sh.odd[st][64 * half + e] < kTok) S[e] = NAN;
-                }
-                if (OUTPUT) {
-                    if (i + 1 < chunks) publish();
-                    wait(&sh.o_full, c & 1);
+                    arrive(&sh.pv_ready);
+                    o = (__nv_bfloat16 *)a.o + ((int64_t)(s.first + i * kTok + (row & ~3)) * a.H + s.h) * kHeadDim + 32 * u +
+                        8 * (lane & 3);
+                    o_rows = min(kTok, s.rows - i * kTok);
+                    o_odd = odd;
+                    // the state
+                    const float decay = exp2f(whole);
+                    wait(&sh.d_full, c & 1);
                     tc_fence_after();
-                    const bool lost = gave_up();
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float x[32];
-                        tmem_ld32(to + 32 * k, x);
+                        float x[16];
+                        tmem_ld16(td + 16 * k, x);
                         tmem_ld_wait_for(x);
-                        if (k == 1) {
-                            tc_fence_before();
-                            mbar_arrive(&sh.o_empty);
-                        }
-                        uint32_t u[4][4];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j >> 2][j & 3] = pack2(x[2 * j] * a.scale, x[2 * j + 1] * a.scale);
-                        if (odd) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (sh.odd[st][64 * half + 32 * k + j] <= row) u[j >> 3][(j >> 1) & 3] |= j & 1 ? 0x7fff0000u : 0x7fffu;
-                        }
-                        if (lost) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) u[j >> 2][j & 3] = 0x7fff7fffu;
-                        }
-                        // four lanes exchange their units of 16 bytes, so that a store writes 64 bytes of eight rows
-#pragma unroll
-                        for (int o = 1; o < 4; o <<= 1) {
-                            const bool up = lane & o;
-#pragma unroll
-                            for (int m = 0; m < 4; ++m)
-                                if (!(m & o))
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? u[m][j] : u[m | o][j], o);
-                                        if (up) u[m][j] = got; else u[m | o][j] = got;
-                                    }
-                        }
-                        const int t0 = 32 * w + (lane & ~3);
-                        __nv_bfloat16 *o = (__nv_bfloat16 *)a.o + ((int64_t)(s.first + i * kTok + t0) * a.H + s.h) * kHeadDim +
-                                           64 * half + 32 * k + 8 * (lane & 3);
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            if (t0 + m < rows)
-                                *(uint4 *)(o + (int64_t)m * a.H * kHeadDim) = make_uint4(u[m][0], u[m][1], u[m][2], u[m][3]);
+                        for (int j = 0; j < 8; ++j) S[8 * k + j] = fma2(f2(decay, decay), S[8 * k + j], f2(x[2 * j], x[2 * j + 1]));
                     }
+                    tc_fence_before();
+                    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint8_t *from = &sh.odd[c & 3][32 * u + 2 * e];
+                            float lo, hi;
+                            unf2(S[e], lo, hi);
+                            S[e] = f2(from[0] < kTok ? NAN : lo, from[1] < kTok ? NAN : hi);
+                        }
+                    }
+                    // (what follows it, the next chunk's D, is what keeps the check of V from writing `odd` four chunks on
+                    // before these warps have taken that chunk's outputs)
+                    arrive(&sh.d_empty);
+                    if (i + 1 < chunks) publish();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.gates_empty[st]);
-            }
-            if (gave_up()) {
+                if (gave_up()) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) S[e] = NAN;
-            }
-            float *out = nullptr;
-            if (!OUTPUT) out = p.states + ((int64_t)s.entry * a.H + s.h) * kState;
-            else if (s.ends && a.final_state) out = a.final_state + (s.slot * a.H + s.h) * (int64_t)kState;
-            if (out) {
+                    for (int e = 0; e < 16; ++e) S[e] = f2(NAN, NAN);
+                }
+                if (s.ends && a.final_state) {
+                    float *out = a.final_state + (s.slot * a.H + s.h) * (int64_t)kState + place;
 #pragma unroll
-                for (int e = 0; e < 64; ++e) out[place + e * kHeadDim] = S[e];
-            }
-            if (!OUTPUT && half == 0 && row == 0) p.decay[(int64_t)s.entry * a.H + s.h] = exp2f(log_decay);
-        });
+                    for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
+                }
+            });
+            if (c > 0) take_outputs();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -628,35 +761,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The states in front of the segments of each sequence that is cut, in place of the segments' own: entry l gets
 // that in front of segment l + 1.  A sequence's initial state is copied, because its last segment may
 // overwrite it while the first one still reads.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinParts = kState / (4 * kJoinThreads);
 __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const ChunkParams p) {
     griddep_wait();
     griddep_launch_dependents();
     const LinearChunkArgs &a = p.a;
     const int h = blockIdx.y;
-    Item s;
-    if (!state_item(p, blockIdx.x, s) || !s.begins) return;
-    const Span span = span_of(a, s.n);
-    const int count = (span.len - 1) / p.segment;  // entries
-    const int64_t at = (int64_t)blockIdx.z * kJoinThreads + threadIdx.x;
-    const int64_t step = (int64_t)a.H * kState;
-    float x = 0.0f;
-    const int64_t own = ((int64_t)s.entry * a.H + h) * kState + at;
-    if (a.initial_state) {
-        x = a.initial_state[(s.slot * a.H + h) * (int64_t)kState + at];
-        p.first[own] = x;
-    }
-    float *state = p.states + own;
-    const float *decay = p.decay + (int64_t)s.entry * a.H + h;
-    constexpr int kAhead = 8;
-    for (int l = 0; l < count; l += kAhead) {
-        float y[kAhead], d[kAhead];
+    for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
+        const Span span = span_of(a, n);
+        const int64_t slot = slot_of(a, n);
+        if (span.len <= p.segment || slot < 0) continue;
+        const int count = (span.len - 1) / p.segment, entry = span.first / p.segment;
+        const int64_t at = 4 * ((int64_t)blockIdx.z * kJoinThreads + threadIdx.x);
+        const int64_t step = (int64_t)a.H * kState, own = ((int64_t)entry * a.H + h) * kState + at;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.initial_state) {
+            x = *(const float4 *)(a.initial_state + (slot * a.H + h) * (int64_t)kState + at);
+            *(float4 *)(p.first + own) = x;
+        }
+        float *state = p.states + own;
+        const float *decay = p.decay + (int64_t)entry * a.H + h;
+        constexpr int kAhead = 8;
+        for (int l = 0; l < count; l += kAhead) {
+            float4 y[kAhead];
+            float d[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (l + j < count) y[j] = state[(l + j) * step], d[j] = decay[(int64_t)(l + j) * a.H];
+            for (int j = 0; j < kAhead; ++j)
+                if (l + j < count) y[j] = *(const float4 *)(state + (l + j) * step), d[j] = decay[(int64_t)(l + j) * a.H];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (l + j < count) state[(l + j) * step] = x = fmaf(d[j], x, y[j]);
+            for (int j = 0; j < kAhead; ++j) {
+                if (l + j >= count) break;
+                x.x = fmaf(d[j], x.x, y[j].x), x.y = fmaf(d[j], x.y, y[j].y);
+                x.z = fmaf(d[j], x.z, y[j].z), x.w = fmaf(d[j], x.w, y[j].w);
+                *(float4 *)(state + (l + j) * step) = x;
+            }
+        }
     }
 }
 
@@ -695,20 +834,20 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
     p.states = (float *)a.workspace;
     p.first = p.states + entries * a.H * kState;
     p.decay = p.first + entries * a.H * kState;
-    auto launch = [&](auto kernel, int64_t items) {
+    auto launch = [&](auto kernel, int threads, int64_t items) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         return e != cudaSuccess ? e
-                                : launch_dependent(kernel, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(kThreads),
+                                : launch_dependent(kernel, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(threads),
                                                    kSmemBytes, stream, map_q, map_k, map_v, p);
     };
     if (entries > 0) {
-        cudaError_t e = launch(linear_chunk_kernel<false>, entries * a.H);
+        cudaError_t e = launch(linear_chunk_kernel<false>, 640, entries * a.H);
         if (e == cudaSuccess)
-            e = launch_dependent(linear_join_kernel, dim3((unsigned)entries, (unsigned)a.H, kState / kJoinThreads),
+            e = launch_dependent(linear_join_kernel, dim3((unsigned)std::min(a.n_seqs, 4096), (unsigned)a.H, kJoinParts),
                                  dim3(kJoinThreads), 0, stream, p);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t e = launch(linear_chunk_kernel<true>, p.items);
+    const cudaError_t e = launch(linear_chunk_kernel<true>, 896, p.items);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
