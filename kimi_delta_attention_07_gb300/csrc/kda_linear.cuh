@@ -37,6 +37,7 @@ struct LinearChunkArgs {
     int H, group;  // group: heads that share q and k
     float scale;
     void *workspace;
+    int equal_len;  // of each sequence, without cu_seqlens
 };
 size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H);
 // bf16 on the tensor cores; fp32 on the CUDA cores (no workspace)
@@ -63,8 +64,7 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const LinearChunkArgs &a, int n) {
     if (!a.cu_seqlens) {
-        const int len = (int)(a.total_tokens / a.n_seqs);
-        return {n * len, len};
+        return {n * a.equal_len, a.equal_len};
     }
     const int from = a.cu_seqlens[n], to = a.cu_seqlens[n + 1];
     const bool ok = from >= 0 && to >= from && to <= a.total_tokens;

@@ -118,7 +118,8 @@ int kda_linear_chunk_fwd(const void *q, int64_t q_stride, const void *k, int64_t
     const size_t need = kda_linear_chunk_workspace_bytes(total_tokens, n_seqs, H, dtype);
     if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     const LinearChunkArgs a{q, k, v, q_stride, k_stride, v_stride, g, g_stride, initial_state, final_state,
-                            state_indices, n_slots, o, cu_seqlens, n_seqs, total_tokens, H, H / Hk, scale, workspace};
+                            state_indices, n_slots, o, cu_seqlens, n_seqs, total_tokens, H, H / Hk, scale, workspace,
+                            (int)(total_tokens / n_seqs)};
     return launched([&] {
         return dtype == KDA_BF16 ? launch_linear_chunk_tc(a, (cudaStream_t)stream) : launch_linear_chunk_f32(a, (cudaStream_t)stream);
     });

@@ -57,15 +57,17 @@ constexpr uint32_t kTile = 32768;        // 128 tokens x 128 channels: two block
 constexpr uint32_t kHalf = kTile / 2;
 constexpr int kState = kHeadDim * kHeadDim;
 
-// shared memory (from a 1024-byte boundary): two stages of K, Q, V; the copy of S
-constexpr uint32_t kSmK = 0, kSmQ = 2 * kTile, kSmV = 4 * kTile, kSmS = 6 * kTile, kSmShared = 7 * kTile;
+// shared memory (from a 1024-byte boundary): two stages of K, V, Q and the copy of S; without outputs three of K, V
+constexpr uint32_t kSmQ = 4 * kTile, kSmS = 6 * kTile, kSmShared = 7 * kTile;
+__device__ __forceinline__ constexpr uint32_t tile_k(uint32_t st) { return 2 * st * kTile; }
+__device__ __forceinline__ constexpr uint32_t tile_v(uint32_t st) { return (2 * st + 1) * kTile; }
 
 // TMEM columns: X and P (block b of P over the first 16 columns of its scores), O, D, buffers of 32 tokens of Kt in three
 // terms of 16 columns.  Without outputs eight buffers, over X and O as well.
 constexpr uint32_t kTmO = 128, kTmD = 384, kTmK = 256, kTmTerm = 16, kTmBuf = 48;
 
 struct Shared {
-    uint64_t full[2], k_empty[2], q_empty[2], v_empty[2], gates_full[2], gates_empty[2], v_ready[2], kt_full[2], kt_empty[2],
+    uint64_t k_full[3], v_full[3], k_empty[3], v_empty[3], v_ready[3], q_empty[2], gates_full[2], gates_empty[2], kt_full[2], kt_empty[2],
         x_full, qs_full, pv_ready, o_full, o_empty, d_full, d_empty;
     alignas(16) float lower[2][kTok];  // log2 decay of a token's block up to and with it
     float upper[2][kTok];              // decay of a token's block behind it
@@ -81,7 +83,8 @@ struct ChunkParams {
     LinearChunkArgs a;
     int segment;     // tokens
     int entries;     // segments whose state the workspace holds, at most
-    int64_t items;   // of the kernel with outputs: (segment, head)
+    uint32_t items;  // (segment, head) pairs of the kernel with outputs
+    bool joined;     // it follows the others: its inputs are there before it begins
     float *states;   // [entries][H][V][K]
     float *first;    // [entries][H][V][K]: copies of initial states (those that a later CTA may overwrite)
     float *decay;    // [entries][H]
@@ -136,16 +139,16 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
     return r;
 }
 __device__ __forceinline__ int offset_of(const LinearChunkArgs &a, int n) {
-    return a.cu_seqlens ? a.cu_seqlens[n] : n * (int)(a.total_tokens / a.n_seqs);
+    return a.cu_seqlens ? a.cu_seqlens[n] : n * a.equal_len;
 }
 
 // The last sequence n with bound(n) <= at, by the warp's 32 lanes together (bound(0) <= at).
 template <typename F>
-__device__ __forceinline__ int last_below(int n_seqs, int64_t at, F bound) {
+__device__ __forceinline__ int last_below(int n_seqs, int at, F bound) {
     const int lane = threadIdx.x & 31;
     int lo = 0, span = n_seqs;  // in [lo, lo + span)
     while (span > 1) {
-        const int step = (span + 31) / 32, n = lo + lane * step;
+        const int step = (span + 31) >> 5, n = lo + lane * step;
         const bool below = n < lo + span && (lane == 0 || bound(n) <= at);
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
         lo += last * step;
@@ -154,48 +157,38 @@ __device__ __forceinline__ int last_below(int n_seqs, int64_t at, F bound) {
     return lo;
 }
 
-struct Item {
-    int n, h, first, rows;  // first token, tokens (0: nothing to compute)
-    int64_t slot;           // of the sequence's states, -1: none
-    int entry;              // of this segment in the workspace
-    bool begins, ends, cut; // the sequence's first and last segment; whether it has several
-};
+// A segment (and head) to work on, in four registers: what warps look at in every chunk must not be in
+// local memory, for which the L1 cache has no room beside this shared memory.
+enum : uint32_t { kBegins = 1u << 16, kEnds = 1u << 17, kCut = 1u << 18, kNoSlot = 1u << 19 };
+typedef int4 Item;  // first token, tokens (-1: no such segment), sequence, head and flags
+__device__ __forceinline__ int head_of(const Item &s) { return s.w & 0xffff; }
 
 // Segment (and head) `i` of the kernel with outputs.  Sequence n's segments are numbered from
-// floor(offset / segment) + n on, which leaves room for all of them whatever the lengths; false: no such segment.
-__device__ __noinline__ bool output_item(const ChunkParams &p, int64_t i, Item &s) {
-    const LinearChunkArgs &a = p.a;
-    const int64_t rank = i / a.H;
-    s.h = (int)(i - rank * a.H);
-    s.n = last_below(a.n_seqs, rank, [&](int n) { return (int64_t)(offset_of(a, n) / p.segment) + n; });
-    const Span span = span_of(a, s.n);
-    const int l = (int)(rank - span.first / p.segment - s.n);
-    const int count = max(1, (span.len + p.segment - 1) / p.segment);
-    if (span.len < 0 || l < 0 || l >= count) return false;
-    s.first = span.first + l * p.segment;
-    s.rows = min(p.segment, span.len - l * p.segment);
-    s.slot = slot_of(a, s.n);
-    s.entry = span.first / p.segment + l;
-    s.begins = l == 0, s.ends = l == count - 1, s.cut = count > 1;
-    return true;
+// floor(offset / segment) + n on, which leaves room for all of them whatever the lengths.  The segment's entry in the
+// workspace is floor(first / segment).
+__device__ __noinline__ Item output_item(const LinearChunkArgs &a, uint32_t segment, uint32_t i) {
+    const uint32_t rank = i / (uint32_t)a.H, h = i - rank * a.H;
+    const int n = last_below(a.n_seqs, rank, [&](int n) { return (int)((uint32_t)offset_of(a, n) / segment) + n; });
+    const bool slot = slot_of(a, n) >= 0;
+    const Span span = span_of(a, n);
+    const int l = rank - (uint32_t)span.first / segment - n, count = max(1u, (span.len + segment - 1) / segment);
+    if (span.len < 0 || l < 0 || l >= count) return make_int4(0, -1, 0, 0);
+    return make_int4(span.first + l * segment, min((int)segment, span.len - l * (int)segment), n,
+                     h | (l == 0 ? kBegins : 0) | (l == count - 1 ? kEnds : 0) | (count > 1 ? kCut : 0) | (slot ? 0 : kNoSlot));
 }
 
-// Segment of entry m, if it is one that others follow in its sequence: the one that token
-// (m + 1) segment - 1 lies in, or ends with.
-__device__ __noinline__ bool state_item(const ChunkParams &p, int m, Item &s) {
-    const LinearChunkArgs &a = p.a;
-    const int64_t x = (int64_t)(m + 1) * p.segment;
-    s.n = last_below(a.n_seqs, x, [&](int n) { return (int64_t)offset_of(a, n); });
-    const Span span = span_of(a, s.n);
-    if (span.len < 0 || x <= span.first) return false;
-    const int64_t l = (x - span.first - 1) / p.segment;
-    if ((l + 1) * p.segment >= span.len) return false;
-    s.first = span.first + (int)l * p.segment;
-    s.rows = p.segment;
-    s.slot = slot_of(a, s.n);
-    s.entry = m;
-    s.begins = l == 0, s.ends = false, s.cut = true;
-    return s.slot >= 0;
+// Segment of entry m = i / H, if it is one that others follow in its sequence: the one that holds token
+// (m + 1) segment - 1.
+__device__ __noinline__ Item state_item(const LinearChunkArgs &a, uint32_t segment, uint32_t i) {
+    const uint32_t m = i / (uint32_t)a.H, h = i - m * a.H;
+    const int x = (m + 1) * segment;
+    const int n = last_below(a.n_seqs, x, [&](int n) { return offset_of(a, n); });
+    const bool slot = slot_of(a, n) >= 0;
+    const Span span = span_of(a, n);
+    if (span.len < 0 || x <= span.first) return make_int4(0, -1, 0, 0);
+    const int l = (uint32_t)(x - span.first - 1) / segment, from = l * segment;
+    if (span.len - from <= (int)segment || !slot) return make_int4(0, -1, 0, 0);
+    return make_int4(span.first + from, segment, n, h | kCut);
 }
 
 // OUTPUT: o and final states, from the states in front of the segments; else a segment's own state.
@@ -203,16 +196,19 @@ template <bool OUTPUT>
 __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const ChunkParams p) {
+    constexpr uint32_t kStages = OUTPUT ? 2 : 3;
     extern __shared__ __align__(1024) uint8_t sm[];
     Shared &sh = *reinterpret_cast<Shared *>(sm + kSmShared);
     volatile int &dead = sh.dead;
     const LinearChunkArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.full[i], 1), mbar_init(&sh.k_empty[i], OUTPUT ? 9 : 16), mbar_init(&sh.q_empty[i], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&sh.k_full[i], 1), mbar_init(&sh.v_full[i], 1), mbar_init(&sh.k_empty[i], OUTPUT ? 9 : 16);
             mbar_init(&sh.v_empty[i], OUTPUT ? 2 : 1), mbar_init(&sh.v_ready[i], OUTPUT ? 8 : 16);
-            mbar_init(&sh.gates_full[i], 1), mbar_init(&sh.gates_empty[i], OUTPUT ? 24 : 16);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.q_empty[i], 1), mbar_init(&sh.gates_full[i], 1), mbar_init(&sh.gates_empty[i], OUTPUT ? 24 : 16);
             mbar_init(&sh.kt_full[i], OUTPUT ? 4 : 16), mbar_init(&sh.kt_empty[i], 1);
         }
         mbar_init(&sh.x_full, 1), mbar_init(&sh.qs_full, 1), mbar_init(&sh.pv_ready, 16);
@@ -225,7 +221,9 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
-    griddep_wait();
+    // Behind the join only the states in front of the segments are awaited (by the warps that read them, and
+    // write what it reads): the join itself began when all before it was done.
+    if (!OUTPUT || !p.joined || wid >= 12) griddep_wait();
     griddep_launch_dependents();
 
     // a bounded wait; once one has given up, none waits any more
@@ -241,18 +239,12 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     auto gave_up = [&] { return __any_sync(0xffffffffu, dead); };
     // f(item, chunks) for each of this CTA's items, in the same order by every warp
     auto for_items = [&](auto f) {
-        const int64_t items = OUTPUT ? p.items : (int64_t)p.entries * a.H;
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-            Item s;
-            if (OUTPUT) {
-                if (!output_item(p, i, s)) continue;
-            } else {
-                const int m = (int)(i / a.H);
-                s.h = (int)(i - (int64_t)m * a.H);
-                if (!state_item(p, m, s)) continue;
-            }
+        const uint32_t items = OUTPUT ? p.items : (uint32_t)p.entries * a.H;
+        for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
+            const Item s = OUTPUT ? output_item(a, p.segment, i) : state_item(a, p.segment, i);
+            if (s.y < 0) continue;
             // a segment whose states serve o alone does without the third term
-            f(s, s.slot < 0 ? 0 : (s.rows + kTok - 1) / kTok, OUTPUT && s.cut && !s.ends ? 2 : 3);
+            f(s, s.w & kNoSlot ? 0 : (s.y + kTok - 1) / kTok, OUTPUT && (s.w & (kCut | kEnds)) == kCut ? 2 : 3);
         }
     };
 
@@ -260,23 +252,25 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
         // ---- TMA
         uint32_t c = 0;
         for_items([&](const Item &s, int chunks, int terms) {
-            const int hk = s.h / a.group;
+            const int hk = (uint32_t)head_of(s) / (uint32_t)a.group;
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
-                const uint32_t st = c & 1, before = ((c >> 1) & 1) ^ 1;
-                const int row = s.first + i * kTok;
+                const uint32_t st = c % kStages, before = ((c / kStages) & 1) ^ 1;
+                const int row = s.x + i * kTok;
+                auto load = [&](uint32_t at, const CUtensorMap *map, int head, uint64_t *bar) {
+                    tma_load_3d(sm + at, map, 0, head, row, bar);
+                    tma_load_3d(sm + at + kHalf, map, 64, head, row, bar);
+                };
                 wait(&sh.k_empty[st], before);
                 if (OUTPUT) wait(&sh.q_empty[st], before);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sh.k_full[st], OUTPUT ? 2 * kTile : kTile);
+                    load(tile_k(st), &map_k, hk, &sh.k_full[st]);
+                    if (OUTPUT) load(kSmQ + st * kTile, &map_q, hk, &sh.k_full[st]);
+                }
                 wait(&sh.v_empty[st], before);
                 if (elect_one()) {
-                    uint64_t *bar = &sh.full[st];
-                    mbar_arrive_expect_tx(bar, OUTPUT ? 3 * kTile : 2 * kTile);
-#pragma unroll 1
-                    for (int b = 0; b < 2; ++b) {
-                        uint8_t *to = sm + st * kTile + b * kHalf;
-                        tma_load_3d(to + kSmK, &map_k, 64 * b, hk, row, bar);
-                        if (OUTPUT) tma_load_3d(to + kSmQ, &map_q, 64 * b, hk, row, bar);
-                        tma_load_3d(to + kSmV, &map_v, 64 * b, s.h, row, bar);
-                    }
+                    mbar_arrive_expect_tx(&sh.v_full[st], kTile);
+                    load(tile_v(st), &map_v, head_of(s), &sh.v_full[st]);
                 }
                 __syncwarp();
             }
@@ -284,16 +278,16 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     } else if (wid == 1 && OUTPUT) {
         // ---- MMA of X and O
         uint32_t c = 0;
-        const uint32_t q0 = smem_u32(sm + kSmQ), k0 = smem_u32(sm + kSmK), s0 = smem_u32(sm + kSmS);
-        const uint32_t v_lo = (smem_u32(sm + kSmV) >> 4) | ((kHalf >> 4) << 16);
+        const uint32_t q0 = smem_u32(sm + kSmQ), k0 = smem_u32(sm), s0 = smem_u32(sm + kSmS);
+        const uint32_t v_lo = (smem_u32(sm) >> 4) | ((kHalf >> 4) << 16);
         for_items([&](const Item &s, int chunks, int terms) {
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
                 const uint32_t st = c & 1, full = (c >> 1) & 1;
-                wait(&sh.full[st], full);
+                wait(&sh.k_full[st], full);
                 if (c > 0) wait(&sh.o_full, (c - 1) & 1);  // P of the chunk before is read
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_tile<kTok, kTok, kHeadDim, kTok, kTok>(tmem, q0 + st * kTile, k0 + st * kTile, false);
+                    mma_tile<kTok, kTok, kHeadDim, kTok, kTok>(tmem, q0 + st * kTile, k0 + tile_k(st), false);
                     mma_commit(&sh.k_empty[st]);
                     mma_commit(&sh.x_full);
                 }
@@ -313,7 +307,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 #pragma unroll
                     for (int j = 0; j < kTok / 16; ++j)
                         mma_bf16_ts(tmem + kTmO, tmem + 32 * (j >> 1) + 8 * (j & 1),
-                                    ((uint64_t)kDescHi << 32) | (uint64_t)(v_lo + st * (kTile >> 4) + 128 * j), idesc, 1);
+                                    ((uint64_t)kDescHi << 32) | (uint64_t)(v_lo + (tile_v(st) >> 4) + 128 * j), idesc, 1);
                     mma_commit(&sh.v_empty[st]);
                     mma_commit(&sh.o_full);
                 }
@@ -324,13 +318,13 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
         // ---- MMA of D
         // Kt comes in quarters through two buffers, or (without outputs) in whole chunks, likewise
         uint32_t c = 0, kt = 0;
-        const uint32_t v_lo = (smem_u32(sm + kSmV) >> 4) | ((kHalf >> 4) << 16);
+        const uint32_t v_lo = (smem_u32(sm) >> 4) | ((kHalf >> 4) << 16);
         constexpr int kParts = OUTPUT ? 4 : 1;
         for_items([&](const Item &s, int chunks, int terms) {
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
-                const uint32_t st = c & 1;
-                const int steps = (min(kTok, s.rows - i * kTok) + 15) / 16;
-                wait(&sh.v_ready[st], (c >> 1) & 1);
+                const uint32_t st = c % kStages;
+                const int steps = (min(kTok, s.y - i * kTok) + 15) / 16;
+                wait(&sh.v_ready[st], (c / kStages) & 1);
                 if (c > 0) wait(&sh.d_empty, (c - 1) & 1);
 #pragma unroll 1
                 for (int b = 0; b < kParts; ++b, ++kt) {
@@ -340,7 +334,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                         constexpr uint32_t idesc = idesc_bf16(kTok, kTok) | (1u << 16);
                         constexpr int kSteps = 8 / kParts;
                         const uint32_t k_at = tmem + (OUTPUT ? kTmK : 0) + (kt & 1) * (kTmBuf * (4 / kParts));
-                        const uint32_t v_at = v_lo + st * (kTile >> 4) + 256 * b;
+                        const uint32_t v_at = v_lo + (tile_v(st) >> 4) + 256 * b;
 #pragma unroll 1
                         for (int j = 0; j < kSteps && kSteps * b + j < steps; ++j)
 #pragma unroll 1
@@ -367,7 +361,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const int t = i * kTok + 32 * b + lane;
-                    g[b] = t < s.rows ? a.g[(int64_t)(s.first + t) * a.g_stride + s.h] * kLog2e : 0.0f;
+                    g[b] = t < s.y ? a.g[(int64_t)(s.x + t) * a.g_stride + head_of(s)] * kLog2e : 0.0f;
                 }
                 float lower[4], upper[4];
 #pragma unroll
@@ -403,20 +397,21 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
         const uint32_t lanes = (uint32_t)(w * 32) << 16;
         // Kt: this lane's address of a matrix row (matrix 2 j + h: tokens 8 j .., channels 8 h .. of 16)
         const int token = 8 * (lane >> 4) + (lane & 7), channel = 32 * w + 8 * ((lane >> 3) & 1);
-        const uint32_t k_at = smem_u32(sm + kSmK) + (channel >> 6) * kHalf + token * 128;
+        const uint32_t k_at = smem_u32(sm) + (channel >> 6) * kHalf + token * 128;
         const uint32_t unit = (channel & 63) >> 3, turn = token & 7;
         uint32_t kt = 0;
 
         // V: kWidth channels of this thread's row; rows past the sequence's end become zeros, as those of K
         auto check = [&](uint32_t c, int rows) {
-            const uint32_t st = c & 1;
-            wait(&sh.full[st], (c >> 1) & 1);
-            uint8_t *v = sm + kSmV + st * kTile + (g * kWidth >> 6) * kHalf + row * 128;
+            const uint32_t st = c % kStages, full = (c / kStages) & 1;
+            wait(&sh.k_full[st], full);
+            wait(&sh.v_full[st], full);
+            uint8_t *v = sm + tile_v(st) + (g * kWidth >> 6) * kHalf + row * 128;
             const int first16 = (g * kWidth & 63) >> 3;
             if (__builtin_expect(rows < kTok, 0)) {
                 if (row >= rows)
                     for (int j = 0; j < kWidth / 8; ++j)
-                        *(uint4 *)(v + 16 * (first16 + j)) = *(uint4 *)(v - kSmV + kSmK + 16 * (first16 + j)) = make_uint4(0, 0, 0, 0);
+                        *(uint4 *)(v + 16 * (first16 + j)) = *(uint4 *)(v - kTile + 16 * (first16 + j)) = make_uint4(0, 0, 0, 0);
                 __syncwarp();
                 named_bar_sync(5, 128 * kGroups);
             }
@@ -443,24 +438,24 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                 named_bar_sync(1 + g, 128);
             }
             fence_async_smem();
-            wait(&sh.gates_full[st], (c >> 1) & 1);  // (so that who waits for v_ready has the decays, too)
+            wait(&sh.gates_full[c & 1], (c >> 1) & 1);  // (so that who waits for v_ready has the decays, too)
             arrive(&sh.v_ready[st]);
         };
         // Kt: 32 tokens, block b, into the buffer at tk
-        auto make_kt = [&](uint32_t st, int b, int terms, uint32_t tk, uint64_t *empty, uint32_t parity) {
+        auto make_kt = [&](uint32_t c, int b, int terms, uint32_t tk, uint64_t *empty, uint32_t parity) {
             float behind = 0.0f;  // log2 decay of the blocks behind
-            for (int j = b + 1; j < 4; ++j) behind += sh.block[st][j];
+            for (int j = b + 1; j < 4; ++j) behind += sh.block[c & 1][j];
             const float f = exp2f(behind);
             F2 weight[4];  // of tokens 8 j + 2 (lane % 4), and the one after
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 x = *(const float2 *)&sh.upper[st][32 * b + 8 * j + 2 * (lane & 3)];
+                const float2 x = *(const float2 *)&sh.upper[c & 1][32 * b + 8 * j + 2 * (lane & 3)];
                 weight[j] = f2(x.x * f, x.y * f);
             }
 #pragma unroll
             for (int l = 0; l < 2; ++l) {  // 16 channels
                 uint32_t raw[8], term[3][8];
-                const uint32_t from = k_at + st * kTile + 32 * b * 128 + (((unit + 2 * l) ^ turn) << 4);
+                const uint32_t from = k_at + tile_k(c % kStages) + 32 * b * 128 + (((unit + 2 * l) ^ turn) << 4);
                 ldmatrix4_trans(raw, from);
                 ldmatrix4_trans(raw + 4, from + 16 * 128);
                 F2 y[8];
@@ -491,15 +486,14 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             uint32_t c = 0;
             for_items([&](const Item &s, int chunks, int terms) {
                 for (int i = 0; i < chunks; ++i, ++c) {  // (not left early: these warps meet at barriers)
-                    const uint32_t st = c & 1;
-                    check(c, min(kTok, s.rows - i * kTok));
+                    check(c, min(kTok, s.y - i * kTok));
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e, ++kt) {
-                        make_kt(st, g + 2 * e, terms, tmem + kTmK + g * kTmBuf + lanes, &sh.kt_empty[g], (kt & 1) ^ 1);
+                        make_kt(c, g + 2 * e, terms, tmem + kTmK + g * kTmBuf + lanes, &sh.kt_empty[g], (kt & 1) ^ 1);
                         arrive(&sh.kt_full[g]);
                     }
-                    arrive(&sh.k_empty[st]);
-                    arrive(&sh.gates_empty[st]);
+                    arrive(&sh.k_empty[c % kStages]);
+                    arrive(&sh.gates_empty[c & 1]);
                 }
             });
         } else if (!OUTPUT) {
@@ -535,10 +529,10 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                 };
                 for (int i = 0; i < chunks; ++i, ++c) {
                     const uint32_t st = c & 1;
-                    check(c, min(kTok, s.rows - i * kTok));
-                    make_kt(st, g, terms, tmem + st * (4 * kTmBuf) + g * kTmBuf + lanes, &sh.kt_empty[st], ((c >> 1) & 1) ^ 1);
+                    check(c, min(kTok, s.y - i * kTok));
+                    make_kt(c, g, terms, tmem + st * (4 * kTmBuf) + g * kTmBuf + lanes, &sh.kt_empty[st], ((c >> 1) & 1) ^ 1);
                     arrive(&sh.kt_full[st]);
-                    arrive(&sh.k_empty[st]);
+                    arrive(&sh.k_empty[c % kStages]);
                     if (i > 0) update(c - 1);
                     whole = sh.block[st][0] + sh.block[st][1] + sh.block[st][2] + sh.block[st][3];
                     arrive(&sh.gates_empty[st]);
@@ -548,7 +542,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) S[e] = f2(NAN, NAN);
                 }
-                const int64_t at = (int64_t)s.entry * a.H + s.h;
+                const int64_t at = (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * a.H + head_of(s);
                 float *out = p.states + at * kState + (int64_t)(32 * u) * kHeadDim + row;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
@@ -575,13 +569,14 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     for (int j = 0; j < 8; ++j) y[2 * n + (j >> 2)][j & 3] = pack2(x[2 * j], x[2 * j + 1]);
                 }
                 tc_fence_before();
+                arrive(&sh.o_empty);
                 if (__builtin_expect(o_odd | (dead != 0), 0)) {
                     const bool lost = dead;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (lost || sh.odd[(c - 1) & 3][32 * u + j] <= row) y[j >> 3][(j >> 1) & 3] |= j & 1 ? 0x7fff0000u : 0x7fffu;
                 }
-            // four lanes exchange their units of 16 bytes, so that a store writes 64 bytes of eight rows
+                // four lanes exchange their units of 16 bytes, so that a store writes 64 bytes of eight rows
 #pragma unroll
                 for (int n = 1; n < 4; n <<= 1) {
                     const bool up = lane & n;
@@ -601,18 +596,19 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             };
             for_items([&](const Item &s, int chunks, int) {
                 const int64_t place = (int64_t)(32 * u) * kHeadDim + row;  // of this thread's part of a state
-                if (s.slot < 0) {
-                    for (int t = row; t < s.rows; t += kTok) {
-                        uint32_t *to_o = (uint32_t *)((__nv_bfloat16 *)a.o + ((int64_t)(s.first + t) * a.H + s.h) * kHeadDim + 32 * u);
+                if (s.w & kNoSlot) {
+                    for (int t = row; t < s.y; t += kTok) {
+                        uint32_t *to_o = (uint32_t *)((__nv_bfloat16 *)a.o + ((int64_t)(s.x + t) * a.H + head_of(s)) * kHeadDim + 32 * u);
                         for (int j = 0; j < 16; ++j) to_o[j] = 0x7fc07fc0u;
                     }
                     return;
                 }
                 F2 S[16];  // value channels 32 u + 2 e, and the one after
                 const float *init = nullptr;
-                if (!s.begins) init = p.states + ((int64_t)(s.entry - 1) * a.H + s.h) * kState;
+                const int64_t at = (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * a.H + head_of(s);
+                if (!(s.w & kBegins)) init = p.states + (at - a.H) * kState;
                 else if (a.initial_state)
-                    init = s.cut ? p.first + ((int64_t)s.entry * a.H + s.h) * kState : a.initial_state + (s.slot * a.H + s.h) * (int64_t)kState;
+                    init = s.w & kCut ? p.first + at * kState : a.initial_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState;
                 if (init) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) S[e] = f2(init[place + 2 * e * kHeadDim], init[place + (2 * e + 1) * kHeadDim]);
@@ -631,8 +627,8 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                 if (chunks > 0) publish();
                 for (int i = 0; i < chunks; ++i, ++c) {
                     const uint32_t st = c & 1, full = (c >> 1) & 1;
+                    if (c == 0) arrive(&sh.o_empty);
                     if (c > 0) take_outputs();
-                    arrive(&sh.o_empty);
                     wait(&sh.v_ready[st], full);
                     const bool odd = sh.any_odd[u >> 1][c & 3];
                     const float own = sh.lower[st][row];
@@ -644,72 +640,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                         if (b < w && b > u) before += x;
                         whole += x;
                     }
-                    // P: columns 32 u ..
-                    const float f = exp2f(before) * a.scale;
-                    wait(&sh.x_full, c & 1);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int e = 0; e < 2; ++e) {
-                        const int j0 = 32 * u + 16 * e;
-                        uint32_t y[8];
-                        if (u <= w) {
-                            float x[16];
-                            tmem_ld16(tmem + lanes + j0, x);
-                            if (u < w) {
-                                tmem_ld_wait_for(x);
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const float4 z = *(const float4 *)&sh.upper[st][j0 + j];
-                                    y[j / 2] = narrow(mul2(f2(x[j], x[j + 1]), mul2(f2(z.x, z.y), f2(f, f))));
-                                    y[j / 2 + 1] = narrow(mul2(f2(x[j + 2], x[j + 3]), mul2(f2(z.z, z.w), f2(f, f))));
-                                }
-                            } else {
-                                const int seen = row - j0;  // last column that this row sees
-                                tmem_ld_wait_for(x);
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const float4 z = *(const float4 *)&sh.lower[st][j0 + j];
-                                    x[j] = j <= seen ? x[j] * (a.scale * exp2_sfu(own - z.x)) : 0.0f;
-                                    x[j + 1] = j + 1 <= seen ? x[j + 1] * (a.scale * exp2_sfu(own - z.y)) : 0.0f;
-                                    x[j + 2] = j + 2 <= seen ? x[j + 2] * (a.scale * exp2_sfu(own - z.z)) : 0.0f;
-                                    x[j + 3] = j + 3 <= seen ? x[j + 3] * (a.scale * exp2_sfu(own - z.w)) : 0.0f;
-                                    y[j / 2] = pack2(x[j], x[j + 1]);
-                                    y[j / 2 + 1] = pack2(x[j + 2], x[j + 3]);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] = 0;
-                        }
-                        tmem_st8(tmem + lanes + 32 * u + 8 * e, y);  // over scores of the block that are read
-                    }
-                    arrive(&sh.gates_empty[st]);
-                    // O so far, Q . S, times the row's decay
-                    const float to_row = exp2f(upto) * a.scale;
-                    wait(&sh.qs_full, c & 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float x[16];
-                        tmem_ld16(to + 16 * k, x);
-                        tmem_ld_wait_for(x);
-                        uint32_t y[16];
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            float lo, hi;
-                            unf2(mul2(f2(x[j], x[j + 1]), f2(to_row, to_row)), lo, hi);
-                            y[j] = __float_as_uint(lo), y[j + 1] = __float_as_uint(hi);
-                        }
-                        tmem_st16(to + 16 * k, y);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    arrive(&sh.pv_ready);
-                    o = (__nv_bfloat16 *)a.o + ((int64_t)(s.first + i * kTok + (row & ~3)) * a.H + s.h) * kHeadDim + 32 * u +
-                        8 * (lane & 3);
-                    o_rows = min(kTok, s.rows - i * kTok);
-                    o_odd = odd;
-                    // the state
+                    // the state, while the scores are computed
                     const float decay = exp2f(whole);
                     wait(&sh.d_full, c & 1);
                     tc_fence_after();
@@ -734,14 +665,78 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     // (what follows it, the next chunk's D, is what keeps the check of V from writing `odd` four chunks on
                     // before these warps have taken that chunk's outputs)
                     arrive(&sh.d_empty);
+                    // P: columns 32 u ..  e^{G_i - G_j} as a factor of the row and one of the column, with the end of block u
+                    // between them; on the diagonal block, whose rows lie before that end, only while the row's stays finite.
+                    const float tail = u == w ? own - sh.block[st][w] : before;
+                    const float f = exp2f(tail) * a.scale;
+                    wait(&sh.x_full, c & 1);
+                    tc_fence_after();
+                    const bool exact = u == w && __any_sync(0xffffffffu, !(tail < 80.0f));
+#pragma unroll 1
+                    for (int e = 0; e < 2; ++e) {
+                        const int j0 = 32 * u + 16 * e, seen = row - j0;  // seen: the last column that this row sees
+                        uint32_t y[8];
+                        if (u <= w) {
+                            float x[16];
+                            tmem_ld16(tmem + lanes + j0, x);
+                            tmem_ld_wait_for(x);
+                            if (__builtin_expect(exact, 0)) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const float2 z = *(const float2 *)&sh.lower[st][j0 + 2 * j];
+                                    y[j] = pack2(x[2 * j] * (a.scale * exp2f(own - z.x)), x[2 * j + 1] * (a.scale * exp2f(own - z.y)));
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 16; j += 4) {
+                                    const float4 z = *(const float4 *)&sh.upper[st][j0 + j];
+                                    y[j / 2] = narrow(mul2(f2(x[j], x[j + 1]), mul2(f2(z.x, z.y), f2(f, f))));
+                                    y[j / 2 + 1] = narrow(mul2(f2(x[j + 2], x[j + 3]), mul2(f2(z.z, z.w), f2(f, f))));
+                                }
+                            }
+                            if (u == w)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) y[j] = seen > 2 * j ? y[j] : seen == 2 * j ? y[j] & 0xffffu : 0u;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) y[j] = 0;
+                        }
+                        tmem_st8(tmem + lanes + 32 * u + 8 * e, y);  // over scores of the block that are read
+                    }
+                    arrive(&sh.gates_empty[st]);
+                    // O so far, Q . S, times the row's decay
+                    const float to_row = exp2f(upto) * a.scale;
+                    wait(&sh.qs_full, c & 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float x[16];
+                        tmem_ld16(to + 16 * k, x);
+                        tmem_ld_wait_for(x);
+                        uint32_t z[16];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            float lo, hi;
+                            unf2(mul2(f2(x[j], x[j + 1]), f2(to_row, to_row)), lo, hi);
+                            z[j] = __float_as_uint(lo), z[j + 1] = __float_as_uint(hi);
+                        }
+                        tmem_st16(to + 16 * k, z);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    arrive(&sh.pv_ready);
+                    o = (__nv_bfloat16 *)a.o + ((int64_t)(s.x + i * kTok + (row & ~3)) * a.H + head_of(s)) * kHeadDim + 32 * u +
+                        8 * (lane & 3);
+                    o_rows = min(kTok, s.y - i * kTok);
+                    o_odd = odd;
                     if (i + 1 < chunks) publish();
                 }
                 if (gave_up()) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) S[e] = f2(NAN, NAN);
                 }
-                if (s.ends && a.final_state) {
-                    float *out = a.final_state + (s.slot * a.H + s.h) * (int64_t)kState + place;
+                if ((s.w & kEnds) && a.final_state) {
+                    float *out = a.final_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState + place;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
                 }
@@ -830,7 +825,8 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
     const int64_t segment = segment_of(T, a.H), entries = entries_of(T, a.H);
     p.segment = (int)segment;
     p.entries = (int)entries;
-    p.items = (T / segment + a.n_seqs) * a.H;
+    p.items = (uint32_t)((T / segment + a.n_seqs) * a.H);
+    p.joined = entries > 0;
     p.states = (float *)a.workspace;
     p.first = p.states + entries * a.H * kState;
     p.decay = p.first + entries * a.H * kState;
