@@ -67,7 +67,7 @@ __device__ __forceinline__ constexpr uint32_t tile_v(uint32_t st) { return (2 * 
 constexpr uint32_t kTmO = 128, kTmD = 384, kTmK = 256, kTmTerm = 16, kTmBuf = 48;
 
 struct Shared {
-    uint64_t k_full[3], v_full[3], k_empty[3], v_empty[3], v_ready[3], q_empty[2], gates_full[2], gates_empty[2], kt_full[2], kt_empty[2],
+    uint64_t k_full[3], v_full[3], k_empty[3], v_empty[3], v_ready[3], q_full[2], q_empty[2], gates_full[2], gates_empty[2], kt_full[2], kt_empty[2],
         x_full, qs_full, pv_ready, o_full, o_empty, d_full, d_empty;
     alignas(16) float lower[2][kTok];  // log2 decay of a token's block up to and with it
     float upper[2][kTok];              // decay of a token's block behind it
@@ -130,6 +130,12 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t *r, uint32_t addr) {
 __device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t *u) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
                  "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+// 3-D tile, shared -> global (64 channels of 128 tokens of a head), in the issuing thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const void *tmap, const void *src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
 // The larger magnitude of two pairs of bf16, NaN if either is.
@@ -195,7 +201,8 @@ __device__ __noinline__ Item state_item(const LinearChunkArgs &a, uint32_t segme
 template <bool OUTPUT>
 __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                        const __grid_constant__ CUtensorMap map_v, const ChunkParams p) {
+                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
+                        const ChunkParams p) {
     constexpr uint32_t kStages = OUTPUT ? 2 : 3;
     extern __shared__ __align__(1024) uint8_t sm[];
     Shared &sh = *reinterpret_cast<Shared *>(sm + kSmShared);
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             mbar_init(&sh.v_empty[i], OUTPUT ? 2 : 1), mbar_init(&sh.v_ready[i], OUTPUT ? 8 : 16);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.q_empty[i], 1), mbar_init(&sh.gates_full[i], 1), mbar_init(&sh.gates_empty[i], OUTPUT ? 24 : 16);
+            mbar_init(&sh.q_full[i], 1), mbar_init(&sh.q_empty[i], 16), mbar_init(&sh.gates_full[i], 1), mbar_init(&sh.gates_empty[i], OUTPUT ? 24 : 16);
             mbar_init(&sh.kt_full[i], OUTPUT ? 4 : 16), mbar_init(&sh.kt_empty[i], 1);
         }
         mbar_init(&sh.x_full, 1), mbar_init(&sh.qs_full, 1), mbar_init(&sh.pv_ready, 16);
@@ -251,8 +258,25 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     if (wid == 0) {
         // ---- TMA
         uint32_t c = 0;
+        // With outputs, a chunk's o is left in the place of its Q, whose products are done, and leaves from there
+        // before the next Q comes (16-byte stores of a row a thread took 2400 clocks a chunk; in the place of V, which
+        // is wanted earlier, 131072 tokens of 8 heads take 343 instead of 325 us).  The last two chunks: first
+        // token, head; -1: rows fewer than the tile's, which the other warps have stored.
+        int token0 = -1, token1 = -1, head0 = 0, head1 = 0;
+        auto store = [&](uint32_t n) {  // o of chunk n
+            const uint32_t st = n % kStages;
+            wait(&sh.q_empty[st], (n / kStages) & 1);
+            const int token = n & 1 ? token1 : token0, head = n & 1 ? head1 : head0;
+            if (token >= 0 && !gave_up() && elect_one()) {
+                tma_store_3d(&map_o, sm + kSmQ + st * kTile, 0, head, token);
+                tma_store_3d(&map_o, sm + kSmQ + st * kTile + kHalf, 64, head, token);
+                bulk_commit();
+                bulk_wait_read();
+            }
+            __syncwarp();
+        };
         for_items([&](const Item &s, int chunks, int terms) {
-            const int hk = (uint32_t)head_of(s) / (uint32_t)a.group;
+            const int h = head_of(s), hk = (uint32_t)h / (uint32_t)a.group;
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
                 const uint32_t st = c % kStages, before = ((c / kStages) & 1) ^ 1;
                 const int row = s.x + i * kTok;
@@ -261,20 +285,33 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     tma_load_3d(sm + at + kHalf, map, 64, head, row, bar);
                 };
                 wait(&sh.k_empty[st], before);
-                if (OUTPUT) wait(&sh.q_empty[st], before);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&sh.k_full[st], OUTPUT ? 2 * kTile : kTile);
+                    mbar_arrive_expect_tx(&sh.k_full[st], kTile);
                     load(tile_k(st), &map_k, hk, &sh.k_full[st]);
-                    if (OUTPUT) load(kSmQ + st * kTile, &map_q, hk, &sh.k_full[st]);
                 }
                 wait(&sh.v_empty[st], before);
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&sh.v_full[st], kTile);
-                    load(tile_v(st), &map_v, head_of(s), &sh.v_full[st]);
+                    load(tile_v(st), &map_v, h, &sh.v_full[st]);
+                }
+                if (OUTPUT) {
+                    if (c >= kStages) store(c - kStages);
+                    const int token = s.y - i * kTok >= kTok ? row : -1;
+                    if (c & 1) token1 = token, head1 = h;
+                    else token0 = token, head0 = h;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&sh.q_full[st], kTile);
+                        load(kSmQ + st * kTile, &map_q, hk, &sh.q_full[st]);
+                    }
                 }
                 __syncwarp();
             }
         });
+        if (OUTPUT) {
+            for (uint32_t n = c > kStages ? c - kStages : 0; n < c; ++n) store(n);
+            if (elect_one()) bulk_wait_all();
+            __syncwarp();
+        }
     } else if (wid == 1 && OUTPUT) {
         // ---- MMA of X and O
         uint32_t c = 0;
@@ -284,6 +321,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             for (int i = 0; i < chunks && !gave_up(); ++i, ++c) {
                 const uint32_t st = c & 1, full = (c >> 1) & 1;
                 wait(&sh.k_full[st], full);
+                wait(&sh.q_full[st], full);
                 if (c > 0) wait(&sh.o_full, (c - 1) & 1);  // P of the chunk before is read
                 tc_fence_after();
                 if (elect_one()) {
@@ -296,7 +334,6 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                 tc_fence_after();
                 if (elect_one()) {
                     mma_tile<kTok, kTok, kHeadDim, kTok, kTok, false, true>(tmem + kTmO, q0 + st * kTile, s0, false);
-                    mma_commit(&sh.q_empty[st]);
                     mma_commit(&sh.qs_full);
                 }
                 __syncwarp();
@@ -538,10 +575,6 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     arrive(&sh.gates_empty[st]);
                 }
                 if (chunks > 0) update(c - 1);
-                if (gave_up()) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) S[e] = f2(NAN, NAN);
-                }
                 const int64_t at = (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * a.H + head_of(s);
                 float *out = p.states + at * kState + (int64_t)(32 * u) * kHeadDim + row;
 #pragma unroll
@@ -552,47 +585,41 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             // ---- P, the state and the outputs: a thread stands for a row of P, a token of o and a key channel of the state
             uint32_t c = 0;
             const uint32_t to = tmem + kTmO + 32 * u + lanes, td = tmem + kTmD + 32 * u + lanes;
-            // outputs that are not taken yet: the last chunk's, from the first of the four rows that four lanes exchange
+            // the last chunk's outputs, which are not taken yet: this thread's 32 values (where there are fewer than 128 rows)
             __nv_bfloat16 *o = nullptr;
             int o_rows = 0;
             bool o_odd = false;
             auto take_outputs = [&] {
-                wait(&sh.o_full, (c - 1) & 1);
+                const uint32_t n = c - 1;
+                wait(&sh.o_full, n & 1);
                 tc_fence_after();
                 uint32_t y[4][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int k = 0; k < 2; ++k) {
                     float x[16];
-                    tmem_ld16(to + 16 * n, x);
+                    tmem_ld16(to + 16 * k, x);
                     tmem_ld_wait_for(x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[2 * n + (j >> 2)][j & 3] = pack2(x[2 * j], x[2 * j + 1]);
+                    for (int j = 0; j < 8; ++j) y[2 * k + (j >> 2)][j & 3] = pack2(x[2 * j], x[2 * j + 1]);
                 }
                 tc_fence_before();
                 arrive(&sh.o_empty);
-                if (__builtin_expect(o_odd | (dead != 0), 0)) {
-                    const bool lost = dead;
+                if (__builtin_expect(o_odd, 0)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (lost || sh.odd[(c - 1) & 3][32 * u + j] <= row) y[j >> 3][(j >> 1) & 3] |= j & 1 ? 0x7fff0000u : 0x7fffu;
+                        if (sh.odd[n & 3][32 * u + j] <= row) y[j >> 3][(j >> 1) & 3] |= j & 1 ? 0x7fff0000u : 0x7fffu;
                 }
-                // four lanes exchange their units of 16 bytes, so that a store writes 64 bytes of eight rows
+                if (o_rows == kTok) {  // into the place of Q, for the copying warp
+                    uint8_t *q = sm + kSmQ + (n & 1) * kTile + (u >> 1) * kHalf + row * 128;
 #pragma unroll
-                for (int n = 1; n < 4; n <<= 1) {
-                    const bool up = lane & n;
+                    for (int j = 0; j < 4; ++j)
+                        *(uint4 *)(q + (((4 * (u & 1) + j) ^ (row & 7)) << 4)) = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
+                    fence_async_smem();
+                } else if (row < o_rows) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        if (!(m & n))
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? y[m][j] : y[m | n][j], n);
-                                if (up) y[m][j] = got; else y[m | n][j] = got;
-                            }
+                    for (int j = 0; j < 4; ++j) ((uint4 *)o)[j] = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
                 }
-                const int64_t step = (int64_t)a.H * kHeadDim;
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if ((row & ~3) + m < o_rows) *(uint4 *)(o + m * step) = make_uint4(y[m][0], y[m][1], y[m][2], y[m][3]);
+                arrive(&sh.q_empty[n & 1]);
             };
             for_items([&](const Item &s, int chunks, int) {
                 const int64_t place = (int64_t)(32 * u) * kHeadDim + row;  // of this thread's part of a state
@@ -725,15 +752,10 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     arrive(&sh.pv_ready);
-                    o = (__nv_bfloat16 *)a.o + ((int64_t)(s.x + i * kTok + (row & ~3)) * a.H + head_of(s)) * kHeadDim + 32 * u +
-                        8 * (lane & 3);
+                    o = (__nv_bfloat16 *)a.o + ((int64_t)(s.x + i * kTok + row) * a.H + head_of(s)) * kHeadDim + 32 * u;
                     o_rows = min(kTok, s.y - i * kTok);
                     o_odd = odd;
                     if (i + 1 < chunks) publish();
-                }
-                if (gave_up()) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) S[e] = f2(NAN, NAN);
                 }
                 if ((s.w & kEnds) && a.final_state) {
                     float *out = a.final_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState + place;
@@ -746,9 +768,22 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (dead) {  // copies still in flight land before the memory is given up
+    if (dead) {  // a wait gave up: copies still in flight land, then all that this CTA had to write becomes NaN
         const long long t0 = clock64();
         while (clock64() - t0 < 100000000LL) __nanosleep(1000);
+        for_items([&](const Item &s, int, int) {
+            const int64_t at = (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * a.H + head_of(s);
+            float *state = OUTPUT ? nullptr : p.states + at * kState;
+            if (OUTPUT) {
+                for (int64_t j = tid; j < (int64_t)s.y * kHeadDim; j += blockDim.x)
+                    ((__nv_bfloat16 *)a.o)[((s.x + j / kHeadDim) * a.H + head_of(s)) * kHeadDim + j % kHeadDim] = __float2bfloat16_rn(NAN);
+                if ((s.w & kEnds) && !(s.w & kNoSlot) && a.final_state)
+                    state = a.final_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState;
+            }
+            if (state)
+                for (int j = tid; j < kState; j += blockDim.x) state[j] = NAN;
+            if (!OUTPUT && tid == 0) p.decay[at] = NAN;
+        });
     }
     if (wid == 1) tmem_dealloc(tmem, 512);
 }
@@ -813,13 +848,14 @@ size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H) {
 cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream) {
     const int64_t T = a.total_tokens, rows = std::max<int64_t>(T, 1);
     const int hk = a.H / a.group;
-    CUtensorMap map_q, map_k, map_v;
+    CUtensorMap map_q, map_k, map_v, map_o;
     // (without a token there is no copy, and maybe no pointer)
     const void *none = a.final_state ? (const void *)a.final_state : a.initial_state;
     if (T == 0 && !none) return cudaSuccess;
     if (!encode_heads64(&map_q, T ? a.q : none, kHeadDim, hk, rows, a.q_stride, kTok) ||
         !encode_heads64(&map_k, T ? a.k : none, kHeadDim, hk, rows, a.k_stride, kTok) ||
-        !encode_heads64(&map_v, T ? a.v : none, kHeadDim, a.H, rows, a.v_stride, kTok))
+        !encode_heads64(&map_v, T ? a.v : none, kHeadDim, a.H, rows, a.v_stride, kTok) ||
+        !encode_heads64(&map_o, T ? a.o : none, kHeadDim, a.H, rows, (int64_t)a.H * kHeadDim, kTok))
         return cudaErrorUnknown;
     ChunkParams p{a};
     const int64_t segment = segment_of(T, a.H), entries = entries_of(T, a.H);
@@ -834,7 +870,7 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         return e != cudaSuccess ? e
                                 : launch_dependent(kernel, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(threads),
-                                                   kSmemBytes, stream, map_q, map_k, map_v, p);
+                                                   kSmemBytes, stream, map_q, map_k, map_v, map_o, p);
     };
     if (entries > 0) {
         cudaError_t e = launch(linear_chunk_kernel<false>, 640, entries * a.H);
