@@ -79,16 +79,87 @@ struct Shared {
 constexpr uint32_t kSmemBytes = kSmShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory");
 
+// A segment to work on, in four registers: what warps look at in every chunk must not be in local memory,
+// for which the L1 cache has no room beside this shared memory.
+enum : int { kBegins = 1 << 16, kEnds = 1 << 17, kCut = 1 << 18, kNoSlot = 1 << 19 };
+typedef int4 Item;  // first token, tokens, sequence, flags (and in the low 16 bits, once it is picked, the head)
+__device__ __forceinline__ int head_of(const Item &s) { return s.w & 0xffff; }
+
 struct ChunkParams {
     LinearChunkArgs a;
-    int segment;     // tokens
-    int entries;     // segments whose state the workspace holds, at most
-    uint32_t items;  // (segment, head) pairs of the kernel with outputs
-    bool joined;     // it follows the others: its inputs are there before it begins
-    float *states;   // [entries][H][V][K]
-    float *first;    // [entries][H][V][K]: copies of initial states (those that a later CTA may overwrite)
-    float *decay;    // [entries][H]
+    int segment;    // tokens
+    int entries;    // segments whose state the workspace holds, at most; floor(first token / segment) is a segment's
+    bool joined;    // the kernel follows the others: its inputs are there before it begins
+    int *counts;    // segments of each list (no lists of a single sequence)
+    Item *outputs;  // all segments, the longest first
+    Item *inner;    // [entries]: those that others follow in their sequence
+    float *states;  // [entries][H][V][K]
+    float *first;   // [entries][H][V][K]: copies of initial states (those that a later CTA may overwrite)
+    float *decay;   // [entries][H]
 };
+
+// The segments: a list of all for the outputs, sorted by length (into kBuckets classes), and one of those that have a
+// successor.  Their order in a class is left to chance; what is computed does not depend on it.  (Sequences that
+// overlap, as no well-formed offsets do, may be more than the lists hold; what is past their ends is left out.)
+constexpr int kIndexThreads = 1024, kBuckets = 64;
+typedef unsigned long long Count;
+__global__ void __launch_bounds__(kIndexThreads) linear_index_kernel(const ChunkParams p) {
+    __shared__ Count place[kBuckets], inner;
+    const LinearChunkArgs &a = p.a;
+    const int tid = threadIdx.x, segment = p.segment;
+    const Count most = p.entries + a.n_seqs, most_inner = p.entries;
+    for (int i = tid; i < kBuckets; i += blockDim.x) place[i] = 0;
+    if (tid == 0) inner = 0;
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const float scale = (kBuckets - 1) / (float)segment;
+    auto bucket = [&](int rows) { return max(0, kBuckets - 1 - (int)(rows * scale)); };
+    const int threads = blockDim.x;
+#pragma unroll 1
+    for (int n = tid; n < a.n_seqs; n += threads) {
+        const Span span = span_of(a, n);
+        if (span.len < 0) continue;
+        const int full = span.len > 0 ? (span.len - 1) / segment : 0;  // segments before the last one
+        if (full > 0) atomicAdd(&place[0], (Count)full);
+        atomicAdd(&place[bucket(span.len - full * segment)], (Count)1);
+    }
+    __syncthreads();
+    if (tid < 32) {
+        const Count x = place[2 * tid], own = x + place[2 * tid + 1];
+        Count upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Count y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (tid >= o) upto += y;
+        }
+        place[2 * tid] = upto - own;
+        place[2 * tid + 1] = upto - own + x;
+        if (tid == 31) p.counts[0] = (int)min(upto, most);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int n = tid; n < a.n_seqs; n += threads) {
+        const Span span = span_of(a, n);
+        if (span.len < 0) continue;
+        const int full = span.len > 0 ? (span.len - 1) / segment : 0, slot = slot_of(a, n) < 0 ? kNoSlot : 0;
+        const int cut = full > 0 ? kCut : 0;
+        if (full > 0) {
+            Count at = atomicAdd(&place[0], (Count)full), in = slot ? most_inner : atomicAdd(&inner, (Count)full);
+#pragma unroll 1
+            for (int l = 0; l < full; ++l, ++at, ++in) {
+                const Item s = make_int4(span.first + l * segment, segment, n, (l == 0 ? kBegins : 0) | cut | slot);
+                if (at < most) p.outputs[at] = s;
+                if (in < most_inner) p.inner[in] = s;
+            }
+        }
+        const int rows = span.len - full * segment;
+        const Count at = atomicAdd(&place[bucket(rows)], (Count)1);
+        if (at < most) p.outputs[at] = make_int4(span.first + full * segment, rows, n, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
+    }
+    __syncthreads();
+    if (tid == 0) p.counts[1] = (int)min(inner, most_inner);
+}
 
 // Two fp32 as one operand of the packed instructions.
 typedef uint64_t F2;
@@ -144,59 +215,6 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
     asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ int offset_of(const LinearChunkArgs &a, int n) {
-    return a.cu_seqlens ? a.cu_seqlens[n] : n * a.equal_len;
-}
-
-// The last sequence n with bound(n) <= at, by the warp's 32 lanes together (bound(0) <= at).
-template <typename F>
-__device__ __forceinline__ int last_below(int n_seqs, int at, F bound) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, span = n_seqs;  // in [lo, lo + span)
-    while (span > 1) {
-        const int step = (span + 31) >> 5, n = lo + lane * step;
-        const bool below = n < lo + span && (lane == 0 || bound(n) <= at);
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
-        lo += last * step;
-        span = min(step, span - last * step);
-    }
-    return lo;
-}
-
-// A segment (and head) to work on, in four registers: what warps look at in every chunk must not be in
-// local memory, for which the L1 cache has no room beside this shared memory.
-enum : uint32_t { kBegins = 1u << 16, kEnds = 1u << 17, kCut = 1u << 18, kNoSlot = 1u << 19 };
-typedef int4 Item;  // first token, tokens (-1: no such segment), sequence, head and flags
-__device__ __forceinline__ int head_of(const Item &s) { return s.w & 0xffff; }
-
-// Segment (and head) `i` of the kernel with outputs.  Sequence n's segments are numbered from
-// floor(offset / segment) + n on, which leaves room for all of them whatever the lengths.  The segment's entry in the
-// workspace is floor(first / segment).
-__device__ __noinline__ Item output_item(const LinearChunkArgs &a, uint32_t segment, uint32_t i) {
-    const uint32_t rank = i / (uint32_t)a.H, h = i - rank * a.H;
-    const int n = last_below(a.n_seqs, rank, [&](int n) { return (int)((uint32_t)offset_of(a, n) / segment) + n; });
-    const bool slot = slot_of(a, n) >= 0;
-    const Span span = span_of(a, n);
-    const int l = rank - (uint32_t)span.first / segment - n, count = max(1u, (span.len + segment - 1) / segment);
-    if (span.len < 0 || l < 0 || l >= count) return make_int4(0, -1, 0, 0);
-    return make_int4(span.first + l * segment, min((int)segment, span.len - l * (int)segment), n,
-                     h | (l == 0 ? kBegins : 0) | (l == count - 1 ? kEnds : 0) | (count > 1 ? kCut : 0) | (slot ? 0 : kNoSlot));
-}
-
-// Segment of entry m = i / H, if it is one that others follow in its sequence: the one that holds token
-// (m + 1) segment - 1.
-__device__ __noinline__ Item state_item(const LinearChunkArgs &a, uint32_t segment, uint32_t i) {
-    const uint32_t m = i / (uint32_t)a.H, h = i - m * a.H;
-    const int x = (m + 1) * segment;
-    const int n = last_below(a.n_seqs, x, [&](int n) { return offset_of(a, n); });
-    const bool slot = slot_of(a, n) >= 0;
-    const Span span = span_of(a, n);
-    if (span.len < 0 || x <= span.first) return make_int4(0, -1, 0, 0);
-    const int l = (uint32_t)(x - span.first - 1) / segment, from = l * segment;
-    if (span.len - from <= (int)segment || !slot) return make_int4(0, -1, 0, 0);
-    return make_int4(span.first + from, segment, n, h | kCut);
-}
-
 // OUTPUT: o and final states, from the states in front of the segments; else a segment's own state.
 template <bool OUTPUT>
 __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
@@ -244,12 +262,26 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
         if (lane == 0) mbar_arrive(bar);
     };
     auto gave_up = [&] { return __any_sync(0xffffffffu, dead); };
-    // f(item, chunks) for each of this CTA's items, in the same order by every warp
+    // f(segment and head, chunks, terms) for each of this CTA's, in the same order by every warp: back and forth over
+    // the list, so that who had one of the longest gets one of the shortest next
     auto for_items = [&](auto f) {
-        const uint32_t items = OUTPUT ? p.items : (uint32_t)p.entries * a.H;
-        for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
-            const Item s = OUTPUT ? output_item(a, p.segment, i) : state_item(a, p.segment, i);
-            if (s.y < 0) continue;
+        // (one sequence needs no lists)
+        const Span only = a.n_seqs == 1 ? span_of(a, 0) : Span{0, -1};
+        const int slot = a.n_seqs == 1 && slot_of(a, 0) < 0 ? kNoSlot : 0, full = only.len > 0 ? (uint32_t)(only.len - 1) / p.segment : 0;
+        const int count = a.n_seqs > 1 ? p.counts[OUTPUT ? 0 : 1] : only.len < 0 ? 0 : OUTPUT ? full + 1 : slot ? 0 : full;
+        const uint32_t items = (uint32_t)count * a.H;
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (i >= items) break;
+            const uint32_t n = i / (uint32_t)a.H;
+            Item s;
+            if (a.n_seqs == 1) {
+                s = make_int4(only.first + n * p.segment, min(p.segment, only.len - (int)n * p.segment), 0,
+                              (n == 0 ? kBegins : 0) | (n == full ? kEnds : 0) | (full > 0 ? kCut : 0) | slot);
+            } else {
+                s = (OUTPUT ? p.outputs : p.inner)[n];
+            }
+            s.w |= i - n * a.H;
             // a segment whose states serve o alone does without the third term
             f(s, s.w & kNoSlot ? 0 : (s.y + kTok - 1) / kTok, OUTPUT && (s.w & (kCut | kEnds)) == kCut ? 2 : 3);
         }
@@ -838,12 +870,23 @@ inline int64_t entries_of(int64_t total_tokens, int H) {
     return total_tokens > 0 ? (total_tokens - 1) / segment_of(total_tokens, H) : 0;
 }
 
+struct Layout {
+    size_t outputs, inner, decay, states, total;
+};
+inline Layout layout(int64_t total_tokens, int n_seqs, int H) {
+    const int64_t entries = entries_of(total_tokens, H);
+    Layout l;
+    l.outputs = n_seqs > 1 ? 256 : 0;
+    l.inner = l.outputs + (n_seqs > 1 ? align_up((size_t)(entries + n_seqs) * sizeof(Item), 256) : 0);
+    l.decay = l.inner + (n_seqs > 1 ? align_up((size_t)entries * sizeof(Item), 256) : 0);
+    l.states = l.decay + align_up((size_t)entries * H * sizeof(float), 256);
+    l.total = l.states + (size_t)entries * H * 2 * kState * sizeof(float);
+    return l;
+}
+
 }  // namespace
 
-size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H) {
-    const int64_t entries = entries_of(total_tokens, H) * H;
-    return (size_t)entries * 2 * kState * sizeof(float) + align_up((size_t)entries * sizeof(float), 256);
-}
+size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H) { return layout(total_tokens, n_seqs, H).total; }
 
 cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream) {
     const int64_t T = a.total_tokens, rows = std::max<int64_t>(T, 1);
@@ -859,27 +902,34 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
         return cudaErrorUnknown;
     ChunkParams p{a};
     const int64_t segment = segment_of(T, a.H), entries = entries_of(T, a.H);
+    const Layout l = layout(T, a.n_seqs, a.H);
+    uint8_t *ws = (uint8_t *)a.workspace;
     p.segment = (int)segment;
     p.entries = (int)entries;
-    p.items = (uint32_t)((T / segment + a.n_seqs) * a.H);
     p.joined = entries > 0;
-    p.states = (float *)a.workspace;
+    p.counts = (int *)ws;
+    p.outputs = (Item *)(ws + l.outputs);
+    p.inner = (Item *)(ws + l.inner);
+    p.decay = (float *)(ws + l.decay);
+    p.states = (float *)(ws + l.states);
     p.first = p.states + entries * a.H * kState;
-    p.decay = p.first + entries * a.H * kState;
     auto launch = [&](auto kernel, int threads, int64_t items) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         return e != cudaSuccess ? e
                                 : launch_dependent(kernel, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(threads),
                                                    kSmemBytes, stream, map_q, map_k, map_v, map_o, p);
     };
+    cudaError_t e = cudaSuccess;
+    if (a.n_seqs > 1) e = launch_dependent(linear_index_kernel, dim3(1), dim3(std::min(kIndexThreads, (a.n_seqs + 31) / 32 * 32)), 0, stream, p);
+    if (e != cudaSuccess) return e;
     if (entries > 0) {
-        cudaError_t e = launch(linear_chunk_kernel<false>, 640, entries * a.H);
+        e = launch(linear_chunk_kernel<false>, 640, entries * a.H);
         if (e == cudaSuccess)
             e = launch_dependent(linear_join_kernel, dim3((unsigned)std::min(a.n_seqs, 4096), (unsigned)a.H, kJoinParts),
                                  dim3(kJoinThreads), 0, stream, p);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t e = launch(linear_chunk_kernel<true>, 896, p.items);
+    e = launch(linear_chunk_kernel<true>, 896, (entries + a.n_seqs) * a.H);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
