@@ -161,34 +161,6 @@ __global__ void __launch_bounds__(kIndexThreads) linear_index_kernel(const Chunk
     if (tid == 0) p.counts[1] = (int)min(inner, most_inner);
 }
 
-// Two fp32 as one operand of the packed instructions.
-typedef uint64_t F2;
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unf2(F2 x, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-// Two bf16 of a register as fp32.
-__device__ __forceinline__ F2 wide(uint32_t two) {
-    return f2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t narrow(F2 x) {
-    float lo, hi;
-    unf2(x, lo, hi);
-    return pack2(lo, hi);
-}
-
 // Four 8 x 8 matrices of bf16, transposed: matrix m's rows are the 16 bytes that lanes 8 m .. 8 m + 7 point at;
 // r[m] holds the elements (row 2 (lane % 4), 2 (lane % 4) + 1; column lane / 4).
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t *r, uint32_t addr) {
