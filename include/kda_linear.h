@@ -89,14 +89,16 @@ size_t kda_linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H,
  * the scores and the state enter the products that give o as bf16 (two roundings
  * beside o's own); what is written to the state is split into three bf16 terms, so
  * that the states are as exact as fp32 sums.  fp32 runs on the CUDA cores, token by
- * token.
+ * token.  Long sequences are cut into segments that are worked on at the same time.
  * A zero-length sequence hands back its initial state (or zeros).  A slot outside
  * [0, n_slots) gives NaN in that sequence's rows of o and leaves the pools alone.
  * Tokens of a sequence whose offsets are decreasing or out of range are not written,
- * nor is its state.  Values that are not finite reach the rows behind them of their own
- * sequence and no other: a NaN or an infinity in v of token j makes that channel NaN from
- * row j on, and in the state (fp32 inputs: what the formula gives).  Results do not depend on
- * timing; where a sequence is cut, and with it the rounding, follows from T, N, H and
+ * nor is its state.  (Offsets that step back make sequences overlap: which of them are
+ * then computed is not defined, nothing outside the buffers is read or written.)
+ * Values that are not finite reach the rows behind them of their own
+ * sequence and no other: a NaN or an infinity in v of token j makes that channel NaN
+ * (fp32 inputs: NaN or infinite) from row j on, and in the state.  Results do not depend on
+ * timing; where a sequence is cut, and with it the rounding, follows from T, H and
  * the offsets.  A bounded wait of a kernel that gave up (a copy that never landed)
  * gives NaN in what that part had to write.
  *

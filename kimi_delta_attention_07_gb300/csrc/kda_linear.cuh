@@ -68,8 +68,9 @@ struct LinearChunkArgs {
     void *workspace;
     int equal_len;  // of each sequence, without cu_seqlens
 };
-size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H);
-// bf16 on the tensor cores; fp32 on the CUDA cores (no workspace)
+size_t linear_chunk_tc_workspace_bytes(int64_t total_tokens, int n_seqs, int H);
+size_t linear_chunk_f32_workspace_bytes(int64_t total_tokens, int n_seqs, int H);
+// bf16 on the tensor cores; fp32 on the CUDA cores
 cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream);
 cudaError_t launch_linear_chunk_f32(const LinearChunkArgs &a, cudaStream_t stream);
 

@@ -94,9 +94,10 @@ int kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
 
 size_t kda_linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int dtype) {
     if (total_tokens < 0 || total_tokens > INT32_MAX || n_seqs <= 0 || n_seqs > 65535 || H <= 0 || H > 65535 ||
-        dtype != KDA_BF16)
+        !dtype_ok(dtype))
         return 0;
-    return linear_chunk_workspace_bytes(total_tokens, n_seqs, H);
+    return dtype == KDA_BF16 ? linear_chunk_tc_workspace_bytes(total_tokens, n_seqs, H)
+                             : linear_chunk_f32_workspace_bytes(total_tokens, n_seqs, H);
 }
 
 int kda_linear_chunk_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

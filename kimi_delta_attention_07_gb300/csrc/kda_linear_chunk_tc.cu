@@ -26,7 +26,7 @@
 // many that a GPU is filled): a first kernel takes every segment's own state from zero (all but
 // each sequence's last), a second one joins them to the states in front of the segments, a
 // third one computes the outputs.  Two instantiations of one kernel are the first and
-// the third.
+// the third (kda_linear_segments.cuh).
 //
 // Masked places: rows of a tile past the sequence's end are emptied (V) or taken as 0 (K).  A
 // value that is not finite would reach rows before it as 0 times it: V is looked through,
@@ -44,7 +44,7 @@
 #include <algorithm>
 
 #include "kda_attn.cuh"
-#include "kda_linear.cuh"
+#include "kda_linear_segments.cuh"
 
 namespace kda {
 
@@ -55,7 +55,6 @@ namespace {
 constexpr int kTok = 128;  // tokens of a chunk
 constexpr uint32_t kTile = 32768;        // 128 tokens x 128 channels: two blocks of 64 channels
 constexpr uint32_t kHalf = kTile / 2;
-constexpr int kState = kHeadDim * kHeadDim;
 
 // shared memory (from a 1024-byte boundary): two stages of K, V, Q and the copy of S; without outputs three of K, V
 constexpr uint32_t kSmQ = 4 * kTile, kSmS = 6 * kTile, kSmShared = 7 * kTile;
@@ -78,88 +77,6 @@ struct Shared {
 };
 constexpr uint32_t kSmemBytes = kSmShared + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory");
-
-// A segment to work on, in four registers: what warps look at in every chunk must not be in local memory,
-// for which the L1 cache has no room beside this shared memory.
-enum : int { kBegins = 1 << 16, kEnds = 1 << 17, kCut = 1 << 18, kNoSlot = 1 << 19 };
-typedef int4 Item;  // first token, tokens, sequence, flags (and in the low 16 bits, once it is picked, the head)
-__device__ __forceinline__ int head_of(const Item &s) { return s.w & 0xffff; }
-
-struct ChunkParams {
-    LinearChunkArgs a;
-    int segment;    // tokens
-    int entries;    // segments whose state the workspace holds, at most; floor(first token / segment) is a segment's
-    bool joined;    // the kernel follows the others: its inputs are there before it begins
-    int *counts;    // segments of each list (no lists of a single sequence)
-    Item *outputs;  // all segments, the longest first
-    Item *inner;    // [entries]: those that others follow in their sequence
-    float *states;  // [entries][H][V][K]
-    float *first;   // [entries][H][V][K]: copies of initial states (those that a later CTA may overwrite)
-    float *decay;   // [entries][H]
-};
-
-// The segments: a list of all for the outputs, sorted by length (into kBuckets classes), and one of those that have a
-// successor.  Their order in a class is left to chance; what is computed does not depend on it.  (Sequences that
-// overlap, as no well-formed offsets do, may be more than the lists hold; what is past their ends is left out.)
-constexpr int kIndexThreads = 1024, kBuckets = 64;
-typedef unsigned long long Count;
-__global__ void __launch_bounds__(kIndexThreads) linear_index_kernel(const ChunkParams p) {
-    __shared__ Count place[kBuckets], inner;
-    const LinearChunkArgs &a = p.a;
-    const int tid = threadIdx.x, segment = p.segment;
-    const Count most = p.entries + a.n_seqs, most_inner = p.entries;
-    for (int i = tid; i < kBuckets; i += blockDim.x) place[i] = 0;
-    if (tid == 0) inner = 0;
-    __syncthreads();
-    griddep_wait();
-    griddep_launch_dependents();
-    const float scale = (kBuckets - 1) / (float)segment;
-    auto bucket = [&](int rows) { return max(0, kBuckets - 1 - (int)(rows * scale)); };
-    const int threads = blockDim.x;
-#pragma unroll 1
-    for (int n = tid; n < a.n_seqs; n += threads) {
-        const Span span = span_of(a, n);
-        if (span.len < 0) continue;
-        const int full = span.len > 0 ? (span.len - 1) / segment : 0;  // segments before the last one
-        if (full > 0) atomicAdd(&place[0], (Count)full);
-        atomicAdd(&place[bucket(span.len - full * segment)], (Count)1);
-    }
-    __syncthreads();
-    if (tid < 32) {
-        const Count x = place[2 * tid], own = x + place[2 * tid + 1];
-        Count upto = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const Count y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (tid >= o) upto += y;
-        }
-        place[2 * tid] = upto - own;
-        place[2 * tid + 1] = upto - own + x;
-        if (tid == 31) p.counts[0] = (int)min(upto, most);
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int n = tid; n < a.n_seqs; n += threads) {
-        const Span span = span_of(a, n);
-        if (span.len < 0) continue;
-        const int full = span.len > 0 ? (span.len - 1) / segment : 0, slot = slot_of(a, n) < 0 ? kNoSlot : 0;
-        const int cut = full > 0 ? kCut : 0;
-        if (full > 0) {
-            Count at = atomicAdd(&place[0], (Count)full), in = slot ? most_inner : atomicAdd(&inner, (Count)full);
-#pragma unroll 1
-            for (int l = 0; l < full; ++l, ++at, ++in) {
-                const Item s = make_int4(span.first + l * segment, segment, n, (l == 0 ? kBegins : 0) | cut | slot);
-                if (at < most) p.outputs[at] = s;
-                if (in < most_inner) p.inner[in] = s;
-            }
-        }
-        const int rows = span.len - full * segment;
-        const Count at = atomicAdd(&place[bucket(rows)], (Count)1);
-        if (at < most) p.outputs[at] = make_int4(span.first + full * segment, rows, n, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
-    }
-    __syncthreads();
-    if (tid == 0) p.counts[1] = (int)min(inner, most_inner);
-}
 
 // Four 8 x 8 matrices of bf16, transposed: matrix m's rows are the 16 bytes that lanes 8 m .. 8 m + 7 point at;
 // r[m] holds the elements (row 2 (lane % 4), 2 (lane % 4) + 1; column lane / 4).
@@ -234,29 +151,12 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
         if (lane == 0) mbar_arrive(bar);
     };
     auto gave_up = [&] { return __any_sync(0xffffffffu, dead); };
-    // f(segment and head, chunks, terms) for each of this CTA's, in the same order by every warp: back and forth over
-    // the list, so that who had one of the longest gets one of the shortest next
+    // f(segment and head, chunks, terms) for each of this CTA's, in the same order by every warp
     auto for_items = [&](auto f) {
-        // (one sequence needs no lists)
-        const Span only = a.n_seqs == 1 ? span_of(a, 0) : Span{0, -1};
-        const int slot = a.n_seqs == 1 && slot_of(a, 0) < 0 ? kNoSlot : 0, full = only.len > 0 ? (uint32_t)(only.len - 1) / p.segment : 0;
-        const int count = a.n_seqs > 1 ? p.counts[OUTPUT ? 0 : 1] : only.len < 0 ? 0 : OUTPUT ? full + 1 : slot ? 0 : full;
-        const uint32_t items = (uint32_t)count * a.H;
-        for (uint32_t k = 0;; ++k) {
-            const uint32_t i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (i >= items) break;
-            const uint32_t n = i / (uint32_t)a.H;
-            Item s;
-            if (a.n_seqs == 1) {
-                s = make_int4(only.first + n * p.segment, min(p.segment, only.len - (int)n * p.segment), 0,
-                              (n == 0 ? kBegins : 0) | (n == full ? kEnds : 0) | (full > 0 ? kCut : 0) | slot);
-            } else {
-                s = (OUTPUT ? p.outputs : p.inner)[n];
-            }
-            s.w |= i - n * a.H;
+        for_segments<OUTPUT>(p, blockIdx.x, gridDim.x, [&](const Item &s) {
             // a segment whose states serve o alone does without the third term
             f(s, s.w & kNoSlot ? 0 : (s.y + kTok - 1) / kTok, OUTPUT && (s.w & (kCut | kEnds)) == kCut ? 2 : 3);
-        }
+        });
     };
 
     if (wid == 0) {
@@ -579,7 +479,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     arrive(&sh.gates_empty[st]);
                 }
                 if (chunks > 0) update(c - 1);
-                const int64_t at = (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * a.H + head_of(s);
+                const int64_t at = entry_of(p, s);
                 float *out = p.states + at * kState + (int64_t)(32 * u) * kHeadDim + row;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
@@ -635,11 +535,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     return;
                 }
                 F2 S[16];  // value channels 32 u + 2 e, and the one after
-                const float *init = nullptr;
-                const int64_t at = (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * a.H + head_of(s);
-                if (!(s.w & kBegins)) init = p.states + (at - a.H) * kState;
-                else if (a.initial_state)
-                    init = s.w & kCut ? p.first + at * kState : a.initial_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState;
+                const float *init = state_before(p, s);
                 if (init) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) S[e] = f2(init[place + 2 * e * kHeadDim], init[place + (2 * e + 1) * kHeadDim]);
@@ -761,8 +657,8 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     o_odd = odd;
                     if (i + 1 < chunks) publish();
                 }
-                if ((s.w & kEnds) && a.final_state) {
-                    float *out = a.final_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState + place;
+                if (float *out = state_after(p, s)) {
+                    out += place;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
                 }
@@ -776,13 +672,12 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
         const long long t0 = clock64();
         while (clock64() - t0 < 100000000LL) __nanosleep(1000);
         for_items([&](const Item &s, int, int) {
-            const int64_t at = (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * a.H + head_of(s);
+            const int64_t at = entry_of(p, s);
             float *state = OUTPUT ? nullptr : p.states + at * kState;
             if (OUTPUT) {
                 for (int64_t j = tid; j < (int64_t)s.y * kHeadDim; j += blockDim.x)
                     ((__nv_bfloat16 *)a.o)[((s.x + j / kHeadDim) * a.H + head_of(s)) * kHeadDim + j % kHeadDim] = __float2bfloat16_rn(NAN);
-                if ((s.w & kEnds) && !(s.w & kNoSlot) && a.final_state)
-                    state = a.final_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState;
+                if (!(s.w & kNoSlot)) state = state_after(p, s);
             }
             if (state)
                 for (int j = tid; j < kState; j += blockDim.x) state[j] = NAN;
@@ -792,73 +687,17 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     if (wid == 1) tmem_dealloc(tmem, 512);
 }
 
-// The states in front of the segments of each sequence that is cut, in place of the segments' own: entry l gets
-// that in front of segment l + 1.  A sequence's initial state is copied, because its last segment may
-// overwrite it while the first one still reads.
-constexpr int kJoinThreads = 256, kJoinParts = kState / (4 * kJoinThreads);
-__global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const ChunkParams p) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const LinearChunkArgs &a = p.a;
-    const int h = blockIdx.y;
-    for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
-        const Span span = span_of(a, n);
-        const int64_t slot = slot_of(a, n);
-        if (span.len <= p.segment || slot < 0) continue;
-        const int count = (span.len - 1) / p.segment, entry = span.first / p.segment;
-        const int64_t at = 4 * ((int64_t)blockIdx.z * kJoinThreads + threadIdx.x);
-        const int64_t step = (int64_t)a.H * kState, own = ((int64_t)entry * a.H + h) * kState + at;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (a.initial_state) {
-            x = *(const float4 *)(a.initial_state + (slot * a.H + h) * (int64_t)kState + at);
-            *(float4 *)(p.first + own) = x;
-        }
-        float *state = p.states + own;
-        const float *decay = p.decay + (int64_t)entry * a.H + h;
-        constexpr int kAhead = 8;
-        for (int l = 0; l < count; l += kAhead) {
-            float4 y[kAhead];
-            float d[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (l + j < count) y[j] = *(const float4 *)(state + (l + j) * step), d[j] = decay[(int64_t)(l + j) * a.H];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                if (l + j >= count) break;
-                x.x = fmaf(d[j], x.x, y[j].x), x.y = fmaf(d[j], x.y, y[j].y);
-                x.z = fmaf(d[j], x.z, y[j].z), x.w = fmaf(d[j], x.w, y[j].w);
-                *(float4 *)(state + (l + j) * step) = x;
-            }
-        }
-    }
-}
-
 // Tokens of a segment: so many that the segments of all heads are about as many as SMs.
 inline int64_t segment_of(int64_t total_tokens, int H) {
     const int64_t chunks = (total_tokens + kTok - 1) / kTok, each = std::max<int64_t>(1, sm_count() / H);
     return kTok * std::max<int64_t>(1, (chunks + each - 1) / each);
 }
-inline int64_t entries_of(int64_t total_tokens, int H) {
-    return total_tokens > 0 ? (total_tokens - 1) / segment_of(total_tokens, H) : 0;
-}
-
-struct Layout {
-    size_t outputs, inner, decay, states, total;
-};
-inline Layout layout(int64_t total_tokens, int n_seqs, int H) {
-    const int64_t entries = entries_of(total_tokens, H);
-    Layout l;
-    l.outputs = n_seqs > 1 ? 256 : 0;
-    l.inner = l.outputs + (n_seqs > 1 ? align_up((size_t)(entries + n_seqs) * sizeof(Item), 256) : 0);
-    l.decay = l.inner + (n_seqs > 1 ? align_up((size_t)entries * sizeof(Item), 256) : 0);
-    l.states = l.decay + align_up((size_t)entries * H * sizeof(float), 256);
-    l.total = l.states + (size_t)entries * H * 2 * kState * sizeof(float);
-    return l;
-}
 
 }  // namespace
 
-size_t linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H) { return layout(total_tokens, n_seqs, H).total; }
+size_t linear_chunk_tc_workspace_bytes(int64_t total_tokens, int n_seqs, int H) {
+    return segments_workspace_bytes(total_tokens, n_seqs, H, segment_of(total_tokens, H));
+}
 
 cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream) {
     const int64_t T = a.total_tokens, rows = std::max<int64_t>(T, 1);
@@ -872,36 +711,19 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
         !encode_heads64(&map_v, T ? a.v : none, kHeadDim, a.H, rows, a.v_stride, kTok) ||
         !encode_heads64(&map_o, T ? a.o : none, kHeadDim, a.H, rows, (int64_t)a.H * kHeadDim, kTok))
         return cudaErrorUnknown;
-    ChunkParams p{a};
-    const int64_t segment = segment_of(T, a.H), entries = entries_of(T, a.H);
-    const Layout l = layout(T, a.n_seqs, a.H);
-    uint8_t *ws = (uint8_t *)a.workspace;
-    p.segment = (int)segment;
-    p.entries = (int)entries;
-    p.joined = entries > 0;
-    p.counts = (int *)ws;
-    p.outputs = (Item *)(ws + l.outputs);
-    p.inner = (Item *)(ws + l.inner);
-    p.decay = (float *)(ws + l.decay);
-    p.states = (float *)(ws + l.states);
-    p.first = p.states + entries * a.H * kState;
+    const ChunkParams p = plan_segments(a, segment_of(T, a.H));
     auto launch = [&](auto kernel, int threads, int64_t items) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         return e != cudaSuccess ? e
                                 : launch_dependent(kernel, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(threads),
                                                    kSmemBytes, stream, map_q, map_k, map_v, map_o, p);
     };
-    cudaError_t e = cudaSuccess;
-    if (a.n_seqs > 1) e = launch_dependent(linear_index_kernel, dim3(1), dim3(std::min(kIndexThreads, (a.n_seqs + 31) / 32 * 32)), 0, stream, p);
-    if (e != cudaSuccess) return e;
-    if (entries > 0) {
-        e = launch(linear_chunk_kernel<false>, 640, entries * a.H);
-        if (e == cudaSuccess)
-            e = launch_dependent(linear_join_kernel, dim3((unsigned)std::min(a.n_seqs, 4096), (unsigned)a.H, kJoinParts),
-                                 dim3(kJoinThreads), 0, stream, p);
-        if (e != cudaSuccess) return e;
+    cudaError_t e = launch_segment_lists(p, stream);
+    if (e == cudaSuccess && p.entries > 0) {
+        e = launch(linear_chunk_kernel<false>, 640, (int64_t)p.entries * a.H);
+        if (e == cudaSuccess) e = launch_segment_join(p, stream);
     }
-    e = launch(linear_chunk_kernel<true>, 896, (entries + a.n_seqs) * a.H);
+    if (e == cudaSuccess) e = launch(linear_chunk_kernel<true>, 896, ((int64_t)p.entries + a.n_seqs) * a.H);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -1,0 +1,163 @@
+// Segments of a chunked linear-attention forward: the lists of them, and the join of their states.
+#include <algorithm>
+
+#include "kda_linear_segments.cuh"
+
+namespace kda {
+namespace {
+
+// The segments: a list of all for the outputs, sorted by length (into kBuckets classes), and one of those that have a
+// successor.  Their order in a class is left to chance; what is computed does not depend on it.  (Sequences that
+// overlap, as no well-formed offsets do, may be more than the lists hold; what is past their ends is left out.)
+constexpr int kIndexThreads = 1024, kBuckets = 64;
+typedef unsigned long long Count;
+__global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const ChunkParams p) {
+    __shared__ Count place[kBuckets], inner;
+    const LinearChunkArgs &a = p.a;
+    const int tid = threadIdx.x, segment = p.segment;
+    const Count most = p.entries + a.n_seqs, most_inner = p.entries;
+    for (int i = tid; i < kBuckets; i += blockDim.x) place[i] = 0;
+    if (tid == 0) inner = 0;
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const float scale = (kBuckets - 1) / (float)segment;
+    auto bucket = [&](int rows) { return max(0, kBuckets - 1 - (int)(rows * scale)); };
+    const int threads = blockDim.x;
+#pragma unroll 1
+    for (int n = tid; n < a.n_seqs; n += threads) {
+        const Span span = span_of(a, n);
+        if (span.len < 0) continue;
+        const int full = span.len > 0 ? (span.len - 1) / segment : 0;  // segments before the last one
+        if (full > 0) atomicAdd(&place[0], (Count)full);
+        atomicAdd(&place[bucket(span.len - full * segment)], (Count)1);
+    }
+    __syncthreads();
+    if (tid < 32) {
+        const Count x = place[2 * tid], own = x + place[2 * tid + 1];
+        Count upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Count y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (tid >= o) upto += y;
+        }
+        place[2 * tid] = upto - own;
+        place[2 * tid + 1] = upto - own + x;
+        if (tid == 31) p.counts[0] = (int)min(upto, most);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int n = tid; n < a.n_seqs; n += threads) {
+        const Span span = span_of(a, n);
+        if (span.len < 0) continue;
+        const int full = span.len > 0 ? (span.len - 1) / segment : 0, slot = slot_of(a, n) < 0 ? kNoSlot : 0;
+        const int cut = full > 0 ? kCut : 0;
+        if (full > 0) {
+            Count at = atomicAdd(&place[0], (Count)full), in = slot ? most_inner : atomicAdd(&inner, (Count)full);
+#pragma unroll 1
+            for (int l = 0; l < full; ++l, ++at, ++in) {
+                const Item s = make_int4(span.first + l * segment, segment, n, (l == 0 ? kBegins : 0) | cut | slot);
+                if (at < most) p.outputs[at] = s;
+                if (in < most_inner) p.inner[in] = s;
+            }
+        }
+        const int rows = span.len - full * segment;
+        const Count at = atomicAdd(&place[bucket(rows)], (Count)1);
+        if (at < most) p.outputs[at] = make_int4(span.first + full * segment, rows, n, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
+    }
+    __syncthreads();
+    if (tid == 0) p.counts[1] = (int)min(inner, most_inner);
+}
+
+// The states in front of the segments of each sequence that is cut, in place of the segments' own: entry l gets
+// that in front of segment l + 1.  A sequence's initial state is copied, because its last segment may
+// overwrite it while the first one still reads.
+constexpr int kJoinThreads = 256, kJoinParts = kState / (4 * kJoinThreads);
+__global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const LinearChunkArgs &a = p.a;
+    const int h = blockIdx.y;
+    for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
+        const Span span = span_of(a, n);
+        const int64_t slot = slot_of(a, n);
+        if (span.len <= p.segment || slot < 0) continue;
+        const int count = (span.len - 1) / p.segment, entry = span.first / p.segment;
+        const int64_t at = 4 * ((int64_t)blockIdx.z * kJoinThreads + threadIdx.x);
+        const int64_t step = (int64_t)a.H * kState, own = ((int64_t)entry * a.H + h) * kState + at;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.initial_state) {
+            x = *(const float4 *)(a.initial_state + (slot * a.H + h) * (int64_t)kState + at);
+            *(float4 *)(p.first + own) = x;
+        }
+        float *state = p.states + own;
+        const float *decay = p.decay + (int64_t)entry * a.H + h;
+        constexpr int kAhead = 8;
+        for (int l = 0; l < count; l += kAhead) {
+            float4 y[kAhead];
+            float d[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (l + j < count) y[j] = *(const float4 *)(state + (l + j) * step), d[j] = decay[(int64_t)(l + j) * a.H];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (l + j >= count) break;
+                x.x = fmaf(d[j], x.x, y[j].x), x.y = fmaf(d[j], x.y, y[j].y);
+                x.z = fmaf(d[j], x.z, y[j].z), x.w = fmaf(d[j], x.w, y[j].w);
+                *(float4 *)(state + (l + j) * step) = x;
+            }
+        }
+    }
+}
+
+// A segment's entry is floor(first token / segment): distinct for those that have a successor, whatever the lengths.
+inline int64_t entries_of(int64_t total_tokens, int64_t segment) { return total_tokens > 0 ? (total_tokens - 1) / segment : 0; }
+
+struct Layout {
+    size_t outputs, inner, decay, states, total;
+};
+inline Layout layout(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
+    const int64_t entries = entries_of(total_tokens, segment);
+    const bool lists = n_seqs > 1;
+    Layout l;
+    l.outputs = lists ? 256 : 0;
+    l.inner = l.outputs + (lists ? align_up((size_t)(entries + n_seqs) * sizeof(Item), 256) : 0);
+    l.decay = l.inner + (lists ? align_up((size_t)entries * sizeof(Item), 256) : 0);
+    l.states = l.decay + align_up((size_t)entries * H * sizeof(float), 256);
+    l.total = l.states + (size_t)entries * H * 2 * kState * sizeof(float);
+    return l;
+}
+
+}  // namespace
+
+size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
+    return layout(total_tokens, n_seqs, H, segment).total;
+}
+
+ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment) {
+    const Layout l = layout(a.total_tokens, a.n_seqs, a.H, segment);
+    uint8_t *ws = (uint8_t *)a.workspace;
+    ChunkParams p{a};
+    p.segment = (int)segment;
+    p.entries = (int)entries_of(a.total_tokens, segment);
+    p.joined = p.entries > 0;
+    p.counts = (int *)ws;
+    p.outputs = (Item *)(ws + l.outputs);
+    p.inner = (Item *)(ws + l.inner);
+    p.decay = (float *)(ws + l.decay);
+    p.states = (float *)(ws + l.states);
+    p.first = p.states + (int64_t)p.entries * a.H * kState;
+    return p;
+}
+
+cudaError_t launch_segment_lists(const ChunkParams &p, cudaStream_t stream) {
+    if (p.a.n_seqs == 1) return cudaSuccess;
+    return launch_dependent(segment_lists_kernel, dim3(1), dim3(std::min(kIndexThreads, (p.a.n_seqs + 31) / 32 * 32)), 0, stream, p);
+}
+
+cudaError_t launch_segment_join(const ChunkParams &p, cudaStream_t stream) {
+    return launch_dependent(segment_join_kernel, dim3((unsigned)std::min(p.a.n_seqs, 4096), (unsigned)p.a.H, kJoinParts),
+                            dim3(kJoinThreads), 0, stream, p);
+}
+
+}  // namespace kda
