@@ -1,26 +1,39 @@
 // Linear attention with one decay a head over packed fp32 sequences, token by token on the CUDA cores:
 //   S <- e^g S + k v^T,  o = scale S^T q
 //
-// 6 * 128 * 128 fp32 operations a token and head.  A CTA takes sixteen rows of S^T (value
-// channels) of one (segment, head), eight lanes a row and sixteen key channels a lane in
-// registers.  Tokens come through shared memory in blocks of sixteen, the next block requested
-// while one is worked on; four tokens share the lanes' exchange for o.  What bounds it is the chain of
-// a token's instructions, so that long sequences are cut into segments (kda_linear_segments.cuh):
-// two sequences of 1001 and 500 tokens, 16 heads, @ us, 252 us uncut and with an exchange a token.
+// A CTA takes 32 rows of S^T (value channels) of one (segment, head), eight lanes for two rows and sixteen key
+// channels a lane, in registers.  Tokens come through shared memory in blocks of sixteen, the next block
+// requested while one is worked on; four tokens share the lanes' exchange for o.
 //
-// A decay near one is the sum of two floats: as one, its rounding error would come back in every
-// token that it is applied to (a fixed decay of 2^-8 a token: 1e-5 in the state).
+// Eight tokens at a time with G_t the decays since their first one: S_t = e^{G_t} (S_0 + sum_j e^{-G_j} k_j v_j^T), so
+// that an element of the state costs one fma a token, and one for o, and e^{G_8} once in eight;
+// in fp32 while |G| < 8 (2^-22 in e^{G_t - G_j}), else token by token.  Sequences are cut into
+// segments (kda_linear_segments.cuh).  Two sequences of 1001 and 500 tokens, 16 heads: @ us; 196 with
+// a product for each decay and one row a thread, 252 uncut and with an exchange a token.
+//
+// A decay near one is the sum of two floats: as one, its rounding error would come back every
+// time that it is applied (a fixed decay of 2^-8 a token: 1e-5 in the state).
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_linear_segments.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kRows = 16;  // of S^T, a CTA
-constexpr int kLanes = 8;  // of a row
-constexpr int kThreads = kRows * kLanes;
+constexpr int kRows = 32;   // of S^T, a CTA: two a thread, 16 apart
+constexpr int kLanes = 8;   // of a row
+constexpr int kThreads = kRows / 2 * kLanes;
 constexpr int kBlock = 16;  // tokens in shared memory at a time
+constexpr int kSub = 8;     // tokens that share a reference for their decays
+constexpr float kMostDecay = 8.0f;
+
+// e^g as the sum of two floats
+__device__ __forceinline__ float2 decay_of(float g) {
+    const float d = expf(g);
+    // (d - 1 is exact from 1/2 to 2; smaller decays leave nothing for their error to come back in)
+    return make_float2(d, d > 0.5f && d < 2.0f ? expm1f(g) - (d - 1.0f) : 0.0f);
+}
 
 // OUTPUT: o and final states, from the states in front of the segments; else a segment's own state.
 template <bool OUTPUT>
@@ -28,7 +41,10 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
     // (a row of 128 channels as 8 lanes of 16: channel 32 i + 4 l + j is lane l's)
     __shared__ __align__(16) float sq[OUTPUT ? kBlock : 1][kHeadDim], sk[kBlock][kHeadDim];
     __shared__ float sv[kBlock][kRows];
-    __shared__ float2 sg[kBlock];
+    __shared__ float2 sg[kBlock];          // a token's decay
+    __shared__ float2 su[kBlock];          // e^{G_t}, e^{-G_t}
+    __shared__ float2 se[kBlock / kSub];   // e^{G_8}
+    __shared__ bool strong[kBlock / kSub]; // |G| >= kMostDecay
     griddep_wait();
     griddep_launch_dependents();
     const LinearChunkArgs &a = p.a;
@@ -43,12 +59,13 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
             return;
         }
         const int place = (row0 + row) * kHeadDim + 4 * l;  // of this thread's part of a state
-        F2 s[8];
+        constexpr int kOther = kRows / 2 * kHeadDim;        // its second row's, behind it
+        F2 s[2][8];
         const float *init = OUTPUT ? state_before(p, seg) : nullptr;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 x = init ? *(const float4 *)(init + place + 32 * i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            s[2 * i] = f2(x.x, x.y), s[2 * i + 1] = f2(x.z, x.w);
+        for (int i = 0; i < 8; ++i) {
+            const float4 x = init ? *(const float4 *)(init + place + (i >> 2) * kOther + 32 * (i & 3)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            s[i >> 2][2 * (i & 3)] = f2(x.x, x.y), s[i >> 2][2 * (i & 3) + 1] = f2(x.z, x.w);
         }
         const float *q = (const float *)a.q + h / a.group * kHeadDim, *k = (const float *)a.k + h / a.group * kHeadDim,
                     *v = (const float *)a.v + h * kHeadDim + row0;
@@ -81,72 +98,114 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
             }
 #pragma unroll
             for (int i = 0; i < kBlock * kRows / kThreads; ++i) sv[(tid + i * kThreads) / kRows][tid % kRows] = rv[i];
-            if (tid < kBlock) {
-                const float d = expf(rg);
-                // (d - 1 is exact from 1/2 to 2; smaller decays leave nothing for their error to come back in)
-                sg[tid] = make_float2(d, d > 0.5f && d < 2.0f ? expm1f(rg) - (d - 1.0f) : 0.0f);
-                total += rg;
+            if (tid < 32) {
+                const float g = tid < kBlock ? rg : 0.0f;
+                float G = g;
+#pragma unroll
+                for (int m = 1; m < kSub; m <<= 1) {
+                    const float x = __shfl_up_sync(0xffffffffu, G, m);
+                    if (tid % kSub >= m) G += x;
+                }
+                const uint32_t weak = __ballot_sync(0xffffffffu, fabsf(G) < kMostDecay);
+                if (tid < kBlock) {
+                    sg[tid] = decay_of(g);
+                    su[tid] = make_float2(expf(G), expf(-G));
+                    if (tid % kSub == kSub - 1) {
+                        se[tid / kSub] = decay_of(G);
+                        strong[tid / kSub] = ((weak >> (tid - (kSub - 1))) & 0xff) != 0xff;
+                    }
+                    total += g;
+                }
             }
             __syncthreads();
             request(t0 + kBlock);
-            const int block = min(kBlock, len - t0);
-            auto step = [&](int t) {  // this lane's part of row . q
-                const float2 d = sg[t];
-                const float vt = sv[t][row];
-                F2 sum = 0;
+            // o of a token, from this lane's parts of row . q: the sums over eight lanes of four values (of two rows and two
+            // tokens): lane l gets that of value l % 4
+            auto reduce = [&](float (&x)[4]) {
+#pragma unroll
+                for (int m = 2; m > 0; m >>= 1) {
+                    const bool hi = l & m;
+#pragma unroll
+                    for (int i = 0; i < m; ++i) {
+                        const float send = hi ? x[i] : x[i + m];
+                        x[i] = (hi ? x[i + m] : x[i]) + __shfl_xor_sync(0xffffffffu, send, m);
+                    }
+                }
+                return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 4);
+            };
+            // one token: S += k v^T, behind a product with its decay where the tokens have no reference; x: this lane's parts of S^T q
+            auto step = [&](int t, auto decays, float (&x)[2]) {
+                const float2 d = decays ? sg[t] : su[t];
+                F2 v2[2], sum[2] = {0, 0};
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float vt = sv[t][row + r * (kRows / 2)] * (decays ? 1.0f : d.y);
+                    v2[r] = f2(vt, vt);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float4 kk = *(const float4 *)&sk[t][4 * l + 32 * i];
                     const F2 k2[2] = {f2(kk.x, kk.y), f2(kk.z, kk.w)};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        s[2 * i + j] = fma2(f2(d.x, d.x), s[2 * i + j], fma2(f2(d.y, d.y), s[2 * i + j], mul2(f2(vt, vt), k2[j])));
+                    F2 q2[2];
                     if (OUTPUT) {
                         const float4 qq = *(const float4 *)&sq[t][4 * l + 32 * i];
-                        sum = fma2(s[2 * i], f2(qq.x, qq.y), sum);
-                        sum = fma2(s[2 * i + 1], f2(qq.z, qq.w), sum);
+                        q2[0] = f2(qq.x, qq.y), q2[1] = f2(qq.z, qq.w);
                     }
-                }
-                float lo, hi;
-                unf2(sum, lo, hi);
-                return lo + hi;
-            };
-            int t = 0;
-            for (; t + 4 <= block; t += 4) {
-                float x[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = step(t + i);
-                if (OUTPUT) {
-                    // the sums over eight lanes of four tokens: lane l gets token l % 4's
+                    for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int m = 2; m > 0; m >>= 1) {
-                        const bool hi = l & m;
-#pragma unroll
-                        for (int i = 0; i < m; ++i) {
-                            const float send = hi ? x[i] : x[i + m];
-                            x[i] = (hi ? x[i + m] : x[i]) + __shfl_xor_sync(0xffffffffu, send, m);
+                        for (int j = 0; j < 2; ++j) {
+                            F2 &y = s[r][2 * i + j];
+                            if (decays) y = fma2(f2(d.x, d.x), y, fma2(f2(d.y, d.y), y, mul2(v2[r], k2[j])));
+                            else y = fma2(v2[r], k2[j], y);
+                            if (OUTPUT) sum[r] = fma2(y, q2[j], sum[r]);
                         }
-                    }
-                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 4);
-                    if (l < 4) o[(first + t0 + t + l) * a.H * kHeadDim + row] = a.scale * x[0];
                 }
-            }
-            for (; t < block; ++t) {
-                float x = step(t);
-                if (OUTPUT) {
 #pragma unroll
-                    for (int m = 1; m < kLanes; m <<= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-                    if (l == 0) o[(first + t0 + t) * a.H * kHeadDim + row] = a.scale * x;
+                for (int r = 0; r < 2; ++r) {
+                    float lo, hi;
+                    unf2(sum[r], lo, hi);
+                    x[r] = (lo + hi) * (decays ? 1.0f : d.x);
+                }
+            };
+            auto tokens = [&](int begin, int end, auto decays) {
+#pragma unroll 1
+                for (int t = begin; t < end; t += 2) {
+                    float x[2][2] = {};
+                    step(t, decays, x[0]);
+                    if (t + 1 < end) step(t + 1, decays, x[1]);
+                    if (OUTPUT) {
+                        float y[4] = {x[0][0], x[0][1], x[1][0], x[1][1]};
+                        const float sum = reduce(y);
+                        if (l < 4 && t + (l >> 1) < end)
+                            o[(first + t0 + t + (l >> 1)) * a.H * kHeadDim + row + (l & 1) * (kRows / 2)] = a.scale * sum;
+                    }
+                }
+            };
+            const int block = min(kBlock, len - t0);
+#pragma unroll 1
+            for (int b = 0; b * kSub < block; ++b) {
+                const int end = min((b + 1) * kSub, block);
+                if (strong[b]) {
+                    tokens(b * kSub, end, std::true_type());
+                } else {
+                    tokens(b * kSub, end, std::false_type());
+                    const float2 d = se[b];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        F2 &y = s[i >> 3][i & 7];
+                        y = fma2(f2(d.x, d.x), y, mul2(f2(d.y, d.y), y));
+                    }
                 }
             }
         }
         float *out = OUTPUT ? state_after(p, seg) : p.states + entry_of(p, seg) * kState;
         if (out)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 float4 x;
-                unf2(s[2 * i], x.x, x.y), unf2(s[2 * i + 1], x.z, x.w);
-                *(float4 *)(out + place + 32 * i) = x;
+                unf2(s[i >> 2][2 * (i & 3)], x.x, x.y), unf2(s[i >> 2][2 * (i & 3) + 1], x.z, x.w);
+                *(float4 *)(out + place + (i >> 2) * kOther + 32 * (i & 3)) = x;
             }
         if (!OUTPUT && blockIdx.y == 0 && tid < 32) {
             total = warp_sum(tid < kBlock ? total : 0.0f);
