@@ -70,6 +70,9 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
         const float *q = (const float *)a.q + h / a.group * kHeadDim, *k = (const float *)a.k + h / a.group * kHeadDim,
                     *v = (const float *)a.v + h * kHeadDim + row0;
         constexpr int kVecs = kBlock * kHeadDim / 4 / kThreads;  // of four channels, of q (and of k) a thread
+        // where lane l's share of four tokens' o goes: row (l & 1) of token l >> 1
+        const int64_t o_step = (int64_t)a.H * kHeadDim;
+        float *o_at = o + (first + (l >> 1)) * o_step + row + (l & 1) * (kRows / 2);
         float4 rq[kVecs], rk[kVecs];
         float rv[kBlock * kRows / kThreads], rg = 0.0f, total = 0.0f;
         auto request = [&](int t0) {
@@ -119,11 +122,10 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
             }
             __syncthreads();
             request(t0 + kBlock);
-            // o of a token, from this lane's parts of row . q: the sums over eight lanes of four values (of two rows and two
-            // tokens): lane l gets that of value l % 4
-            auto reduce = [&](float (&x)[4]) {
+            // the sums over eight lanes of eight values (two rows of four tokens): lane l gets that of value l
+            auto reduce = [&](float (&x)[8]) {
 #pragma unroll
-                for (int m = 2; m > 0; m >>= 1) {
+                for (int m = 4; m > 0; m >>= 1) {
                     const bool hi = l & m;
 #pragma unroll
                     for (int i = 0; i < m; ++i) {
@@ -131,10 +133,10 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
                         x[i] = (hi ? x[i + m] : x[i]) + __shfl_xor_sync(0xffffffffu, send, m);
                     }
                 }
-                return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 4);
+                return x[0];
             };
             // one token: S += k v^T, behind a product with its decay where the tokens have no reference; x: this lane's parts of S^T q
-            auto step = [&](int t, auto decays, float (&x)[2]) {
+            auto step = [&](int t, auto decays, float *x) {
                 const float2 d = decays ? sg[t] : su[t];
                 F2 v2[2], sum[2] = {0, 0};
 #pragma unroll
@@ -170,15 +172,19 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
             };
             auto tokens = [&](int begin, int end, auto decays) {
 #pragma unroll 1
-                for (int t = begin; t < end; t += 2) {
-                    float x[2][2] = {};
-                    step(t, decays, x[0]);
-                    if (t + 1 < end) step(t + 1, decays, x[1]);
+                for (int t = begin; t < end; t += 4) {
+                    float x[8] = {};
+                    if (t + 4 <= end) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) step(t + i, decays, x + 2 * i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+                            if (t + i < end) step(t + i, decays, x + 2 * i);
+                    }
                     if (OUTPUT) {
-                        float y[4] = {x[0][0], x[0][1], x[1][0], x[1][1]};
-                        const float sum = reduce(y);
-                        if (l < 4 && t + (l >> 1) < end)
-                            o[(first + t0 + t + (l >> 1)) * a.H * kHeadDim + row + (l & 1) * (kRows / 2)] = a.scale * sum;
+                        const float sum = reduce(x);
+                        if (t + (l >> 1) < end) o_at[(int64_t)(t0 + t) * o_step] = a.scale * sum;
                     }
                 }
             };
@@ -214,10 +220,10 @@ __global__ void __launch_bounds__(kThreads) linear_chunk_f32_kernel(const ChunkP
     });
 }
 
-// Tokens of a segment: so many that there are some four CTAs a SM, and no fewer than cost what the cut costs.
+// Tokens of a segment: so many that there are some twelve CTAs a SM, of which three are resident.
 inline int64_t segment_of(int64_t total_tokens, int H) {
-    constexpr int64_t kLeast = 128;
-    const int64_t each = std::max<int64_t>(1, 4 * sm_count() / (H * (kHeadDim / kRows)));
+    constexpr int64_t kLeast = 64;
+    const int64_t each = std::max<int64_t>(1, 12 * sm_count() / (H * (kHeadDim / kRows)));
     return kLeast * std::max<int64_t>(1, (total_tokens + each * kLeast - 1) / (each * kLeast));
 }
 
