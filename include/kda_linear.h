@@ -85,6 +85,7 @@ size_t kda_linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H,
  *                  [N, H, V, K], or pools of n_slots states indexed by
  *                  state_indices (distinct); initial_state NULL = zeros,
  *                  final_state NULL = not written, final_state may be initial_state
+ *   o              shares no memory with the inputs or the states
  * bf16 runs on the tensor cores: chunks of 128 tokens, fp32 accumulation and states;
  * the scores and the state enter the products that give o as bf16 (two roundings
  * beside o's own); what is written to the state is split into three bf16 terms, so

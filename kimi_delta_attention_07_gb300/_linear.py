@@ -143,9 +143,9 @@ def kda_linear_chunk_fwd(q, k, v, g, *, cu_seqlens=None, n_seqs=None, initial_st
         slots = N
     else:
         held = [t.shape[0] for t in (initial_state, final_state) if t is not None]
-        if final_state is None and output_final_state:
+        if not held or (final_state is None and output_final_state):
             raise ValueError("with state_indices, final_state must be the destination pool")
-        slots = min(held, default=0) if n_slots is None else int(n_slots)
+        slots = min(held) if n_slots is None else int(n_slots)
     p0 = pf = None
     for name, t in (("initial_state", initial_state), ("final_state", final_state)):
         if t is None:

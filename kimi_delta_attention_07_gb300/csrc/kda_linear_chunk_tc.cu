@@ -351,8 +351,10 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             const int first16 = (g * kWidth & 63) >> 3;
             if (__builtin_expect(rows < kTok, 0)) {
                 if (row >= rows)
-                    for (int j = 0; j < kWidth / 8; ++j)
-                        *(uint4 *)(v + 16 * (first16 + j)) = *(uint4 *)(v - kTile + 16 * (first16 + j)) = make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < kWidth / 8; ++j) {
+                        const int at = ((first16 + j) ^ (row & 7)) << 4;
+                        *(uint4 *)(v + at) = *(uint4 *)(v - kTile + at) = make_uint4(0, 0, 0, 0);
+                    }
                 __syncwarp();
                 named_bar_sync(5, 128 * kGroups);
             }
@@ -430,7 +432,11 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     check(c, min(kTok, s.y - i * kTok));
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e, ++kt) {
-                        make_kt(c, g + 2 * e, terms, tmem + kTmK + g * kTmBuf + lanes, &sh.kt_empty[g], (kt & 1) ^ 1);
+                        if (32 * (g + 2 * e) < s.y - i * kTok) {
+                            make_kt(c, g + 2 * e, terms, tmem + kTmK + g * kTmBuf + lanes, &sh.kt_empty[g], (kt & 1) ^ 1);
+                        } else {  // no token: the quarter's products are left out, too
+                            wait(&sh.kt_empty[g], (kt & 1) ^ 1);
+                        }
                         arrive(&sh.kt_full[g]);
                     }
                     arrive(&sh.k_empty[c % kStages]);
@@ -687,16 +693,19 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     if (wid == 1) tmem_dealloc(tmem, 512);
 }
 
-// Tokens of a segment: so many that the segments of all heads are about as many as SMs.
-inline int64_t segment_of(int64_t total_tokens, int H) {
+// Tokens of a segment: so many that the segments of all heads are about as many as SMs.  A cut costs two launches
+// and some 10 us, as much as three chunks: five chunks are left whole, no segment has fewer than two of them, or, where
+// there are several sequences, four.  (5 sequences of 17 to 200 tokens, 8 heads: 22.8 us of the device cut by the chunk, @ whole.)
+inline int64_t segment_of(int64_t total_tokens, int n_seqs, int H) {
     const int64_t chunks = (total_tokens + kTok - 1) / kTok, each = std::max<int64_t>(1, sm_count() / H);
-    return kTok * std::max<int64_t>(1, (chunks + each - 1) / each);
+    if (chunks <= 5) return kTok * std::max<int64_t>(1, chunks);
+    return kTok * std::max<int64_t>(n_seqs == 1 ? 2 : 4, (chunks + each - 1) / each);
 }
 
 }  // namespace
 
 size_t linear_chunk_tc_workspace_bytes(int64_t total_tokens, int n_seqs, int H) {
-    return segments_workspace_bytes(total_tokens, n_seqs, H, segment_of(total_tokens, H));
+    return segments_workspace_bytes(total_tokens, n_seqs, H, segment_of(total_tokens, n_seqs, H));
 }
 
 cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream) {
@@ -711,7 +720,7 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
         !encode_heads64(&map_v, T ? a.v : none, kHeadDim, a.H, rows, a.v_stride, kTok) ||
         !encode_heads64(&map_o, T ? a.o : none, kHeadDim, a.H, rows, (int64_t)a.H * kHeadDim, kTok))
         return cudaErrorUnknown;
-    const ChunkParams p = plan_segments(a, segment_of(T, a.H));
+    const ChunkParams p = plan_segments(a, segment_of(T, a.n_seqs, a.H));
     auto launch = [&](auto kernel, int threads, int64_t items) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         return e != cudaSuccess ? e

@@ -12,12 +12,12 @@ namespace {
 constexpr int kIndexThreads = 1024, kBuckets = 64;
 typedef unsigned long long Count;
 __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const ChunkParams p) {
-    __shared__ Count place[kBuckets], inner;
+    __shared__ Count place[kBuckets], inner, cuts;
     const LinearChunkArgs &a = p.a;
     const int tid = threadIdx.x, segment = p.segment;
     const Count most = p.entries + a.n_seqs, most_inner = p.entries;
     for (int i = tid; i < kBuckets; i += blockDim.x) place[i] = 0;
-    if (tid == 0) inner = 0;
+    if (tid == 0) inner = cuts = 0;
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
@@ -50,23 +50,25 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
     for (int n = tid; n < a.n_seqs; n += threads) {
         const Span span = span_of(a, n);
         if (span.len < 0) continue;
-        const int full = span.len > 0 ? (span.len - 1) / segment : 0, slot = slot_of(a, n) < 0 ? kNoSlot : 0;
+        const int full = span.len > 0 ? (span.len - 1) / segment : 0, at_slot = (int)slot_of(a, n), slot = at_slot < 0 ? kNoSlot : 0;
         const int cut = full > 0 ? kCut : 0;
         if (full > 0) {
             Count at = atomicAdd(&place[0], (Count)full), in = slot ? most_inner : atomicAdd(&inner, (Count)full);
+            const Count c = slot ? most_inner : atomicAdd(&cuts, (Count)1);
+            if (c < most_inner) p.cuts[c] = make_int4(span.first, full, at_slot, 0);
 #pragma unroll 1
             for (int l = 0; l < full; ++l, ++at, ++in) {
-                const Item s = make_int4(span.first + l * segment, segment, n, (l == 0 ? kBegins : 0) | cut | slot);
+                const Item s = make_int4(span.first + l * segment, segment, at_slot, (l == 0 ? kBegins : 0) | cut | slot);
                 if (at < most) p.outputs[at] = s;
                 if (in < most_inner) p.inner[in] = s;
             }
         }
         const int rows = span.len - full * segment;
         const Count at = atomicAdd(&place[bucket(rows)], (Count)1);
-        if (at < most) p.outputs[at] = make_int4(span.first + full * segment, rows, n, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
+        if (at < most) p.outputs[at] = make_int4(span.first + full * segment, rows, at_slot, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
     }
     __syncthreads();
-    if (tid == 0) p.counts[1] = (int)min(inner, most_inner);
+    if (tid == 0) p.counts[1] = (int)min(inner, most_inner), p.counts[2] = (int)min(cuts, most_inner);
 }
 
 // The states in front of the segments of each sequence that is cut, in place of the segments' own: entry l gets
@@ -78,16 +80,22 @@ __global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkP
     griddep_launch_dependents();
     const LinearChunkArgs &a = p.a;
     const int h = blockIdx.y;
-    for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
-        const Span span = span_of(a, n);
-        const int64_t slot = slot_of(a, n);
-        if (span.len <= p.segment || slot < 0) continue;
-        const int count = (span.len - 1) / p.segment, entry = span.first / p.segment;
+    Item only = make_int4(0, 0, 0, 0);
+    if (a.n_seqs == 1) {
+        const Span span = span_of(a, 0);
+        const int64_t slot = slot_of(a, 0);
+        if (span.len <= p.segment || slot < 0) return;
+        only = make_int4(span.first, (span.len - 1) / p.segment, (int)slot, 0);
+    }
+    const int listed = a.n_seqs == 1 ? 1 : p.counts[2];
+    for (int i = blockIdx.x; i < listed; i += gridDim.x) {
+        const Item s = a.n_seqs == 1 ? only : p.cuts[i];
+        const int count = s.y, entry = s.x / p.segment;
         const int64_t at = 4 * ((int64_t)blockIdx.z * kJoinThreads + threadIdx.x);
         const int64_t step = (int64_t)a.H * kState, own = ((int64_t)entry * a.H + h) * kState + at;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (a.initial_state) {
-            x = *(const float4 *)(a.initial_state + (slot * a.H + h) * (int64_t)kState + at);
+            x = *(const float4 *)(a.initial_state + ((int64_t)s.z * a.H + h) * kState + at);
             *(float4 *)(p.first + own) = x;
         }
         float *state = p.states + own;
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkP
 inline int64_t entries_of(int64_t total_tokens, int64_t segment) { return total_tokens > 0 ? (total_tokens - 1) / segment : 0; }
 
 struct Layout {
-    size_t outputs, inner, decay, states, total;
+    size_t outputs, inner, cuts, decay, states, total;
 };
 inline Layout layout(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
     const int64_t entries = entries_of(total_tokens, segment);
@@ -122,7 +130,8 @@ inline Layout layout(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
     Layout l;
     l.outputs = lists ? 256 : 0;
     l.inner = l.outputs + (lists ? align_up((size_t)(entries + n_seqs) * sizeof(Item), 256) : 0);
-    l.decay = l.inner + (lists ? align_up((size_t)entries * sizeof(Item), 256) : 0);
+    l.cuts = l.inner + (lists ? align_up((size_t)entries * sizeof(Item), 256) : 0);
+    l.decay = l.cuts + (lists ? align_up((size_t)entries * sizeof(Item), 256) : 0);
     l.states = l.decay + align_up((size_t)entries * H * sizeof(float), 256);
     l.total = l.states + (size_t)entries * H * 2 * kState * sizeof(float);
     return l;
@@ -144,6 +153,7 @@ ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment) {
     p.counts = (int *)ws;
     p.outputs = (Item *)(ws + l.outputs);
     p.inner = (Item *)(ws + l.inner);
+    p.cuts = (Item *)(ws + l.cuts);
     p.decay = (float *)(ws + l.decay);
     p.states = (float *)(ws + l.states);
     p.first = p.states + (int64_t)p.entries * a.H * kState;
@@ -156,7 +166,7 @@ cudaError_t launch_segment_lists(const ChunkParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_segment_join(const ChunkParams &p, cudaStream_t stream) {
-    return launch_dependent(segment_join_kernel, dim3((unsigned)std::min(p.a.n_seqs, 4096), (unsigned)p.a.H, kJoinParts),
+    return launch_dependent(segment_join_kernel, dim3((unsigned)std::min(p.a.n_seqs, p.entries), (unsigned)p.a.H, kJoinParts),
                             dim3(kJoinThreads), 0, stream, p);
 }
 

@@ -12,7 +12,7 @@ constexpr int kState = kHeadDim * kHeadDim;
 // A segment to work on, in four registers: what warps look at in every chunk must not be in local memory,
 // for which the L1 cache has no room beside this shared memory.
 enum : int { kBegins = 1 << 16, kEnds = 1 << 17, kCut = 1 << 18, kNoSlot = 1 << 19 };
-typedef int4 Item;  // first token, tokens, sequence, flags (and in the low 16 bits, once it is picked, the head)
+typedef int4 Item;  // first token, tokens, slot of the states, flags (and in the low 16 bits, once it is picked, the head)
 __device__ __forceinline__ int head_of(const Item &s) { return s.w & 0xffff; }
 
 struct ChunkParams {
@@ -20,9 +20,10 @@ struct ChunkParams {
     int segment;    // tokens
     int entries;    // segments whose state the workspace holds, at most; floor(first token / segment) is a segment's
     bool joined;    // the kernel follows the others: its inputs are there before it begins
-    int *counts;    // segments of each list (no lists of a single sequence)
+    int *counts;    // length of each list (no lists of a single sequence)
     Item *outputs;  // all segments, the longest first
     Item *inner;    // [entries]: those that others follow in their sequence
+    Item *cuts;     // [entries]: the sequences that are cut: first token, such segments, slot
     float *states;  // [entries][H][V][K]
     float *first;   // [entries][H][V][K]: copies of initial states (those that a later CTA may overwrite)
     float *decay;   // [entries][H]
@@ -36,8 +37,8 @@ __device__ __forceinline__ void for_segments(const ChunkParams &p, uint32_t cta,
     // (one sequence needs no lists)
     const bool one = a.n_seqs == 1;
     const Span only = one ? span_of(a, 0) : Span{0, -1};
-    const int slot = one && slot_of(a, 0) < 0 ? kNoSlot : 0, full = only.len > 0 ? (uint32_t)(only.len - 1) / p.segment : 0;
-    const int count = !one ? p.counts[OUTPUT ? 0 : 1] : only.len < 0 ? 0 : OUTPUT ? full + 1 : slot ? 0 : full;
+    const int slot = one ? (int)slot_of(a, 0) : 0, full = only.len > 0 ? (uint32_t)(only.len - 1) / p.segment : 0;
+    const int count = !one ? p.counts[OUTPUT ? 0 : 1] : only.len < 0 ? 0 : OUTPUT ? full + 1 : slot < 0 ? 0 : full;
     const uint32_t items = (uint32_t)count * a.H;
     for (uint32_t k = 0;; ++k) {
         const uint32_t i = k * ctas + (k & 1 ? ctas - 1 - cta : cta);
@@ -45,8 +46,8 @@ __device__ __forceinline__ void for_segments(const ChunkParams &p, uint32_t cta,
         const uint32_t n = i / (uint32_t)a.H;
         Item s;
         if (one) {
-            s = make_int4(only.first + n * p.segment, min(p.segment, only.len - (int)n * p.segment), 0,
-                          (n == 0 ? kBegins : 0) | (n == full ? kEnds : 0) | (full > 0 ? kCut : 0) | slot);
+            s = make_int4(only.first + n * p.segment, min(p.segment, only.len - (int)n * p.segment), slot,
+                          (n == 0 ? kBegins : 0) | (n == full ? kEnds : 0) | (full > 0 ? kCut : 0) | (slot < 0 ? kNoSlot : 0));
         } else {
             s = (OUTPUT ? p.outputs : p.inner)[n];
         }
@@ -64,12 +65,12 @@ __device__ __forceinline__ const float *state_before(const ChunkParams &p, const
     const int64_t at = entry_of(p, s);
     if (!(s.w & kBegins)) return p.states + (at - a.H) * kState;
     if (!a.initial_state) return nullptr;
-    return s.w & kCut ? p.first + at * kState : a.initial_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState;
+    return s.w & kCut ? p.first + at * kState : a.initial_state + ((int64_t)s.z * a.H + head_of(s)) * kState;
 }
 // Where the state behind a segment goes: nullptr if nowhere.
 __device__ __forceinline__ float *state_after(const ChunkParams &p, const Item &s) {
     const LinearChunkArgs &a = p.a;
-    return (s.w & kEnds) && a.final_state ? a.final_state + (slot_of(a, s.z) * a.H + head_of(s)) * (int64_t)kState : nullptr;
+    return (s.w & kEnds) && a.final_state ? a.final_state + ((int64_t)s.z * a.H + head_of(s)) * kState : nullptr;
 }
 
 size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int64_t segment);
