@@ -8,67 +8,82 @@ namespace {
 
 // The segments: a list of all for the outputs, sorted by length (into kBuckets classes), and one of those that have a
 // successor.  Their order in a class is left to chance; what is computed does not depend on it.  (Sequences that
-// overlap, as no well-formed offsets do, may be more than the lists hold; what is past their ends is left out.)
+// overlap, as no well-formed offsets do, may be more than the lists hold; what is past their ends is left out.
+// 65535 sequences of at most `entries` such segments each, some hundreds, are below 2^31.)
+// Lanes whose sequences are of one class share an addition: on their own, 4096 sequences of one length took 283 us.
 constexpr int kIndexThreads = 1024, kBuckets = 64;
-typedef unsigned long long Count;
 __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const ChunkParams p) {
-    __shared__ Count place[kBuckets], inner, cuts;
+    __shared__ int place[kBuckets], inner, cuts;
     const LinearChunkArgs &a = p.a;
-    const int tid = threadIdx.x, segment = p.segment;
-    const Count most = p.entries + a.n_seqs, most_inner = p.entries;
-    for (int i = tid; i < kBuckets; i += blockDim.x) place[i] = 0;
+    const int tid = threadIdx.x, lane = tid & 31, segment = p.segment, threads = blockDim.x;
+    const int most = p.entries + a.n_seqs, most_inner = p.entries;
+    for (int i = tid; i < kBuckets; i += threads) place[i] = 0;
     if (tid == 0) inner = cuts = 0;
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
     const float scale = (kBuckets - 1) / (float)segment;
-    auto bucket = [&](int rows) { return max(0, kBuckets - 1 - (int)(rows * scale)); };
-    const int threads = blockDim.x;
+    // f(first token, segments before the last one, tokens of that, slot; its class, -1: no sequence; the lanes of this class), by whole
+    // warps, offsets and slots of four sequences a thread requested together
+    auto for_sequences = [&](auto f) {
+        constexpr int kAhead = 4;
 #pragma unroll 1
-    for (int n = tid; n < a.n_seqs; n += threads) {
-        const Span span = span_of(a, n);
-        if (span.len < 0) continue;
-        const int full = span.len > 0 ? (span.len - 1) / segment : 0;  // segments before the last one
-        if (full > 0) atomicAdd(&place[0], (Count)full);
-        atomicAdd(&place[bucket(span.len - full * segment)], (Count)1);
-    }
+        for (int n0 = tid - lane; n0 < a.n_seqs; n0 += kAhead * threads) {
+            Span span[kAhead];
+            int slot[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int n = n0 + j * threads + lane;
+                span[j] = n < a.n_seqs ? span_of(a, n) : Span{0, -1};
+                slot[j] = n < a.n_seqs ? (int)slot_of(a, n) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int len = span[j].len, full = len > 0 ? (len - 1) / segment : 0, rows = len - full * segment;
+                const int bucket = len < 0 ? -1 : max(0, kBuckets - 1 - (int)(rows * scale));
+                f(span[j].first, full, rows, slot[j], bucket, __match_any_sync(0xffffffffu, bucket));
+            }
+        }
+    };
+    for_sequences([&](int, int full, int, int, int bucket, uint32_t same) {
+        if (full > 0) atomicAdd(&place[0], full);
+        if (bucket >= 0 && lane == __ffs(same) - 1) atomicAdd(&place[bucket], __popc(same));
+    });
     __syncthreads();
     if (tid < 32) {
-        const Count x = place[2 * tid], own = x + place[2 * tid + 1];
-        Count upto = own;
+        const int x = place[2 * tid], own = x + place[2 * tid + 1];
+        int upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const Count y = __shfl_up_sync(0xffffffffu, upto, o);
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
             if (tid >= o) upto += y;
         }
         place[2 * tid] = upto - own;
         place[2 * tid + 1] = upto - own + x;
-        if (tid == 31) p.counts[0] = (int)min(upto, most);
+        if (tid == 31) p.counts[0] = min(upto, most);
     }
     __syncthreads();
-#pragma unroll 1
-    for (int n = tid; n < a.n_seqs; n += threads) {
-        const Span span = span_of(a, n);
-        if (span.len < 0) continue;
-        const int full = span.len > 0 ? (span.len - 1) / segment : 0, at_slot = (int)slot_of(a, n), slot = at_slot < 0 ? kNoSlot : 0;
-        const int cut = full > 0 ? kCut : 0;
+    for_sequences([&](int first, int full, int rows, int at_slot, int bucket, uint32_t same) {
+        const int slot = at_slot < 0 ? kNoSlot : 0, cut = full > 0 ? kCut : 0;
         if (full > 0) {
-            Count at = atomicAdd(&place[0], (Count)full), in = slot ? most_inner : atomicAdd(&inner, (Count)full);
-            const Count c = slot ? most_inner : atomicAdd(&cuts, (Count)1);
-            if (c < most_inner) p.cuts[c] = make_int4(span.first, full, at_slot, 0);
+            int at = atomicAdd(&place[0], full), in = slot ? most_inner : atomicAdd(&inner, full);
+            const int c = slot ? most_inner : atomicAdd(&cuts, 1);
+            if (c < most_inner) p.cuts[c] = make_int4(first, full, at_slot, 0);
 #pragma unroll 1
             for (int l = 0; l < full; ++l, ++at, ++in) {
-                const Item s = make_int4(span.first + l * segment, segment, at_slot, (l == 0 ? kBegins : 0) | cut | slot);
+                const Item s = make_int4(first + l * segment, segment, at_slot, (l == 0 ? kBegins : 0) | cut | slot);
                 if (at < most) p.outputs[at] = s;
                 if (in < most_inner) p.inner[in] = s;
             }
         }
-        const int rows = span.len - full * segment;
-        const Count at = atomicAdd(&place[bucket(rows)], (Count)1);
-        if (at < most) p.outputs[at] = make_int4(span.first + full * segment, rows, at_slot, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
-    }
+        const int leader = __ffs(same) - 1;
+        int at = bucket >= 0 && lane == leader ? atomicAdd(&place[bucket], __popc(same)) : 0;
+        at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1));
+        if (bucket >= 0 && at < most)
+            p.outputs[at] = make_int4(first + full * segment, rows, at_slot, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
+    });
     __syncthreads();
-    if (tid == 0) p.counts[1] = (int)min(inner, most_inner), p.counts[2] = (int)min(cuts, most_inner);
+    if (tid == 0) p.counts[1] = min(inner, most_inner), p.counts[2] = min(cuts, most_inner);
 }
 
 // The states in front of the segments of each sequence that is cut, in place of the segments' own: entry l gets
