@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 
 // Tokens of a segment: so many that the segments of all heads are about as many as SMs.  A cut costs two launches
 // and some 10 us, as much as three chunks: five chunks are left whole, no segment has fewer than two of them, or, where
-// there are several sequences, four.  (5 sequences of 17 to 200 tokens, 8 heads: 22.8 us of the device cut by the chunk, @ whole.)
+// there are several sequences, four.  (5 sequences of 17 to 200 tokens, 8 heads: 22.8 us of the device cut by the chunk, 15.7 whole.)
 inline int64_t segment_of(int64_t total_tokens, int n_seqs, int H) {
     const int64_t chunks = (total_tokens + kTok - 1) / kTok, each = std::max<int64_t>(1, sm_count() / H);
     if (chunks <= 5) return kTok * std::max<int64_t>(1, chunks);
