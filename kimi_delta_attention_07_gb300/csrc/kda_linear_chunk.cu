@@ -10,10 +10,10 @@
 // in fp32 while |G| < 8 (2^-22 in e^{G_t - G_j}), else token by token.  Sequences are cut into
 // segments (kda_linear_segments.cuh).
 //
-// Two sequences of 1001 and 500 tokens, 16 heads: 94 us; 135 with two rows a thread, 196 with
+// Two sequences of 1001 and 500 tokens, 16 heads: 91 us; 135 with two rows a thread, 196 with
 // a product for each decay and one row a thread, 252 uncut and with an exchange a token.  What bounds it: 12 warps
 // a SM (their registers hold the state), whose fma and shared-memory pipes are each half busy (4096 tokens of
-// 32 heads: 394 us, of which 174 are its fmas at the pipe's rate).
+// 32 heads: 375 us, of which 174 are its fmas at the pipe's rate).
 //
 // A decay near one is the sum of two floats: as one, its rounding error would come back every
 // time that it is applied (a fixed decay of 2^-8 a token: 1e-5 in the state).
@@ -46,7 +46,7 @@ __device__ __forceinline__ float2 decay_of(float g) {
 }
 
 // OUTPUT: o and final states, from the states in front of the segments; else a segment's own state.
-template <bool OUTPUT>
+template <bool OUTPUT, Source SOURCE>
 __global__ void __launch_bounds__(kThreads, 3) linear_chunk_f32_kernel(const ChunkParams p) {
     // (a row of 128 channels as 8 lanes of 16: channel 32 i + 4 l + j is lane l's)
     __shared__ __align__(16) float sq[OUTPUT ? 2 : 1][OUTPUT ? kBlock : 1][kHeadDim], sk[2][kBlock][kHeadDim], sv[2][kBlock][kRows];
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 3) linear_chunk_f32_kernel(const Chu
     griddep_launch_dependents();
     const LinearChunkArgs &a = p.a;
     const int row0 = blockIdx.y * kRows, tid = threadIdx.x, row = tid / kLanes * kOwn, l = tid % kLanes;
-    for_segments<OUTPUT>(p, blockIdx.x, gridDim.x, [&](const Item &seg) {
+    for_segments<OUTPUT, SOURCE>(p, blockIdx.x, gridDim.x, [&](const Item &seg) {
         const int h = head_of(seg), len = seg.y;
         const int64_t first = seg.x;
         float *o = (float *)a.o + h * kHeadDim + row0;
@@ -229,15 +229,20 @@ size_t linear_chunk_f32_workspace_bytes(int64_t total_tokens, int n_seqs, int H)
 
 cudaError_t launch_linear_chunk_f32(const LinearChunkArgs &a, cudaStream_t stream) {
     const ChunkParams p = plan_segments(a, segment_of(a.total_tokens, a.H));
+    const Source source = source_of(p);
     auto launch = [&](auto kernel, int64_t items) {
         return launch_dependent(kernel, dim3((unsigned)items, kHeadDim / kRows), dim3(kThreads), 0, stream, p);
     };
     cudaError_t e = launch_segment_lists(p, stream);
     if (e == cudaSuccess && p.entries > 0) {
-        e = launch(linear_chunk_f32_kernel<false>, (int64_t)p.entries * a.H);
+        e = launch(source == kOne ? linear_chunk_f32_kernel<false, kOne> : linear_chunk_f32_kernel<false, kListed>, (int64_t)p.entries * a.H);
         if (e == cudaSuccess) e = launch_segment_join(p, stream);
     }
-    if (e == cudaSuccess) e = launch(linear_chunk_f32_kernel<true>, ((int64_t)p.entries + a.n_seqs) * a.H);
+    if (e == cudaSuccess)
+        e = launch(source == kOne     ? linear_chunk_f32_kernel<true, kOne>
+                   : source == kWhole ? linear_chunk_f32_kernel<true, kWhole>
+                                      : linear_chunk_f32_kernel<true, kListed>,
+                   ((int64_t)p.entries + a.n_seqs) * a.H);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

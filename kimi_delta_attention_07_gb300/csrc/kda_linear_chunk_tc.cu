@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
     return r;
 }
 // OUTPUT: o and final states, from the states in front of the segments; else a segment's own state.
-template <bool OUTPUT>
+template <bool OUTPUT, Source SOURCE>
 __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
     auto gave_up = [&] { return __any_sync(0xffffffffu, dead); };
     // f(segment and head, chunks, terms) for each of this CTA's, in the same order by every warp
     auto for_items = [&](auto f) {
-        for_segments<OUTPUT>(p, blockIdx.x, gridDim.x, [&](const Item &s) {
+        for_segments<OUTPUT, SOURCE>(p, blockIdx.x, gridDim.x, [&](const Item &s) {
             // a segment whose states serve o alone does without the third term
             f(s, s.w & kNoSlot ? 0 : (s.y + kTok - 1) / kTok, OUTPUT && (s.w & (kCut | kEnds)) == kCut ? 2 : 3);
         });
@@ -721,6 +721,7 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
         !encode_heads64(&map_o, T ? a.o : none, kHeadDim, a.H, rows, (int64_t)a.H * kHeadDim, kTok))
         return cudaErrorUnknown;
     const ChunkParams p = plan_segments(a, segment_of(T, a.n_seqs, a.H));
+    const Source source = source_of(p);
     auto launch = [&](auto kernel, int threads, int64_t items) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         return e != cudaSuccess ? e
@@ -729,10 +730,14 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
     };
     cudaError_t e = launch_segment_lists(p, stream);
     if (e == cudaSuccess && p.entries > 0) {
-        e = launch(linear_chunk_kernel<false>, 640, (int64_t)p.entries * a.H);
+        e = launch(source == kOne ? linear_chunk_kernel<false, kOne> : linear_chunk_kernel<false, kListed>, 640, (int64_t)p.entries * a.H);
         if (e == cudaSuccess) e = launch_segment_join(p, stream);
     }
-    if (e == cudaSuccess) e = launch(linear_chunk_kernel<true>, 896, ((int64_t)p.entries + a.n_seqs) * a.H);
+    if (e == cudaSuccess)
+        e = launch(source == kOne     ? linear_chunk_kernel<true, kOne>
+                   : source == kWhole ? linear_chunk_kernel<true, kWhole>
+                                      : linear_chunk_kernel<true, kListed>,
+                   896, ((int64_t)p.entries + a.n_seqs) * a.H);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

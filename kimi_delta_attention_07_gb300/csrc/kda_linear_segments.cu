@@ -141,7 +141,7 @@ struct Layout {
 };
 inline Layout layout(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
     const int64_t entries = entries_of(total_tokens, segment);
-    const bool lists = n_seqs > 1;
+    const bool lists = n_seqs > 1 && entries > 0;
     Layout l;
     l.outputs = lists ? 256 : 0;
     l.inner = l.outputs + (lists ? align_up((size_t)(entries + n_seqs) * sizeof(Item), 256) : 0);
@@ -176,7 +176,7 @@ ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment) {
 }
 
 cudaError_t launch_segment_lists(const ChunkParams &p, cudaStream_t stream) {
-    if (p.a.n_seqs == 1) return cudaSuccess;
+    if (source_of(p) != kListed) return cudaSuccess;
     return launch_dependent(segment_lists_kernel, dim3(1), dim3(std::min(kIndexThreads, (p.a.n_seqs + 31) / 32 * 32)), 0, stream, p);
 }
 
