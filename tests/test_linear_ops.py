@@ -581,3 +581,149 @@ def test_prompt_then_steps_follow_one_longer_prompt(kda):
             # two bf16 products and roundings against one: a few half steps of an output row
             off = (got[i].double() - whole[i][n + s].double()).norm() / whole[i][n + s].double().norm()
             assert off < 2.0 ** -6, (i, s, float(off))
+
+
+# ---- calls that share something, sizes at the ends ----------------------------------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_chunk_decay_not_finite_leaves_the_rows_before_it(kda, dtype, value):
+    q, k, v, g = (x.clone() for x in layer_inputs(300, 2, 1, dtype, 0))
+    at = 170
+    g[at, 1] = value
+    o, s = kda.kda_linear_chunk_fwd(q, k, v, g)
+    ref, inner, outer, S, A = layer_ref(q[:at], k[:at], v[:at], g[:at], torch.zeros_like(s[0]), 128 ** -0.5)
+    within(o[:at], ref, o_bound(ref, inner, outer, at, dtype), "o before it")
+    assert not o[at:, 1].isfinite().any() and not s[0, 1].isfinite().any()
+    assert o[:, 0].isfinite().all() and s[0, 0].isfinite().all()
+
+
+def test_two_graphs_share_a_workspace(kda):
+    cu = i32([0, 1900, 2500])
+    ws = torch.empty(max(256, kda.kda_linear_chunk_workspace_bytes(2500, 2, 2)), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for seed in (0, 40):
+        x = layer_inputs(2500, 2, 2, torch.bfloat16, seed)
+        ref = kda.kda_linear_chunk_fwd(*x, cu_seqlens=cu)
+        out = tuple(torch.empty_like(t) for t in ref)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kda.kda_linear_chunk_fwd(*x, cu_seqlens=cu, o=out[0], final_state=out[1], workspace=ws)
+        graphs.append((graph, x, ref, out))
+    for _ in range(4):
+        for graph, _, _, out in graphs:
+            out[0].zero_(), out[1].zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, _, ref, out in graphs:
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+
+
+def test_steps_and_rope_on_two_streams_at_once(kda):
+    freq = (100.0 ** (-torch.arange(16) / 16)).cuda()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+
+    def run(seed, stream):
+        q, k, v, g = layer_inputs(40, 4, 2, torch.bfloat16, seed)
+        pool = normal((40, 4, 128, 128), seed + 3, torch.float32)
+        pos = torch.arange(40, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        yield
+        for _ in range(20):
+            a, b = kda.kda_head_norm_rope(q, k, positions=pos, inv_freq=freq, stream=stream)
+            o = kda.kda_linear_step(a, b, v, g, pool, stream=stream)
+            yield
+        torch.cuda.synchronize()
+        yield o, pool
+
+    alone = [list(run(seed, None))[-1] for seed in (0, 60)]
+    together = list(zip(*(run(seed, streams[i]) for i, seed in enumerate((0, 60)))))[-1]
+    for x, y in zip(alone, together):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+def test_chunk_thousands_of_sequences_and_a_long_one(kda):
+    lens = [3] * 2500 + [1500, 0] + [3, 7] * 1300
+    N, T, H = len(lens), sum(lens), 2
+    q, k, v, g = layer_inputs(T, H, 2, torch.bfloat16, 0)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    pool = normal((N + 1, H, 128, 128), 3, torch.float32)
+    start = pool.clone()
+    index = (torch.arange(N - 1, -1, -1) + 1).to(torch.int32)
+    gone = [0, 2400, 4000]
+    index[gone] = torch.tensor([-1, N + 1, -5], dtype=torch.int32)
+    o = torch.full((T, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=cu, initial_state=pool, final_state=pool, state_indices=index.cuda(), o=o)
+    for n in (1, 2399, 2499, 2500, 2501, 2502, 3999, N - 1):
+        a, b, slot = int(cu[n]), int(cu[n + 1]), int(index[n])
+        if a == b:
+            assert torch.equal(pool[slot], start[slot])
+            continue
+        ref, inner, outer, S, A = layer_ref(q[a:b], k[a:b], v[a:b], g[a:b], start[slot], 128 ** -0.5)
+        within(o[a:b], ref, o_bound(ref, inner, outer, b - a, torch.bfloat16), f"o of sequence {n}")
+        within(pool[slot], S, s_bound(A, b - a, torch.bfloat16), f"state of sequence {n}")
+    rows = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for n in gone:
+        rows[int(cu[n]): int(cu[n + 1])] = True
+    assert o[rows].isnan().all() and o[~rows].isfinite().all() and not (o[~rows] == 7.0).all(-1).any()
+    for slot in [0] + [N - n for n in gone]:
+        assert torch.equal(pool[slot], start[slot])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_chunk_more_heads_than_sms_and_no_token(kda, dtype):
+    check_chunk(kda, [130, 0, 10], 170, 1, dtype)
+    check_chunk(kda, [0, 0, 0], 2, 2, dtype)
+    check_chunk(kda, [0, 0, 0], 2, 2, dtype, carry=False)
+    check_chunk(kda, [20, 0, 30], 3, 3, dtype, in_place=True)
+
+
+def test_multi_step_keeps_the_last_state_of_a_slot_that_it_repeats(kda):
+    N, S, H = 3, 4, 2
+    q, k, v, g = layer_inputs(N * S, H, H, torch.bfloat16, 0)
+    pool = normal((N, H, 128, 128), 3, torch.float32)
+    one = pool.clone()
+    shape = lambda x: x.unflatten(0, (N, S))  # noqa: E731
+    o = kda.kda_linear_multi_step(shape(q), shape(k), shape(v), shape(g), pool, i32([[n] * S for n in range(N)]))
+    for t in range(S):
+        got = kda.kda_linear_step(*(shape(x)[:, t].contiguous() for x in (q, k, v, g)), one)
+        assert torch.equal(o[:, t], got)
+    assert torch.equal(pool, one)
+
+
+def test_offsets_behind_32_bits(kda):
+    """Slots and tokens whose elements lie behind 2^31 of their buffers."""
+    pool = torch.empty((140000, 1, 128, 128), device="cuda")
+    slot, T, stride = 139990, 18, 1 << 27
+    x = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda").view(T, 1, stride)
+    q, k, v = (x[:, :, 128 * i: 128 * i + 128] for i in range(3))
+    for i, t in enumerate((q, k, v)):
+        t.copy_(normal((T, 1, 128), i))
+    g = decays(T, 1, 5, "token")
+    s0 = normal((1, 128, 128), 6, torch.float32)
+    ref, inner, outer, S, A = layer_ref(q, k, v, g, s0, 128 ** -0.5)
+    pool[slot] = s0
+    o, _ = kda.kda_linear_chunk_fwd(q, k, v, g, initial_state=pool, final_state=pool, state_indices=i32([slot]))
+    within(o, ref, o_bound(ref, inner, outer, T, torch.bfloat16), "o")
+    within(pool[slot], S, s_bound(A, T, torch.bfloat16), "state")
+    pool[slot] = s0
+    for t in range(T):
+        one = kda.kda_linear_step(q[t:], k[t:], v[t:], g[t:], pool, state_indices=i32([slot] + [-1] * (T - t - 1)))
+        within(one[0], ref[t], 2.0 ** -8 * ref[t].abs() * (1 + 2.0 ** -8) + (t + 1) * 2.0 ** -19 * outer[t] + 1e-37, f"o of token {t}")
+    within(pool[slot], S, T * 2.0 ** -21 * A, "state of the steps")
+    freq, pos = (10000.0 ** (-torch.arange(64) / 64)).cuda(), torch.arange(T, dtype=torch.int32, device="cuda")
+    a, _ = kda.kda_head_norm_rope(q, positions=pos, inv_freq=freq)
+    b, _ = kda.kda_head_norm_rope(q.contiguous(), positions=pos, inv_freq=freq)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_chunk_decays_above_zero(kda, dtype):
+    # (their sum over 128 tokens stays below 20)
+    q, k, v, _ = layer_inputs(300, 2, 2, dtype, 0)
+    g = torch.rand((300, 2), generator=gen(9), device="cuda") * 0.25 - 0.1
+    o, s = kda.kda_linear_chunk_fwd(q, k, v, g)
+    ref, inner, outer, S, A = layer_ref(q, k, v, g, torch.zeros_like(s[0]), 128 ** -0.5)
+    within(o, ref, o_bound(ref, inner, outer, 300, dtype), "o")
+    within(s[0], S, s_bound(A, 300, dtype), "state")
