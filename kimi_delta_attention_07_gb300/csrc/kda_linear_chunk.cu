@@ -228,7 +228,7 @@ size_t linear_chunk_f32_workspace_bytes(int64_t total_tokens, int n_seqs, int H)
 }
 
 cudaError_t launch_linear_chunk_f32(const LinearChunkArgs &a, cudaStream_t stream) {
-    const ChunkParams p = plan_segments(a, segment_of(a.total_tokens, a.H));
+    const ChunkParams p = plan_segments(a, segment_of(a.total_tokens, a.H), 3 * sm_count() / (kHeadDim / kRows), 24);
     const Source source = source_of(p);
     auto launch = [&](auto kernel, int64_t items) {
         return launch_dependent(kernel, dim3((unsigned)items, kHeadDim / kRows), dim3(kThreads), 0, stream, p);

@@ -720,7 +720,7 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
         !encode_heads64(&map_v, T ? a.v : none, kHeadDim, a.H, rows, a.v_stride, kTok) ||
         !encode_heads64(&map_o, T ? a.o : none, kHeadDim, a.H, rows, (int64_t)a.H * kHeadDim, kTok))
         return cudaErrorUnknown;
-    const ChunkParams p = plan_segments(a, segment_of(T, a.n_seqs, a.H));
+    const ChunkParams p = plan_segments(a, segment_of(T, a.n_seqs, a.H), sm_count(), 3 * kTok);
     const Source source = source_of(p);
     auto launch = [&](auto kernel, int threads, int64_t items) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);

@@ -15,37 +15,63 @@ constexpr int kIndexThreads = 1024, kBuckets = 64;
 __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const ChunkParams p) {
     __shared__ int place[kBuckets], inner, cuts;
     const LinearChunkArgs &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, segment = p.segment, threads = blockDim.x;
+    __shared__ int longest, followed;
+    __shared__ uint32_t sum;
+    const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
     const int most = p.entries + a.n_seqs, most_inner = p.entries;
     for (int i = tid; i < kBuckets; i += threads) place[i] = 0;
-    if (tid == 0) inner = cuts = 0;
+    if (tid == 0) inner = cuts = longest = followed = sum = 0;
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
-    const float scale = (kBuckets - 1) / (float)segment;
-    // f(first token, segments before the last one, tokens of that, slot; its class, -1: no sequence; the lanes of this class), by whole
-    // warps, offsets and slots of four sequences a thread requested together
+    // f(first token, tokens (-1: no sequence), slot), by whole warps, offsets and slots of four sequences a thread
+    // requested together (once, if there are no more)
+    constexpr int kAhead = 4;
+    Span span[kAhead];
+    int slots[kAhead], held = -1;
     auto for_sequences = [&](auto f) {
-        constexpr int kAhead = 4;
 #pragma unroll 1
         for (int n0 = tid - lane; n0 < a.n_seqs; n0 += kAhead * threads) {
-            Span span[kAhead];
-            int slot[kAhead];
+            if (n0 != held) {
+                held = n0;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int n = n0 + j * threads + lane;
-                span[j] = n < a.n_seqs ? span_of(a, n) : Span{0, -1};
-                slot[j] = n < a.n_seqs ? (int)slot_of(a, n) : 0;
+                for (int j = 0; j < kAhead; ++j) {
+                    const int n = n0 + j * threads + lane;
+                    span[j] = n < a.n_seqs ? span_of(a, n) : Span{0, -1};
+                    slots[j] = n < a.n_seqs ? (int)slot_of(a, n) : 0;
+                }
             }
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int len = span[j].len, full = len > 0 ? (len - 1) / segment : 0, rows = len - full * segment;
-                const int bucket = len < 0 ? -1 : max(0, kBuckets - 1 - (int)(rows * scale));
-                f(span[j].first, full, rows, slot[j], bucket, __match_any_sync(0xffffffffu, bucket));
-            }
+            for (int j = 0; j < kAhead; ++j)
+                if (n0 + j * threads < a.n_seqs) f(span[j].first, span[j].len, slots[j]);
         }
     };
-    for_sequences([&](int, int full, int, int, int bucket, uint32_t same) {
+    // Cut, or not: by the time of the longest part, or of all (and a quarter of that for the uneven end) where that is
+    // more.  A segment's own state takes half the time of its outputs.  (16 sequences of 4000 tokens, 8 heads: 142 us
+    // uncut, 200 cut; one of 60000 and 15 of 300: cut, 192.  Longer segments than p.segment never come out
+    // more than a little better than these two.)
+    int my_longest = 0, my_followed = 0;
+    uint32_t my_sum = 0;
+    for_sequences([&](int, int len, int) {
+        if (len <= 0) return;
+        my_longest = max(my_longest, len), my_sum += len;
+        my_followed += (uint32_t)(len - 1) / (uint32_t)p.segment;
+    });
+    my_longest = __reduce_max_sync(0xffffffffu, my_longest), my_sum = __reduce_add_sync(0xffffffffu, my_sum);
+    my_followed = __reduce_add_sync(0xffffffffu, my_followed);
+    if (lane == 0) atomicMax(&longest, my_longest), atomicAdd(&sum, my_sum), atomicAdd(&followed, my_followed);
+    __syncthreads();
+    const float each = a.H / (float)p.parallel, whole = (float)sum * each;
+    const float uncut = fmaxf(longest, whole + 0.25f * longest);
+    const float cut_up = fmaxf(p.segment, whole + 0.25f * p.segment) + p.fixed + 0.5f * fmaxf(p.segment, (float)followed * p.segment * each);
+    const int segment = followed > 0 && cut_up < uncut ? p.segment : max(longest, 1);
+    const float scale = (kBuckets - 1) / (float)segment;
+    // the segments before a sequence's last one, the tokens of that, and its class
+    auto full_of = [&](int len) { return len > 0 ? (int)((uint32_t)(len - 1) / (uint32_t)segment) : 0; };
+    auto bucket_of = [&](int len, int rows) { return len < 0 ? -1 : max(0, kBuckets - 1 - (int)(rows * scale)); };
+    for_sequences([&](int, int len, int) {
+        const int full = full_of(len), bucket = bucket_of(len, len - full * segment);
+        const uint32_t same = __match_any_sync(0xffffffffu, bucket);
         if (full > 0) atomicAdd(&place[0], full);
         if (bucket >= 0 && lane == __ffs(same) - 1) atomicAdd(&place[bucket], __popc(same));
     });
@@ -63,15 +89,17 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
         if (tid == 31) p.counts[0] = min(upto, most);
     }
     __syncthreads();
-    for_sequences([&](int first, int full, int rows, int at_slot, int bucket, uint32_t same) {
+    for_sequences([&](int first, int len, int at_slot) {
+        const int full = full_of(len), rows = len - full * segment, bucket = bucket_of(len, rows), entry = (uint32_t)first / (uint32_t)segment;
+        const uint32_t same = __match_any_sync(0xffffffffu, bucket);
         const int slot = at_slot < 0 ? kNoSlot : 0, cut = full > 0 ? kCut : 0;
         if (full > 0) {
             int at = atomicAdd(&place[0], full), in = slot ? most_inner : atomicAdd(&inner, full);
             const int c = slot ? most_inner : atomicAdd(&cuts, 1);
-            if (c < most_inner) p.cuts[c] = make_int4(first, full, at_slot, 0);
+            if (c < most_inner) p.cuts[c] = make_int4(entry, full, at_slot, 0);
 #pragma unroll 1
             for (int l = 0; l < full; ++l, ++at, ++in) {
-                const Item s = make_int4(first + l * segment, segment, at_slot, (l == 0 ? kBegins : 0) | cut | slot);
+                const Item s = make_int4(first + l * segment, segment, at_slot, (l == 0 ? kBegins : 0) | cut | slot | (entry + l) << kEntry);
                 if (at < most) p.outputs[at] = s;
                 if (in < most_inner) p.inner[in] = s;
             }
@@ -80,7 +108,7 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
         int at = bucket >= 0 && lane == leader ? atomicAdd(&place[bucket], __popc(same)) : 0;
         at = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1));
         if (bucket >= 0 && at < most)
-            p.outputs[at] = make_int4(first + full * segment, rows, at_slot, (full == 0 ? kBegins : 0) | kEnds | cut | slot);
+            p.outputs[at] = make_int4(first + full * segment, rows, at_slot, (full == 0 ? kBegins : 0) | kEnds | cut | slot | (entry + full) << kEntry);
     });
     __syncthreads();
     if (tid == 0) p.counts[1] = min(inner, most_inner), p.counts[2] = min(cuts, most_inner);
@@ -100,12 +128,12 @@ __global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkP
         const Span span = span_of(a, 0);
         const int64_t slot = slot_of(a, 0);
         if (span.len <= p.segment || slot < 0) return;
-        only = make_int4(span.first, (span.len - 1) / p.segment, (int)slot, 0);
+        only = make_int4(0, (span.len - 1) / p.segment, (int)slot, 0);
     }
     const int listed = a.n_seqs == 1 ? 1 : p.counts[2];
     for (int i = blockIdx.x; i < listed; i += gridDim.x) {
         const Item s = a.n_seqs == 1 ? only : p.cuts[i];
-        const int count = s.y, entry = s.x / p.segment;
+        const int count = s.y, entry = s.x;
         const int64_t at = 4 * ((int64_t)blockIdx.z * kJoinThreads + threadIdx.x);
         const int64_t step = (int64_t)a.H * kState, own = ((int64_t)entry * a.H + h) * kState + at;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -133,7 +161,8 @@ __global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkP
     }
 }
 
-// A segment's entry is floor(first token / segment): distinct for those that have a successor, whatever the lengths.
+// A segment's entry is floor(sequence's first token / segment) and its place in the sequence: distinct for those that have a
+// successor, whatever the lengths.
 inline int64_t entries_of(int64_t total_tokens, int64_t segment) { return total_tokens > 0 ? (total_tokens - 1) / segment : 0; }
 
 struct Layout {
@@ -158,13 +187,15 @@ size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int64_t
     return layout(total_tokens, n_seqs, H, segment).total;
 }
 
-ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment) {
+ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment, int parallel, int fixed) {
     const Layout l = layout(a.total_tokens, a.n_seqs, a.H, segment);
     uint8_t *ws = (uint8_t *)a.workspace;
     ChunkParams p{a};
     p.segment = (int)segment;
     p.entries = (int)entries_of(a.total_tokens, segment);
     p.joined = p.entries > 0;
+    p.parallel = parallel;
+    p.fixed = fixed;
     p.counts = (int *)ws;
     p.outputs = (Item *)(ws + l.outputs);
     p.inner = (Item *)(ws + l.inner);

@@ -12,18 +12,22 @@ constexpr int kState = kHeadDim * kHeadDim;
 // A segment to work on, in four registers: what warps look at in every chunk must not be in local memory,
 // for which the L1 cache has no room beside this shared memory.
 enum : int { kBegins = 1 << 16, kEnds = 1 << 17, kCut = 1 << 18, kNoSlot = 1 << 19 };
-typedef int4 Item;  // first token, tokens, slot of the states, flags (and in the low 16 bits, once it is picked, the head)
+constexpr int kEntry = 20;
+// first token, tokens, slot of the states, flags: in the low 16 bits, once it is picked, the head, in the upper 12 its entry (some hundreds at most)
+typedef int4 Item;
 __device__ __forceinline__ int head_of(const Item &s) { return s.w & 0xffff; }
 
 struct ChunkParams {
     LinearChunkArgs a;
-    int segment;    // tokens
-    int entries;    // segments whose state the workspace holds, at most; floor(first token / segment) is a segment's
+    int segment;    // tokens; several sequences may be left uncut
+    int entries;    // segments whose state the workspace holds, at most
+    int parallel;   // segments and heads that are worked on at the same time
+    int fixed;      // tokens of one that cost as much as the two launches of a cut
     bool joined;    // the kernel follows the others: its inputs are there before it begins
     int *counts;    // length of each list (no lists of a single sequence, or where no sequence is long enough to be cut)
     Item *outputs;  // all segments, the longest first
     Item *inner;    // [entries]: those that others follow in their sequence
-    Item *cuts;     // [entries]: the sequences that are cut: first token, such segments, slot
+    Item *cuts;     // [entries]: the sequences that are cut: first entry, such segments, slot
     float *states;  // [entries][H][V][K]
     float *first;   // [entries][H][V][K]: copies of initial states (those that a later CTA may overwrite)
     float *decay;   // [entries][H]
@@ -53,7 +57,7 @@ __device__ __forceinline__ void for_segments(const ChunkParams &p, uint32_t cta,
             s = (OUTPUT ? p.outputs : p.inner)[n];
         } else if constexpr (SOURCE == kOne) {
             s = make_int4(only.first + n * p.segment, min(p.segment, only.len - (int)n * p.segment), slot,
-                          (n == 0 ? kBegins : 0) | (n == full ? kEnds : 0) | (full > 0 ? kCut : 0) | (slot < 0 ? kNoSlot : 0));
+                          (n == 0 ? kBegins : 0) | (n == full ? kEnds : 0) | (full > 0 ? kCut : 0) | (slot < 0 ? kNoSlot : 0) | (n << kEntry));
         } else {
             const Span span = span_of(a, n);
             const int own = (int)slot_of(a, n);
@@ -66,7 +70,7 @@ __device__ __forceinline__ void for_segments(const ChunkParams &p, uint32_t cta,
 }
 // A segment's (and head's) place in states, first and decay.
 __device__ __forceinline__ int64_t entry_of(const ChunkParams &p, const Item &s) {
-    return (int64_t)((uint32_t)s.x / (uint32_t)p.segment) * p.a.H + head_of(s);
+    return (int64_t)((uint32_t)s.w >> kEntry) * p.a.H + head_of(s);
 }
 // The state in front of a segment: nullptr for zeros.
 __device__ __forceinline__ const float *state_before(const ChunkParams &p, const Item &s) {
@@ -83,7 +87,7 @@ __device__ __forceinline__ float *state_after(const ChunkParams &p, const Item &
 }
 
 size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int64_t segment);
-ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment);
+ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment, int parallel, int fixed);
 cudaError_t launch_segment_lists(const ChunkParams &p, cudaStream_t stream);
 cudaError_t launch_segment_join(const ChunkParams &p, cudaStream_t stream);
 

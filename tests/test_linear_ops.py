@@ -599,6 +599,15 @@ def test_chunk_decay_not_finite_leaves_the_rows_before_it(kda, dtype, value):
     assert o[:, 0].isfinite().all() and s[0, 0].isfinite().all()
 
 
+@pytest.mark.parametrize("lens,H", [([700] * 14, 8), ([1000, 1], 2), ([900, 0, 650], 20)])
+def test_chunk_sequences_that_could_be_cut_and_are_not(kda, lens, H):
+    check_chunk(kda, lens, H, H, in_place=True)
+
+
+def test_chunk_fp32_sequences_that_are_not_cut(kda):
+    check_chunk(kda, [200, 30, 140, 0, 90] * 12, 16, 4, torch.float32)
+
+
 def test_two_graphs_share_a_workspace(kda):
     cu = i32([0, 1900, 2500])
     ws = torch.empty(max(256, kda.kda_linear_chunk_workspace_bytes(2500, 2, 2)), dtype=torch.uint8, device="cuda")
