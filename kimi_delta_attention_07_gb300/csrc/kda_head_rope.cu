@@ -9,7 +9,7 @@
 // heads while the first rows are on their way, and requests each thread's next row
 // before it works on the last one.  What then bounds it is instructions, some 200 a warp and rows of two
 // vectors a lane: fp32 in pairs, indices without a division, weights and angles in shared
-// memory in the order of the lanes (4096 tokens of 64 heads: 25.8 us, 5.2 TB/s; one token a CTA and
+// memory in the order of the lanes (4096 tokens of 64 heads: 25.4 us, 5.3 TB/s; one token a CTA and
 // scalar arithmetic, 38 us; a thread that keeps to a head, with its weights in registers, 27; two
 // rows ahead with 24 warps a SM, 30).
 //
@@ -213,11 +213,13 @@ template <typename T, int LANES>
 cudaError_t launch(const HeadRopeArgs &a, bool norm, bool interleaved, cudaStream_t stream) {
     constexpr int kGroups = kThreads / LANES;
     const int64_t heads = a.heads[0] + a.heads[1], T_ = a.n_tokens;
-    // A CTA's rows are eight times its groups, fewer where that leaves SMs idle: then tokens by themselves, and at last
-    // heads apart.
+    // A CTA's rows are eight times its groups (4096 tokens of 64 heads: 24.1 us of the device; four times 24.6, sixteen 27.6),
+    // fewer where that leaves SMs idle: four CTAs a SM (4096 of 9 heads of 256: 9.4 us; two 12.3), but a row for each group
+    // while every SM has a CTA (777 of 32 heads of 64: 3.3 us; 4.3 without), and at last heads apart
+    // (8 tokens of 40 heads: 2.2 us; 2.6 without).
     const int64_t token_bytes = std::max(1, a.rot_dim / 2 * (interleaved ? 16 : 8));
     int64_t tokens = std::min<int64_t>({std::max<int64_t>(1, 8 * kGroups / heads), kMaxTokens, std::max<int64_t>(1, kTableBytes / token_bytes),
-                                        std::max<int64_t>(1, T_ / (4 * sm_count()))});
+                                        std::max<int64_t>({1, T_ / (4 * sm_count()), std::min<int64_t>(kGroups / heads, T_ / sm_count())})});
     int64_t split = 1;
     while (heads / split > kGroups && (T_ + tokens - 1) / tokens * split < 2 * sm_count()) split *= 2;
     HeadRopeParams p{a, (int)tokens, (int)((heads + split - 1) / split)};

@@ -32,12 +32,15 @@
 // value that is not finite would reach rows before it as 0 times it: V is looked through,
 // such values become 0 and their channel NaN from their row on, in o and in S.
 //
-// What bounds a chunk: not its products (3072 clocks of the tensor core; taking them out changes nothing) but
-// the chain of instructions of a warp, each some seven clocks behind the last. So the work is spread over
-// as many warps as there are registers for.  With outputs, eight warps look through V and make Kt and
+// What bounds a chunk: not its products (3072 of its 7000 clocks; without them it takes a tenth less) but
+// the chain of instructions of a warp, each some seven clocks behind the last.  So the work is spread over
+// as many warps as there are registers for (five groups of four with 128 registers: 9300 clocks).  With outputs, eight warps look through V and make Kt and
 // run ahead, sixteen make P and hold the state, 32 value channels each, and take a chunk's outputs while the
 // next one's scores are computed; without outputs, sixteen warps make a quarter of Kt each and update a
 // quarter of the state while the next chunk's D runs.
+//
+// 131072 tokens of 8 heads: 316 us, of which the segments' states take 104 (4.9 TB/s), the join 6 and the
+// outputs 205 (5.2 TB/s); 4096 tokens of 32 heads: 66 us; 8 sequences of 333 to 4001 tokens, 32 heads, uncut: 140 us.
 //
 // Warps: 0 TMA, 1 MMA of X and O, 2 MMA of D, 3 decays, 4..11 check of V and Kt, 12..27 P, the state
 // and the outputs; without outputs 4..19 all of it.

@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
 // The states in front of the segments of each sequence that is cut, in place of the segments' own: entry l gets
 // that in front of segment l + 1.  A sequence's initial state is copied, because its last segment may
 // overwrite it while the first one still reads.
+// (131072 tokens of 8 heads, 18 segments: 6 us, from L2; eight segments requested ahead.)
 constexpr int kJoinThreads = 256, kJoinParts = kState / (4 * kJoinThreads);
 __global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkParams p) {
     griddep_wait();

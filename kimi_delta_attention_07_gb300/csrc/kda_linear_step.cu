@@ -7,6 +7,9 @@
 // the lanes together, by a reduce-scatter: RPW rows cost RPW shuffles where a
 // reduction of each would take five times as many.  Rows of a head are split over CTAs
 // where there are few heads.  With several tokens the rows stay in registers between them.
+//
+// 256 sequences of 32 heads: 156 us, 6.9 TB/s of states read and written; 64 sequences of 32 heads, 4 tokens each: 106 us,
+// 6.3 TB/s; 4 sequences of 8 heads: 1.9 us of the device.
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -120,7 +123,8 @@ void launch(const LinearStepArgs &a, cudaStream_t stream, cudaError_t *e) {
 template <typename T>
 cudaError_t launch(const LinearStepArgs &a, cudaStream_t stream) {
     cudaError_t e;
-    // a head's rows go to several CTAs until there are some eight a SM
+    // a head's rows go to several CTAs until there are some eight a SM (one sequence of 8 heads: 1.7 us of the device with 2 rows
+    // a warp, 3.0 with 16; 32 of 16 heads: 7.2 with 4, 8.1 with 16, 9.0 with 2; 256 of 32 heads: 154 with 16, 175 with 2)
     int64_t ctas = (int64_t)a.N * a.H;
     int rpw = 16;
     while (rpw > 2 && ctas < 8 * sm_count()) rpw /= 2, ctas *= 2;
