@@ -13,7 +13,10 @@
 // S = e^{G_127} S + D, which the tensor core could not scale.
 //
 // What is rounded: P and the copy of S that O is taken from, to bf16 (as o itself is, so that o's
-// rounding variance doubles; both are read once and kept nowhere).  Kt enters the states, which
+// rounding variance doubles; both are read once and kept nowhere).  Where no sequence is cut for want of tokens, P
+// has a second term: a row of a few tokens may hang on one of its elements (error of o of 4 tokens: 1.5 times o's own
+// rounding without, 1.1 with; 5 sequences of 17 to 200 tokens take 12.9 us of the device with, 12.2 without).  131072 tokens
+// would take 334 instead of 312 us, and there the error is 1.35 times o's rounding whatever the tokens.  Kt enters the states, which
 // are fp32 and live on: it is split into three bf16 terms that hold all 24 bits, three products
 // instead of one.  With two terms the states would be off by 2.3e-6, with one by 1.6e-3.
 //
@@ -64,7 +67,7 @@ constexpr uint32_t kSmQ = 4 * kTile, kSmS = 6 * kTile, kSmShared = 7 * kTile;
 __device__ __forceinline__ constexpr uint32_t tile_k(uint32_t st) { return 2 * st * kTile; }
 __device__ __forceinline__ constexpr uint32_t tile_v(uint32_t st) { return (2 * st + 1) * kTile; }
 
-// TMEM columns: X and P (block b of P over the first 16 columns of its scores), O, D, buffers of 32 tokens of Kt in three
+// TMEM columns: X and P (16 tokens of P over the first 8 columns of their scores, its second term over the next 8), O, D, buffers of 32 tokens of Kt in three
 // terms of 16 columns.  Without outputs eight buffers, over X and O as well.
 constexpr uint32_t kTmO = 128, kTmD = 384, kTmK = 256, kTmTerm = 16, kTmBuf = 48;
 
@@ -114,6 +117,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                         const ChunkParams p) {
     constexpr uint32_t kStages = OUTPUT ? 2 : 3;
+    constexpr int kTerms = SOURCE == kWhole ? 2 : 1;  // of P
     extern __shared__ __align__(1024) uint8_t sm[];
     Shared &sh = *reinterpret_cast<Shared *>(sm + kSmShared);
     volatile int &dead = sh.dead;
@@ -250,8 +254,10 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     constexpr uint32_t idesc = idesc_bf16(kTok, kTok) | (1u << 16);
 #pragma unroll
                     for (int j = 0; j < kTok / 16; ++j)
-                        mma_bf16_ts(tmem + kTmO, tmem + 32 * (j >> 1) + 8 * (j & 1),
-                                    ((uint64_t)kDescHi << 32) | (uint64_t)(v_lo + (tile_v(st) >> 4) + 128 * j), idesc, 1);
+#pragma unroll
+                        for (int t = 0; t < kTerms; ++t)
+                            mma_bf16_ts(tmem + kTmO, tmem + 16 * j + 8 * t,
+                                        ((uint64_t)kDescHi << 32) | (uint64_t)(v_lo + (tile_v(st) >> 4) + 128 * j), idesc, 1);
                     mma_commit(&sh.v_empty[st]);
                     mma_commit(&sh.o_full);
                 }
@@ -611,7 +617,11 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e) {
                         const int j0 = 32 * u + 16 * e, seen = row - j0;  // seen: the last column that this row sees
-                        uint32_t y[8];
+                        uint32_t y[8 * kTerms];  // the columns' leading terms, and what these leave
+                        auto split = [&](int j, F2 z) {
+                            y[j] = narrow(z);
+                            if (kTerms == 2) y[8 + j] = narrow(fma2(wide(y[j]), f2(-1.0f, -1.0f), z));
+                        };
                         if (u <= w) {
                             float x[16];
                             tmem_ld16(tmem + lanes + j0, x);
@@ -620,24 +630,25 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) {
                                     const float2 z = *(const float2 *)&sh.lower[st][j0 + 2 * j];
-                                    y[j] = pack2(x[2 * j] * (a.scale * exp2f(own - z.x)), x[2 * j + 1] * (a.scale * exp2f(own - z.y)));
+                                    split(j, f2(x[2 * j] * (a.scale * exp2f(own - z.x)), x[2 * j + 1] * (a.scale * exp2f(own - z.y))));
                                 }
                             } else {
 #pragma unroll
                                 for (int j = 0; j < 16; j += 4) {
                                     const float4 z = *(const float4 *)&sh.upper[st][j0 + j];
-                                    y[j / 2] = narrow(mul2(f2(x[j], x[j + 1]), mul2(f2(z.x, z.y), f2(f, f))));
-                                    y[j / 2 + 1] = narrow(mul2(f2(x[j + 2], x[j + 3]), mul2(f2(z.z, z.w), f2(f, f))));
+                                    split(j / 2, mul2(f2(x[j], x[j + 1]), mul2(f2(z.x, z.y), f2(f, f))));
+                                    split(j / 2 + 1, mul2(f2(x[j + 2], x[j + 3]), mul2(f2(z.z, z.w), f2(f, f))));
                                 }
                             }
                             if (u == w)
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) y[j] = seen > 2 * j ? y[j] : seen == 2 * j ? y[j] & 0xffffu : 0u;
+                                for (int j = 0; j < 8 * kTerms; ++j) y[j] = seen > 2 * (j & 7) ? y[j] : seen == 2 * (j & 7) ? y[j] & 0xffffu : 0u;
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] = 0;
+                            for (int j = 0; j < 8 * kTerms; ++j) y[j] = 0;
                         }
-                        tmem_st8(tmem + lanes + 32 * u + 8 * e, y);  // over scores of the block that are read
+                        if constexpr (kTerms == 2) tmem_st16(tmem + lanes + j0, y);
+                        else tmem_st8(tmem + lanes + j0, y);  // over scores of the block that are read
                     }
                     arrive(&sh.gates_empty[st]);
                     // O so far, Q . S, times the row's decay
