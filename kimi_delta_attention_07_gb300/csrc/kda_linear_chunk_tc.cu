@@ -35,7 +35,7 @@
 // value that is not finite would reach rows before it as 0 times it: V is looked through,
 // such values become 0 and their channel NaN from their row on, in o and in S.
 //
-// What bounds a chunk: not its products (3072 of its 7000 clocks; without them it takes a tenth less) but
+// What bounds a chunk: not its products (less than half of its 7000 clocks; without them it takes a tenth less) but
 // the chain of instructions of a warp, each some seven clocks behind the last.  So the work is spread over
 // as many warps as there are registers for (five groups of four with 128 registers: 9300 clocks).  With outputs, eight warps look through V and make Kt and
 // run ahead, sixteen make P and hold the state, 32 value channels each, and take a chunk's outputs while the
