@@ -66,6 +66,8 @@ def kda_head_norm_rope(q, k=None, *, positions=None, inv_freq=None, sections=Non
     if q_out is None:
         q_out = _empty((T, Hq, D), dtype, q.device, stream)
     poq, soq = _rows(q_out, "q_out", dtype, (T, Hq, D), dev)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
     pk = pok = None
     Hk = sk = sok = 0
     if k is not None:

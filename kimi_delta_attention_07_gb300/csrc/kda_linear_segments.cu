@@ -213,7 +213,9 @@ cudaError_t launch_segment_lists(const ChunkParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_segment_join(const ChunkParams &p, cudaStream_t stream) {
-    return launch_dependent(segment_join_kernel, dim3((unsigned)std::min(p.a.n_seqs, p.entries), (unsigned)p.a.H, kJoinParts),
+    // (no more CTAs than two for each place of an SM: most calls of several sequences have nothing to join)
+    const int most = std::max(1, 16 * sm_count() / (p.a.H * kJoinParts));
+    return launch_dependent(segment_join_kernel, dim3((unsigned)std::min({p.a.n_seqs, p.entries, most}), (unsigned)p.a.H, kJoinParts),
                             dim3(kJoinThreads), 0, stream, p);
 }
 

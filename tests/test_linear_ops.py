@@ -363,6 +363,12 @@ def test_chunk_not_finite_leaves_the_rows_before_it(kda, dtype, which, value):
         assert not o[at].isfinite().any() and torch.equal(o[at + 1:], clean[at + 1:]) and s.isfinite().all()
 
 
+def test_rope_refuses_a_destination_without_its_source(kda):
+    q = normal((4, 2, 128), 0)
+    with pytest.raises(ValueError, match="k_out without k"):
+        kda.kda_head_norm_rope(q, k_out=torch.empty_like(q))
+
+
 def test_chunk_repeats_bit_for_bit_and_in_a_graph(kda):
     q, k, v, g = layer_inputs(2500, 2, 2, torch.bfloat16, 0)
     cu = i32([0, 1900, 2500])
