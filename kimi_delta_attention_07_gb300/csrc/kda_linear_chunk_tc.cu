@@ -582,31 +582,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                         if (b < w && b > u) before += x;
                         whole += x;
                     }
-                    // the state, while the scores are computed
                     const float decay = exp2f(whole);
-                    wait(&sh.d_full, c & 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float x[16];
-                        tmem_ld16(td + 16 * k, x);
-                        tmem_ld_wait_for(x);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) S[8 * k + j] = fma2(f2(decay, decay), S[8 * k + j], f2(x[2 * j], x[2 * j + 1]));
-                    }
-                    tc_fence_before();
-                    if (__builtin_expect(odd, 0)) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint8_t *from = &sh.odd[c & 3][32 * u + 2 * e];
-                            float lo, hi;
-                            unf2(S[e], lo, hi);
-                            S[e] = f2(from[0] < kTok ? NAN : lo, from[1] < kTok ? NAN : hi);
-                        }
-                    }
-                    // (what follows it, the next chunk's D, is what keeps the check of V from writing `odd` four chunks on
-                    // before these warps have taken that chunk's outputs)
-                    arrive(&sh.d_empty);
                     // P: columns 32 u ..  e^{G_i - G_j} as a factor of the row and one of the column, with the end of block u
                     // between them; on the diagonal block, whose rows lie before that end, only while the row's stays finite.
                     const float tail = u == w ? own - sh.block[st][w] : before;
@@ -651,6 +627,30 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                         else tmem_st8(tmem + lanes + j0, y);  // over scores of the block that are read
                     }
                     arrive(&sh.gates_empty[st]);
+                    // the state, while Q . S is computed
+                    wait(&sh.d_full, c & 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float x[16];
+                        tmem_ld16(td + 16 * k, x);
+                        tmem_ld_wait_for(x);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) S[8 * k + j] = fma2(f2(decay, decay), S[8 * k + j], f2(x[2 * j], x[2 * j + 1]));
+                    }
+                    tc_fence_before();
+                    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint8_t *from = &sh.odd[c & 3][32 * u + 2 * e];
+                            float lo, hi;
+                            unf2(S[e], lo, hi);
+                            S[e] = f2(from[0] < kTok ? NAN : lo, from[1] < kTok ? NAN : hi);
+                        }
+                    }
+                    // (`odd` is written again four chunks on: behind P . V of the chunk after the next, so behind this and
+                    // this chunk's outputs)
+                    arrive(&sh.d_empty);
                     // O so far, Q . S, times the row's decay
                     const float to_row = exp2f(upto) * a.scale;
                     wait(&sh.qs_full, c & 1);
