@@ -48,6 +48,7 @@
 // Warps: 0 TMA, 1 MMA of X and O, 2 MMA of D, 3 decays, 4..11 check of V and Kt, 12..27 P, the state
 // and the outputs; without outputs 4..19 all of it.
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_attn.cuh"
 #include "kda_linear_segments.cuh"
@@ -504,11 +505,8 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             // ---- P, the state and the outputs: a thread stands for a row of P, a token of o and a key channel of the state
             uint32_t c = 0;
             const uint32_t to = tmem + kTmO + 32 * u + lanes, td = tmem + kTmD + 32 * u + lanes;
-            // the last chunk's outputs, which are not taken yet: this thread's 32 values (where there are fewer than 128 rows)
-            __nv_bfloat16 *o = nullptr;
-            int o_rows = 0;
-            bool o_odd = false;
-            auto take_outputs = [&] {
+            // chunk c - 1's outputs: a row of fewer than 128 is stored at o, the others are left for the copying warp
+            auto take_outputs = [&](auto last, __nv_bfloat16 *o, int rows) {
                 const uint32_t n = c - 1;
                 wait(&sh.o_full, n & 1);
                 tc_fence_after();
@@ -522,19 +520,19 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     for (int j = 0; j < 8; ++j) y[2 * k + (j >> 2)][j & 3] = pack2(x[2 * j], x[2 * j + 1]);
                 }
                 tc_fence_before();
-                arrive(&sh.o_empty);
-                if (__builtin_expect(o_odd, 0)) {
+                if (!last) arrive(&sh.o_empty);
+                if (__builtin_expect(sh.any_odd[u >> 1][n & 3], 0)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (sh.odd[n & 3][32 * u + j] <= row) y[j >> 3][(j >> 1) & 3] |= j & 1 ? 0x7fff0000u : 0x7fffu;
                 }
-                if (o_rows == kTok) {  // into the place of Q, for the copying warp
+                if (!last || rows == kTok) {  // into the place of Q
                     uint8_t *q = sm + kSmQ + (n & 1) * kTile + (u >> 1) * kHalf + row * 128;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         *(uint4 *)(q + (((4 * (u & 1) + j) ^ (row & 7)) << 4)) = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
                     fence_async_smem();
-                } else if (row < o_rows) {
+                } else if (row < rows) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) ((uint4 *)o)[j] = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
                 }
@@ -566,11 +564,13 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                             make_uint4(narrow(S[4 * j]), narrow(S[4 * j + 1]), narrow(S[4 * j + 2]), narrow(S[4 * j + 3]));
                     fence_async_smem();
                 };
-                if (chunks > 0) publish();
+                if (chunks > 0) {
+                    publish();
+                    arrive(&sh.o_empty);
+                }
                 for (int i = 0; i < chunks; ++i, ++c) {
                     const uint32_t st = c & 1, full = (c >> 1) & 1;
-                    if (c == 0) arrive(&sh.o_empty);
-                    if (c > 0) take_outputs();
+                    if (i > 0) take_outputs(std::false_type(), nullptr, kTok);
                     wait(&sh.v_ready[st], full);
                     const bool odd = sh.any_odd[u >> 1][c & 3];
                     const float own = sh.lower[st][row];
@@ -672,9 +672,6 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     arrive(&sh.pv_ready);
-                    o = (__nv_bfloat16 *)a.o + ((int64_t)(s.x + i * kTok + row) * a.H + head_of(s)) * kHeadDim + 32 * u;
-                    o_rows = min(kTok, s.y - i * kTok);
-                    o_odd = odd;
                     if (i + 1 < chunks) publish();
                 }
                 if (float *out = state_after(p, s)) {
@@ -682,8 +679,11 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
                 }
+                if (chunks > 0) {
+                    const int first = (chunks - 1) * kTok;
+                    take_outputs(std::true_type(), (__nv_bfloat16 *)a.o + ((int64_t)(s.x + first + row) * a.H + head_of(s)) * kHeadDim + 32 * u, s.y - first);
+                }
             });
-            if (c > 0) take_outputs();
         }
     }
     tc_fence_before();
