@@ -16,7 +16,7 @@
 // rounding variance doubles; both are read once and kept nowhere).  Where no sequence is cut for want of tokens, P
 // has a second term: a row of a few tokens may hang on one of its elements (error of o of 4 tokens: 1.5 times o's own
 // rounding without, 1.1 with; 5 sequences of 17 to 200 tokens take 12.9 us of the device with, 12.2 without).  131072 tokens
-// would take 334 instead of 312 us, and there the error is 1.35 times o's rounding whatever the tokens.  Kt enters the states, which
+// would take 7 % more, and there the error is 1.35 times o's rounding whatever the tokens.  Kt enters the states, which
 // are fp32 and live on: it is split into three bf16 terms that hold all 24 bits, three products
 // instead of one.  With two terms the states would be off by 2.3e-6, with one by 1.6e-3.
 //
@@ -35,15 +35,19 @@
 // value that is not finite would reach rows before it as 0 times it: V is looked through,
 // such values become 0 and their channel NaN from their row on, in o and in S.
 //
-// What bounds a chunk: not its products (less than half of its 7000 clocks; without them it takes a tenth less) but
+// What bounds a chunk: not its products (half of its 6300 clocks; without them it took a tenth less) but
 // the chain of instructions of a warp, each some seven clocks behind the last.  So the work is spread over
 // as many warps as there are registers for (five groups of four with 128 registers: 9300 clocks).  With outputs, eight warps look through V and make Kt and
 // run ahead, sixteen make P and hold the state, 32 value channels each, and take a chunk's outputs while the
 // next one's scores are computed; without outputs, sixteen warps make a quarter of Kt each and update a
 // quarter of the state while the next chunk's D runs.
 //
-// 131072 tokens of 8 heads: 316 us, of which the segments' states take 104 (4.9 TB/s), the join 6 and the
-// outputs 205 (5.2 TB/s); 4096 tokens of 32 heads: 66 us; 8 sequences of 333 to 4001 tokens, 32 heads, uncut: 140 us.
+// What a chunk waits for is ordered so that little waits: its outputs, then P while D's last quarters are made, the state
+// while Q . S is computed (in front of P 313 us for 131072 tokens, behind the scaling of O 327, here 300), the copy of S
+// while P . V is.
+//
+// 131072 tokens of 8 heads: 296 us, of which the segments' states take 104 (4.9 TB/s), the join 6 and the
+// outputs 189 (5.6 TB/s); 4096 tokens of 32 heads: 63 us; 8 sequences of 333 to 4001 tokens, 32 heads, uncut: 128 us.
 //
 // Warps: 0 TMA, 1 MMA of X and O, 2 MMA of D, 3 decays, 4..11 check of V and Kt, 12..27 P, the state
 // and the outputs; without outputs 4..19 all of it.

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
     };
     // Cut, or not: by the time of the longest part, or of all (and a quarter of that for the uneven end) where that is
     // more.  A segment's own state takes half the time of its outputs.  (16 sequences of 4000 tokens, 8 heads: 142 us
-    // uncut, 200 cut; one of 60000 and 15 of 300: cut, 192.  Longer segments than p.segment never come out
+    // uncut, 200 cut, now 125; one of 60000 and 15 of 300: cut, 179.  Longer segments than p.segment never come out
     // more than a little better than these two.)
     int my_longest = 0, my_followed = 0;
     uint32_t my_sum = 0;
