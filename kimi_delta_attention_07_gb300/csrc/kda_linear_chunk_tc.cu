@@ -15,7 +15,7 @@
 // What is rounded: P and the copy of S that O is taken from, to bf16 (as o itself is, so that o's
 // rounding variance doubles; both are read once and kept nowhere).  Where no sequence is cut for want of tokens, P
 // has a second term: a row of a few tokens may hang on one of its elements (error of o of 4 tokens: 1.5 times o's own
-// rounding without, 1.1 with; 5 sequences of 17 to 200 tokens take 12.9 us of the device with, 12.2 without).  131072 tokens
+// rounding without, 1.1 with; 5 sequences of 17 to 200 tokens take 12.9 us of the device with, 12.2 without, at the time).  131072 tokens
 // would take 7 % more, and there the error is 1.35 times o's rounding whatever the tokens.  Kt enters the states, which
 // are fp32 and live on: it is split into three bf16 terms that hold all 24 bits, three products
 // instead of one.  With two terms the states would be off by 2.3e-6, with one by 1.6e-3.
@@ -46,7 +46,7 @@
 // while Q . S is computed (in front of P 313 us for 131072 tokens, behind the scaling of O 327, here 300), the copy of S
 // while P . V is.
 //
-// 131072 tokens of 8 heads: 296 us, of which the segments' states take 104 (4.9 TB/s), the join 6 and the
+// 131072 tokens of 8 heads: 294 us, of which the segments' states take 104 (4.9 TB/s), the join 6 and the
 // outputs 189 (5.6 TB/s); 4096 tokens of 32 heads: 63 us; 8 sequences of 333 to 4001 tokens, 32 heads, uncut: 128 us.
 //
 // Warps: 0 TMA, 1 MMA of X and O, 2 MMA of D, 3 decays, 4..11 check of V and Kt, 12..27 P, the state
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             }
 #pragma unroll
             for (int l = 0; l < 2; ++l) {  // 16 channels
-                uint32_t raw[8], term[3][8];
+                uint32_t raw[8], term[8];
                 const uint32_t from = k_at + tile_k(c % kStages) + 32 * b * 128 + (((unit + 2 * l) ^ turn) << 4);
                 ldmatrix4_trans(raw, from);
                 ldmatrix4_trans(raw + 4, from + 16 * 128);
@@ -419,21 +419,24 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 #pragma unroll
                 for (int m = 0; m < 8; ++m) {  // m = 2 j + h
                     y[m] = mul2(wide(raw[m]), weight[m >> 1]);
-                    term[0][m] = narrow(y[m]);
-                    y[m] = fma2(wide(term[0][m]), f2(-1.0f, -1.0f), y[m]);
-                    term[1][m] = narrow(y[m]);
-                }
-                if (terms == 3) {
-#pragma unroll
-                    for (int m = 0; m < 8; ++m) term[2][m] = narrow(fma2(wide(term[1][m]), f2(-1.0f, -1.0f), y[m]));
+                    term[m] = narrow(y[m]);
                 }
                 if (l == 0) {
                     wait(empty, parity);
                     tc_fence_after();
                 }
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
-                    if (t < terms) tmem_st_16x16(tk + ((uint32_t)(16 * l) << 16) + t * kTmTerm, term[t]);
+                for (int t = 0; t < 3; ++t) {
+                    if (t == 2 && terms < 3) break;
+                    tmem_st_16x16(tk + ((uint32_t)(16 * l) << 16) + t * kTmTerm, term);
+                    if (t < 2) {
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) {
+                            y[m] = fma2(wide(term[m]), f2(-1.0f, -1.0f), y[m]);
+                            term[m] = narrow(y[m]);
+                        }
+                    }
+                }
             }
             tmem_st_wait();
             tc_fence_before();
