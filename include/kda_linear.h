@@ -119,6 +119,8 @@ int kda_linear_chunk_fwd(const void *q, int64_t q_stride, const void *k, int64_t
  *   state_pool  [n_slots, H, V, K] fp32; state_indices int32 [N], distinct, NULL =
  *               slot n (then n_slots >= N).  A slot outside [0, n_slots) leaves the
  *               pool alone and gives NaN in that sequence's o.
+ * The decay is applied as the sum of two floats, so that a slow one does not add up its rounding over
+ * the steps (an infinity in the state may become NaN by it).
  * N = 0 is a no-op.
  */
 int kda_linear_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

@@ -35,6 +35,15 @@ __device__ __forceinline__ uint32_t narrow(F2 x) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// e^g as the sum of two floats.  As one, a decay near one that is applied again and again (token by token,
+// chunk by chunk, segment by segment) brings its rounding error back each time: with a fixed decay of 2^-8 a token,
+// 1e-5 in the state of a thousand tokens.  (d - 1 is exact from 1/2 to 2; smaller decays leave nothing for
+// their error to come back in.)
+__device__ __forceinline__ float2 decay_of(float g) {
+    const float d = expf(g);
+    return make_float2(d, d > 0.5f && d < 2.0f ? expm1f(g) - (d - 1.0f) : 0.0f);
+}
+
 struct HeadRopeArgs {
     const void *x[2];  // q, k
     void *y[2];

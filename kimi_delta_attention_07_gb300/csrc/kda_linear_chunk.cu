@@ -15,8 +15,7 @@
 // a SM (their registers hold the state), whose fma and shared-memory pipes are each half busy (4096 tokens of
 // 32 heads: 375 us, of which 174 are its fmas at the pipe's rate).
 //
-// A decay near one is the sum of two floats: as one, its rounding error would come back every
-// time that it is applied (a fixed decay of 2^-8 a token: 1e-5 in the state).
+// A decay near one is the sum of two floats (decay_of).
 #include <algorithm>
 #include <type_traits>
 
@@ -36,13 +35,6 @@ constexpr float kMostDecay = 8.0f;
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
-}
-
-// e^g as the sum of two floats
-__device__ __forceinline__ float2 decay_of(float g) {
-    const float d = expf(g);
-    // (d - 1 is exact from 1/2 to 2; smaller decays leave nothing for their error to come back in)
-    return make_float2(d, d > 0.5f && d < 2.0f ? expm1f(g) - (d - 1.0f) : 0.0f);
 }
 
 // OUTPUT: o and final states, from the states in front of the segments; else a segment's own state.
