@@ -43,6 +43,11 @@ __device__ __forceinline__ float2 decay_of(float g) {
     const float d = expf(g);
     return make_float2(d, d > 0.5f && d < 2.0f ? expm1f(g) - (d - 1.0f) : 0.0f);
 }
+// 2^x, likewise (the product's rounding is relative to x, and so is its effect over the decay's memory)
+__device__ __forceinline__ float2 decay_of_log2(float x) {
+    const float d = exp2f(x);
+    return make_float2(d, d > 0.5f && d < 2.0f ? expm1f(x * 0.6931471805599453f) - (d - 1.0f) : 0.0f);
+}
 
 struct HeadRopeArgs {
     const void *x[2];  // q, k

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 3) linear_chunk_f32_kernel(const Chu
             }
         if (!OUTPUT && blockIdx.y == 0 && tid < 32) {
             total = warp_sum(tid < kBlock ? total : 0.0f);
-            if (tid == 0) p.decay[entry_of(p, seg)] = expf(total);
+            if (tid == 0) p.decay[entry_of(p, seg)] = decay_of(total);
         }
     });
 }

@@ -10,7 +10,9 @@
 //   O          += P . V      P = X times its decays, bf16 in TMEM over X
 //   D  [d x e] = Kt . V      Kt = K^T times e^{G_127 - G_j}, in TMEM: lane = key channel
 // S stays in registers (fp32, lane = key channel) for as long as a CTA works on a sequence:
-// S = e^{G_127} S + D, which the tensor core could not scale.
+// S = e^{G_127} S + D, which the tensor core could not scale.  e^{G_127}, and a segment's decay, is the sum of two
+// floats (decay_of_log2): applied chunk by chunk, one near one would add up its rounding (131072 tokens of 2^-16 each:
+// states off by 1.8e-6, now by the 3e-7 of their sums).
 //
 // What is rounded: P and the copy of S that O is taken from, to bf16 (as o itself is, so that o's
 // rounding variance doubles; both are read once and kept nowhere).  Where no sequence is cut for want of tokens, P
@@ -82,6 +84,8 @@ struct Shared {
     alignas(16) float lower[2][kTok];  // log2 decay of a token's block up to and with it
     float upper[2][kTok];              // decay of a token's block behind it
     float block[2][4];                 // log2 decay of each block
+    float whole[4];                    // of a chunk; for four chunks, because they are read behind the arrival at gates_empty
+    float2 decay[4];                   // 2 to that, as the sum of two floats
     uint8_t odd[4][kTok];              // a value channel's first row that is not finite (kTok: none), if any_odd
     volatile int any_odd[4][4], dead;  // of a group of channels
     uint32_t tmem_base;
@@ -341,6 +345,10 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     sh.upper[st][32 * b + lane] = upper[b];
                     if (lane == 31) sh.block[st][b] = lower[b];
                 }
+                if (lane == 31) {
+                    const float whole = lower[0] + lower[1] + lower[2] + lower[3];
+                    sh.whole[c & 3] = whole, sh.decay[c & 3] = decay_of_log2(whole);
+                }
                 arrive(&sh.gates_full[st]);
             }
         });
@@ -468,19 +476,20 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                 F2 S[16];  // value channels 32 u + 2 e, and the one after
 #pragma unroll
                 for (int e = 0; e < 16; ++e) S[e] = 0;
-                float log_decay = 0.0f, whole = 0.0f;
+                float log_decay = 0.0f;
                 auto update = [&](uint32_t n) {  // by chunk n
                     wait(&sh.d_full, n & 1);
                     tc_fence_after();
-                    const float decay = exp2f(whole);
-                    log_decay += whole;
+                    const float2 decay = sh.decay[n & 3];
+                    log_decay += sh.whole[n & 3];
                     float x[32];
                     tmem_ld32(td, x);
                     tmem_ld_wait_for(x);
                     tc_fence_before();
                     arrive(&sh.d_empty);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) S[e] = fma2(f2(decay, decay), S[e], f2(x[2 * e], x[2 * e + 1]));
+                    for (int e = 0; e < 16; ++e)
+                        S[e] = fma2(f2(decay.x, decay.x), S[e], fma2(f2(decay.y, decay.y), S[e], f2(x[2 * e], x[2 * e + 1])));
                     if (__builtin_expect(sh.any_odd[u][n & 3], 0)) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -498,7 +507,6 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     arrive(&sh.kt_full[st]);
                     arrive(&sh.k_empty[c % kStages]);
                     if (i > 0) update(c - 1);
-                    whole = sh.block[st][0] + sh.block[st][1] + sh.block[st][2] + sh.block[st][3];
                     arrive(&sh.gates_empty[st]);
                 }
                 if (chunks > 0) update(c - 1);
@@ -506,7 +514,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                 float *out = p.states + at * kState + (int64_t)(32 * u) * kHeadDim + row;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) unf2(S[e], out[2 * e * kHeadDim], out[(2 * e + 1) * kHeadDim]);
-                if (u == 0 && row == 0) p.decay[at] = exp2f(log_decay);
+                if (u == 0 && row == 0) p.decay[at] = decay_of_log2(log_decay);
             });
         } else {
             // ---- P, the state and the outputs: a thread stands for a row of P, a token of o and a key channel of the state
@@ -581,15 +589,13 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     wait(&sh.v_ready[st], full);
                     const bool odd = sh.any_odd[u >> 1][c & 3];
                     const float own = sh.lower[st][row];
-                    float whole = 0.0f, upto = own, before = own;  // before: log2 decay from the end of block u to this row
+                    float upto = own, before = own;  // before: log2 decay from the end of block u to this row
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const float x = sh.block[st][b];
                         if (b < w) upto += x;
                         if (b < w && b > u) before += x;
-                        whole += x;
                     }
-                    const float decay = exp2f(whole);
                     // P: columns 32 u ..  e^{G_i - G_j} as a factor of the row and one of the column, with the end of block u
                     // between them; on the diagonal block, whose rows lie before that end, only while the row's stays finite.
                     const float tail = u == w ? own - sh.block[st][w] : before;
@@ -637,13 +643,17 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     // the state, while Q . S is computed
                     wait(&sh.d_full, c & 1);
                     tc_fence_after();
+                    const float2 decay = sh.decay[c & 3];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float x[16];
                         tmem_ld16(td + 16 * k, x);
                         tmem_ld_wait_for(x);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) S[8 * k + j] = fma2(f2(decay, decay), S[8 * k + j], f2(x[2 * j], x[2 * j + 1]));
+                        for (int j = 0; j < 8; ++j) {
+                            F2 &y = S[8 * k + j];
+                            y = fma2(f2(decay.x, decay.x), y, fma2(f2(decay.y, decay.y), y, f2(x[2 * j], x[2 * j + 1])));
+                        }
                     }
                     tc_fence_before();
                     if (__builtin_expect(odd, 0)) {
@@ -708,7 +718,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
             }
             if (state)
                 for (int j = tid; j < kState; j += blockDim.x) state[j] = NAN;
-            if (!OUTPUT && tid == 0) p.decay[at] = NAN;
+            if (!OUTPUT && tid == 0) p.decay[at] = make_float2(NAN, 0.0f);
         });
     }
     if (wid == 1) tmem_dealloc(tmem, 512);

@@ -30,7 +30,7 @@ struct ChunkParams {
     Item *cuts;     // [entries]: the sequences that are cut: first entry, such segments, slot
     float *states;  // [entries][H][V][K]
     float *first;   // [entries][H][V][K]: copies of initial states (those that a later CTA may overwrite)
-    float *decay;   // [entries][H]
+    float2 *decay;  // [entries][H], each the sum of two floats
 };
 
 // Where the segments are found: in the lists; a single sequence needs none, nor do sequences none of which is long

@@ -57,3 +57,31 @@ def test_steps_keep_a_slow_fixed_decay(kda, S, dtype):
             ref = ref * d + v[:, s].double()[..., :, None] * k[:, s].double()[..., None, :]
     for h in range(H):
         assert rel(pool[S - 1::S, h], ref[:, h]) < 2.0 ** -19, h
+
+
+def final_state(k, v, g):
+    """[H, V, K] behind tokens k, v [T, H, 128] with decays g [T, H], from zero, in 64 bits."""
+    g = g.double()
+    behind = (g.flip(0).cumsum(0).flip(0) - g).exp()
+    return torch.einsum("the,thd->hed", v.double() * behind[..., None], k.double())
+
+
+@pytest.mark.parametrize("dtype,T,n", [(torch.bfloat16, 131072, 1), (torch.bfloat16, 20000, 1), (torch.bfloat16, 6000, 3),
+                                       (torch.float32, 32768, 1), (torch.float32, 9000, 2)])
+@pytest.mark.parametrize("fixed", [True, False])
+def test_chunks_keep_slow_decays(kda, dtype, T, n, fixed):
+    """Decays of 2^-8 to 2^-20 a token over whole prompts, chunk by chunk and segment by segment.  A token's weight
+    carries two exponentials (2^-22 each), three products and its exponent's rounding (2^-24 each, relative to
+    exponents that are at most some units while the weight counts); the sums, a rounding of 2^-24 / sqrt 3 for each of
+    some hundreds of chunks, segments or tokens in a row, add sqrt(200) of those: 2^-20 of the norm in all.  A decay as one
+    float adds 2^-25 for each time that it is applied within its memory: 200 segments 2^-17."""
+    H = 4
+    rate = torch.exp2(-torch.tensor([8.0, 12.0, 16.0, 20.0], device="cuda"))
+    g = (-0.9 * rate if fixed else -rate * torch.rand((T, H), generator=torch.Generator("cuda").manual_seed(5), device="cuda"))
+    q, k, v = (normal((T, H, 128), i, dtype) for i in range(3))
+    cu = [0] + [T * (2 * i + 1) // (2 * n) for i in range(1, n)] + [T]
+    _, s = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu))
+    for i, (a, b) in enumerate(zip(cu, cu[1:])):
+        ref = final_state(k[a:b], v[a:b], g.expand(T, H)[a:b])
+        for h in range(H):
+            assert rel(s[i, h], ref[h]) < 2.0 ** -20, (i, h)
