@@ -88,8 +88,8 @@ size_t kda_linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H,
  *   o              shares no memory with the inputs or the states
  * bf16 runs on the tensor cores: chunks of 128 tokens, fp32 accumulation and states;
  * the scores and the state enter the products that give o as bf16 (two roundings
- * beside o's own; the scores of calls of at most 640 tokens as two terms, 16 bits); what is written to the state is split into three bf16 terms, so
- * that the states are as exact as fp32 sums.  fp32 runs on the CUDA cores, token by
+ * beside o's own; the scores of a sequence's first 128 tokens as two terms, 16 bits); what is written to the state is
+ * split into three bf16 terms, so that the states are as exact as fp32 sums.  fp32 runs on the CUDA cores, token by
  * token.  Long sequences are cut into segments that are worked on at the same time.
  * A zero-length sequence hands back its initial state (or zeros).  A slot outside
  * [0, n_slots) gives NaN in that sequence's rows of o and leaves the pools alone.

@@ -15,10 +15,11 @@
 // states off by 1.8e-6, now by the 3e-7 of their sums).
 //
 // What is rounded: P and the copy of S that O is taken from, to bf16 (as o itself is, so that o's
-// rounding variance doubles; both are read once and kept nowhere).  Where no sequence is cut for want of tokens, P
-// has a second term: a row of a few tokens may hang on one of its elements (error of o of 4 tokens: 1.5 times o's own
-// rounding without, 1.1 with; 5 sequences of 17 to 200 tokens take 12.9 us of the device with, 12.2 without, at the time).  131072 tokens
-// would take 7 % more, and there the error is 1.35 times o's rounding whatever the tokens.  Kt enters the states, which
+// rounding variance doubles; both are read once and kept nowhere).  In the chunk that a sequence begins with, P
+// has a second term: a row of a few tokens may hang on one of its elements (error of o of 4 tokens: 1.4 times o's own
+// rounding without, up to 2 for a row; 1.0 with).  It is a matter of the sequence alone, not of what else is in the call.  4096
+// sequences of 40 tokens take 292 us with, 267 without, 131072 tokens 300 and 298; in every chunk, 331, for an
+// error of 1.2 instead of 1.4 times o's rounding.  Kt enters the states, which
 // are fp32 and live on: it is split into three bf16 terms that hold all 24 bits, three products
 // instead of one.  With two terms the states would be off by 2.3e-6, with one by 1.6e-3.
 //
@@ -85,6 +86,7 @@ struct Shared {
     float upper[2][kTok];              // decay of a token's block behind it
     float block[2][4];                 // log2 decay of each block
     float whole[4];                    // of a chunk; for four chunks, because they are read behind the arrival at gates_empty
+    int early[4];                      // a sequence begins with the chunk: P has two terms
     float2 decay[4];                   // 2 to that, as the sum of two floats
     uint8_t odd[4][kTok];              // a value channel's first row that is not finite (kTok: none), if any_odd
     volatile int any_odd[4][4], dead;  // of a group of channels
@@ -126,7 +128,6 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                         const ChunkParams p) {
     constexpr uint32_t kStages = OUTPUT ? 2 : 3;
-    constexpr int kTerms = SOURCE == kWhole ? 2 : 1;  // of P
     extern __shared__ __align__(1024) uint8_t sm[];
     Shared &sh = *reinterpret_cast<Shared *>(sm + kSmShared);
     volatile int &dead = sh.dead;
@@ -261,12 +262,14 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                 tc_fence_after();
                 if (elect_one()) {
                     constexpr uint32_t idesc = idesc_bf16(kTok, kTok) | (1u << 16);
+                    const uint64_t v_at = ((uint64_t)kDescHi << 32) | (uint64_t)(v_lo + (tile_v(st) >> 4));
 #pragma unroll
-                    for (int j = 0; j < kTok / 16; ++j)
-#pragma unroll
-                        for (int t = 0; t < kTerms; ++t)
-                            mma_bf16_ts(tmem + kTmO, tmem + 16 * j + 8 * t,
-                                        ((uint64_t)kDescHi << 32) | (uint64_t)(v_lo + (tile_v(st) >> 4) + 128 * j), idesc, 1);
+                    for (int j = 0; j < kTok / 16; ++j) mma_bf16_ts(tmem + kTmO, tmem + 16 * j, v_at + 128 * j, idesc, 1);
+                    if (i == 0 && (s.w & kBegins)) {  // the second terms, of the tokens that are there
+                        const int steps = (min(kTok, s.y) + 15) / 16;
+#pragma unroll 1
+                        for (int j = 0; j < steps; ++j) mma_bf16_ts(tmem + kTmO, tmem + 16 * j + 8, v_at + 128 * j, idesc, 1);
+                    }
                     mma_commit(&sh.v_empty[st]);
                     mma_commit(&sh.o_full);
                 }
@@ -346,6 +349,7 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     if (lane == 31) sh.block[st][b] = lower[b];
                 }
                 if (lane == 31) {
+                    sh.early[c & 3] = i == 0 && (s.w & kBegins);
                     const float whole = lower[0] + lower[1] + lower[2] + lower[3];
                     sh.whole[c & 3] = whole, sh.decay[c & 3] = decay_of_log2(whole);
                 }
@@ -603,42 +607,47 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
                     wait(&sh.x_full, c & 1);
                     tc_fence_after();
                     const bool exact = u == w && __any_sync(0xffffffffu, !(tail < 80.0f));
+                    auto make_p = [&](auto two) {
+                        constexpr int terms = two ? 2 : 1;
 #pragma unroll 1
-                    for (int e = 0; e < 2; ++e) {
-                        const int j0 = 32 * u + 16 * e, seen = row - j0;  // seen: the last column that this row sees
-                        uint32_t y[8 * kTerms];  // the columns' leading terms, and what these leave
-                        auto split = [&](int j, F2 z) {
-                            y[j] = narrow(z);
-                            if (kTerms == 2) y[8 + j] = narrow(fma2(wide(y[j]), f2(-1.0f, -1.0f), z));
-                        };
-                        if (u <= w) {
-                            float x[16];
-                            tmem_ld16(tmem + lanes + j0, x);
-                            tmem_ld_wait_for(x);
-                            if (__builtin_expect(exact, 0)) {
+                        for (int e = 0; e < 2; ++e) {
+                            const int j0 = 32 * u + 16 * e, seen = row - j0;  // seen: the last column that this row sees
+                            uint32_t y[8 * terms];  // the columns' leading terms, and what these leave
+                            auto split = [&](int j, F2 z) {
+                                y[j] = narrow(z);
+                                if (terms == 2) y[8 + j] = narrow(fma2(wide(y[j]), f2(-1.0f, -1.0f), z));
+                            };
+                            if (u <= w) {
+                                float x[16];
+                                tmem_ld16(tmem + lanes + j0, x);
+                                tmem_ld_wait_for(x);
+                                if (__builtin_expect(exact, 0)) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const float2 z = *(const float2 *)&sh.lower[st][j0 + 2 * j];
-                                    split(j, f2(x[2 * j] * (a.scale * exp2f(own - z.x)), x[2 * j + 1] * (a.scale * exp2f(own - z.y))));
+                                    for (int j = 0; j < 8; ++j) {
+                                        const float2 z = *(const float2 *)&sh.lower[st][j0 + 2 * j];
+                                        split(j, f2(x[2 * j] * (a.scale * exp2f(own - z.x)), x[2 * j + 1] * (a.scale * exp2f(own - z.y))));
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int j = 0; j < 16; j += 4) {
+                                        const float4 z = *(const float4 *)&sh.upper[st][j0 + j];
+                                        split(j / 2, mul2(f2(x[j], x[j + 1]), mul2(f2(z.x, z.y), f2(f, f))));
+                                        split(j / 2 + 1, mul2(f2(x[j + 2], x[j + 3]), mul2(f2(z.z, z.w), f2(f, f))));
+                                    }
                                 }
+                                if (u == w)
+#pragma unroll
+                                    for (int j = 0; j < 8 * terms; ++j) y[j] = seen > 2 * (j & 7) ? y[j] : seen == 2 * (j & 7) ? y[j] & 0xffffu : 0u;
                             } else {
 #pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const float4 z = *(const float4 *)&sh.upper[st][j0 + j];
-                                    split(j / 2, mul2(f2(x[j], x[j + 1]), mul2(f2(z.x, z.y), f2(f, f))));
-                                    split(j / 2 + 1, mul2(f2(x[j + 2], x[j + 3]), mul2(f2(z.z, z.w), f2(f, f))));
-                                }
+                                for (int j = 0; j < 8 * terms; ++j) y[j] = 0;
                             }
-                            if (u == w)
-#pragma unroll
-                                for (int j = 0; j < 8 * kTerms; ++j) y[j] = seen > 2 * (j & 7) ? y[j] : seen == 2 * (j & 7) ? y[j] & 0xffffu : 0u;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8 * kTerms; ++j) y[j] = 0;
+                            if constexpr (terms == 2) tmem_st16(tmem + lanes + j0, y);
+                            else tmem_st8(tmem + lanes + j0, y);  // over scores of the block that are read
                         }
-                        if constexpr (kTerms == 2) tmem_st16(tmem + lanes + j0, y);
-                        else tmem_st8(tmem + lanes + j0, y);  // over scores of the block that are read
-                    }
+                    };
+                    if (__builtin_expect(sh.early[c & 3], 0)) make_p(std::true_type());
+                    else make_p(std::false_type());
                     arrive(&sh.gates_empty[st]);
                     // the state, while Q . S is computed
                     wait(&sh.d_full, c & 1);

@@ -85,3 +85,56 @@ def test_chunks_keep_slow_decays(kda, dtype, T, n, fixed):
         ref = final_state(k[a:b], v[a:b], g.expand(T, H)[a:b])
         for h in range(H):
             assert rel(s[i, h], ref[h]) < 2.0 ** -20, (i, h)
+
+
+# ---- rows of a few tokens, alone and beside others -------------------------------------
+
+
+def run(kda, data, order, H):
+    """o of the sequences data[i] for i in order, packed, each with 0.5 in its initial state."""
+    q, k, v, g = (torch.cat([data[i][j] for i in order]) for j in range(4))
+    cu = [0]
+    for i in order:
+        cu.append(cu[-1] + data[i][0].shape[0])
+    s0 = torch.full((len(order), H, 128, 128), 0.5, device="cuda")
+    o, s = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu), initial_state=s0)
+    return {i: (o[a:b], s[n]) for n, (i, a, b) in enumerate(zip(order, cu, cu[1:]))}
+
+
+@pytest.mark.parametrize("H,Hk", [(8, 2), (90, 1)])
+def test_a_sequence_does_not_depend_on_the_others(kda, H, Hk):
+    """Short sequences, which no call cuts, bit for bit: alone, a few together, and beside a long one."""
+    lens = [4, 1, 130, 77, 512, 300, 1900]
+    data = [(normal((n, Hk, 128), 5 * i), normal((n, Hk, 128), 5 * i + 1), normal((n, H, 128), 5 * i + 2),
+             -torch.rand((n, H), generator=torch.Generator("cuda").manual_seed(i), device="cuda")) for i, n in enumerate(lens)]
+    together = [run(kda, data, order, H) for order in ([0, 1, 2, 3], [6, 0, 1, 2, 3, 4, 5], [5, 4, 3, 2, 1, 0, 6])]
+    for i in range(6):
+        o, s = run(kda, data, [i], H)[i]
+        for others in together:
+            if i in others:
+                assert torch.equal(others[i][0], o) and torch.equal(others[i][1], s), i
+
+
+@pytest.mark.parametrize("lens", [[4], [4] * 200, [1, 2, 3, 31, 33, 128] * 6, [3, 2500, 5]])
+@pytest.mark.parametrize("decay", [0.0, -0.05, -3.0])
+def test_first_rows_are_off_by_little_more_than_their_own_rounding(kda, lens, decay):
+    """o of a sequence's first 128 tokens from zero: rounded to bf16 (2^-8), behind scores as two bf16 terms (2^-16 of each
+    p_ij v_j) and fp32 sums and decays (2^-17 of |q| |k| |v|, weighed alike: 8 steps of 2^-22 and three exponentials)."""
+    H, T = 4, sum(lens)
+    q, k, v = (normal((T, H, 128), i) for i in range(3))
+    g = torch.full((H,), decay, device="cuda")
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    o, _ = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu))
+    for a, b in zip(cu, cu[1:]):
+        b = min(b, a + 128)
+        x, y, z = (t[a:b].double().transpose(0, 1) for t in (q, k, v))
+        at = torch.arange(b - a, device="cuda", dtype=torch.float64)
+        weight = ((at[:, None] - at) * g.double()[0]).exp().tril() * 128 ** -0.5
+        p = x @ y.transpose(1, 2) * weight
+        ref = p @ z
+        bound = (2.0 ** -8 * (1 + 2.0 ** -7) * ref.abs() + 2.0 ** -16 * (p.abs() @ z.abs())
+                 + 2.0 ** -17 * (x.abs() @ y.abs().transpose(1, 2) * weight @ z.abs()))
+        off = (o[a:b].double().transpose(0, 1) - ref).abs()
+        assert (off <= bound).all(), float((off / bound).max())
