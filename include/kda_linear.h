@@ -74,7 +74,7 @@ int kda_head_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
                        int64_t n_tokens, int Hq, int Hk, int D, int dtype, void *stream);
 
 /* Device workspace (256-byte aligned) of kda_linear_chunk_fwd: the states between the
- * parts that long sequences are cut into.  0: none is needed; 0 on invalid sizes. */
+ * parts that long sequences are cut into, and lists of several sequences.  0: none is needed; 0 on invalid sizes. */
 size_t kda_linear_chunk_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int dtype);
 
 /*

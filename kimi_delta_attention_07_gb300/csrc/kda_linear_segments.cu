@@ -170,9 +170,11 @@ inline int64_t entries_of(int64_t total_tokens, int64_t segment) { return total_
 struct Layout {
     size_t outputs, inner, cuts, decay, states, total;
 };
+// Lists pay for themselves from this many tokens on, if only by their order.
+constexpr int64_t kListTokens = 640;
 inline Layout layout(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
     const int64_t entries = entries_of(total_tokens, segment);
-    const bool lists = n_seqs > 1 && entries > 0;
+    const bool lists = n_seqs > 1 && (entries > 0 || total_tokens > kListTokens);
     Layout l;
     l.outputs = lists ? 256 : 0;
     l.inner = l.outputs + (lists ? align_up((size_t)(entries + n_seqs) * sizeof(Item), 256) : 0);
@@ -195,6 +197,7 @@ ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment, int paralle
     ChunkParams p{a};
     p.segment = (int)segment;
     p.entries = (int)entries_of(a.total_tokens, segment);
+    p.listed = a.n_seqs > 1 && (p.entries > 0 || (a.cu_seqlens && a.total_tokens > kListTokens));
     p.joined = p.entries > 0;
     p.parallel = parallel;
     p.fixed = fixed;

@@ -23,8 +23,9 @@ struct ChunkParams {
     int entries;    // segments whose state the workspace holds, at most
     int parallel;   // segments and heads that are worked on at the same time
     int fixed;      // tokens of one that cost as much as the two launches of a cut
+    bool listed;    // there are lists
     bool joined;    // the kernel follows the others: its inputs are there before it begins
-    int *counts;    // length of each list (no lists of a single sequence, or where no sequence is long enough to be cut)
+    int *counts;    // length of each list
     Item *outputs;  // all segments, the longest first
     Item *inner;    // [entries]: those that others follow in their sequence
     Item *cuts;     // [entries]: the sequences that are cut: first entry, such segments, slot
@@ -33,11 +34,13 @@ struct ChunkParams {
     float2 *decay;  // [entries][H], each the sum of two floats
 };
 
-// Where the segments are found: in the lists; a single sequence needs none, nor do sequences none of which is long
-// enough to be cut (no entries: 5 of 17 to 200 tokens, 8 heads, take 12.2 us of the device, 15.7 with lists).  A kernel for each: with
+// Where the segments are found: in the lists; a single sequence needs none, nor do sequences that cannot be cut (no
+// entries), if they are of one length or have 640 tokens in all (5 of 17 to 200 tokens, 8 heads, take 12.2 us of the
+// device, 15.7 with lists).  Others are listed for their order though there is nothing to cut: with 77 heads and more (eight of 333 to
+// 4001 tokens, 96 heads: 352 us; 414 in the order given, a rising one).  A kernel for each: with
 // a choice in every warp's loop, 131072 tokens of 8 heads take 335 instead of 316 us.
 enum Source { kListed, kOne, kWhole };
-inline Source source_of(const ChunkParams &p) { return p.entries == 0 ? kWhole : p.a.n_seqs == 1 ? kOne : kListed; }
+inline Source source_of(const ChunkParams &p) { return p.listed ? kListed : p.entries > 0 ? kOne : kWhole; }
 
 // f(segment and head) for each of the `cta`-th of `ctas`, of all segments (OUTPUT) or of those that have a successor:
 // back and forth over the list, so that who had one of the longest gets one of the shortest next.

@@ -138,3 +138,22 @@ def test_first_rows_are_off_by_little_more_than_their_own_rounding(kda, lens, de
                  + 2.0 ** -17 * (x.abs() @ y.abs().transpose(1, 2) * weight @ z.abs()))
         off = (o[a:b].double().transpose(0, 1) - ref).abs()
         assert (off <= bound).all(), float((off / bound).max())
+
+
+def test_ragged_sequences_of_many_heads_are_listed(kda):
+    """More than half as many heads as SMs: nothing is cut, and the sequences' order still comes from a list, which
+    takes a workspace.  Against each sequence alone, bit for bit."""
+    H, lens = 96, [100, 3000, 1, 0, 777, 1500, 128, 640]
+    assert kda.kda_linear_chunk_workspace_bytes(sum(lens), len(lens), H) > 0
+    assert kda.kda_linear_chunk_workspace_bytes(sum(lens), 1, H) == 0
+    data = [(normal((n, 2, 128), 5 * i), normal((n, 2, 128), 5 * i + 1), normal((n, H, 128), 5 * i + 2),
+             -torch.rand((n, H), generator=torch.Generator("cuda").manual_seed(i), device="cuda")) for i, n in enumerate(lens)]
+    together = run(kda, data, list(range(len(lens))), H)
+    for i in range(len(lens)):
+        o, s = run(kda, data, [i], H)[i]
+        assert torch.equal(together[i][0], o) and torch.equal(together[i][1], s), i
+    # of one length: as they come
+    q, k, v, g = (torch.cat([d[j] for d in data])[:6000] for j in range(4))
+    o, s = kda.kda_linear_chunk_fwd(q, k, v, g, n_seqs=4)
+    o2, s2 = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32([0, 1500, 3000, 4500, 6000]))
+    assert torch.equal(o, o2) and torch.equal(s, s2)
