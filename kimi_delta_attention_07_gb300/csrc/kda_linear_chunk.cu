@@ -207,20 +207,24 @@ __global__ void __launch_bounds__(kThreads, 3) linear_chunk_f32_kernel(const Chu
 
 // Tokens of a segment: so many that there are some twelve CTAs a SM, of which three are resident (4096 tokens of 16 heads:
 // 210 us; six 220, sixteen 220), and 64 at least (two sequences of 1001 and 500 tokens: 94 us; 32 100, 96 111).
-inline int64_t segment_of(int64_t total_tokens, int H) {
+inline Cut cut_of(int64_t total_tokens, int n_seqs, int H) {
     constexpr int64_t kLeast = 64, kStep = 2 * kBlock;
     const int64_t each = std::max<int64_t>(1, 12 * sm_count() / (H * (kHeadDim / kRows)));
-    return std::max(kLeast, kStep * ((total_tokens + each * kStep - 1) / (each * kStep)));
+    const int64_t segment = std::max(kLeast, kStep * ((total_tokens + each * kStep - 1) / (each * kStep)));
+    // Three CTAs of an SM share its fma pipe: with nothing but one sequence to fill the SMs, segments and heads go at the rate of
+    // 0.7 an SM (1024 tokens of 64 heads: 196 us cut, 212 uncut), and two more launches count like 64 tokens.
+    if (n_seqs == 1) return {segment, 7 * sm_count() / 10, 64};
+    return {segment, 3 * sm_count() / (kHeadDim / kRows), 24};
 }
 
 }  // namespace
 
 size_t linear_chunk_f32_workspace_bytes(int64_t total_tokens, int n_seqs, int H) {
-    return segments_workspace_bytes(total_tokens, n_seqs, H, segment_of(total_tokens, H));
+    return segments_workspace_bytes(total_tokens, n_seqs, H, cut_of(total_tokens, n_seqs, H));
 }
 
 cudaError_t launch_linear_chunk_f32(const LinearChunkArgs &a, cudaStream_t stream) {
-    const ChunkParams p = plan_segments(a, segment_of(a.total_tokens, a.H), 3 * sm_count() / (kHeadDim / kRows), 24);
+    const ChunkParams p = plan_segments(a, cut_of(a.total_tokens, a.n_seqs, a.H));
     const Source source = source_of(p);
     auto launch = [&](auto kernel, int64_t items) {
         return launch_dependent(kernel, dim3((unsigned)items, kHeadDim / kRows), dim3(kThreads), 0, stream, p);

@@ -736,16 +736,16 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 // Tokens of a segment: so many that the segments of all heads are about as many as SMs.  A cut costs two launches
 // and some 10 us, as much as three chunks: five chunks are left whole, no segment has fewer than two of them, or, where
 // there are several sequences, four.  (5 sequences of 17 to 200 tokens, 8 heads: 22.8 us of the device cut by the chunk, 15.7 whole.)
-inline int64_t segment_of(int64_t total_tokens, int n_seqs, int H) {
+inline Cut cut_of(int64_t total_tokens, int n_seqs, int H) {
     const int64_t chunks = (total_tokens + kTok - 1) / kTok, each = std::max<int64_t>(1, sm_count() / H);
-    if (chunks <= 5) return kTok * std::max<int64_t>(1, chunks);
-    return kTok * std::max<int64_t>(n_seqs == 1 ? 2 : 4, (chunks + each - 1) / each);
+    const int64_t least = n_seqs == 1 ? 2 : 4;
+    return {kTok * (chunks <= 5 ? std::max<int64_t>(1, chunks) : std::max(least, (chunks + each - 1) / each)), sm_count(), 3 * kTok};
 }
 
 }  // namespace
 
 size_t linear_chunk_tc_workspace_bytes(int64_t total_tokens, int n_seqs, int H) {
-    return segments_workspace_bytes(total_tokens, n_seqs, H, segment_of(total_tokens, n_seqs, H));
+    return segments_workspace_bytes(total_tokens, n_seqs, H, cut_of(total_tokens, n_seqs, H));
 }
 
 cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream) {
@@ -760,7 +760,7 @@ cudaError_t launch_linear_chunk_tc(const LinearChunkArgs &a, cudaStream_t stream
         !encode_heads64(&map_v, T ? a.v : none, kHeadDim, a.H, rows, a.v_stride, kTok) ||
         !encode_heads64(&map_o, T ? a.o : none, kHeadDim, a.H, rows, (int64_t)a.H * kHeadDim, kTok))
         return cudaErrorUnknown;
-    const ChunkParams p = plan_segments(a, segment_of(T, a.n_seqs, a.H), sm_count(), 3 * kTok);
+    const ChunkParams p = plan_segments(a, cut_of(T, a.n_seqs, a.H));
     const Source source = source_of(p);
     auto launch = [&](auto kernel, int threads, int64_t items) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);

@@ -46,10 +46,7 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
                 if (n0 + j * threads < a.n_seqs) f(span[j].first, span[j].len, slots[j]);
         }
     };
-    // Cut, or not: by the time of the longest part, or of all (and a quarter of that for the uneven end) where that is
-    // more.  A segment's own state takes half the time of its outputs.  (16 sequences of 4000 tokens, 8 heads: 142 us
-    // uncut, 200 cut, now 125; one of 60000 and 15 of 300: cut, 179.  Longer segments than p.segment never come out
-    // more than a little better than these two.)
+    // Cut, or not.  (16 sequences of 4000 tokens, 8 heads: 142 us uncut, 200 cut, now 125; one of 60000 and 15 of 300: cut, 179.)
     int my_longest = 0, my_followed = 0;
     uint32_t my_sum = 0;
     for_sequences([&](int, int len, int) {
@@ -61,10 +58,7 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
     my_followed = __reduce_add_sync(0xffffffffu, my_followed);
     if (lane == 0) atomicMax(&longest, my_longest), atomicAdd(&sum, my_sum), atomicAdd(&followed, my_followed);
     __syncthreads();
-    const float each = a.H / (float)p.parallel, whole = (float)sum * each;
-    const float uncut = fmaxf(longest, whole + 0.25f * longest);
-    const float cut_up = fmaxf(p.segment, whole + 0.25f * p.segment) + p.fixed + 0.5f * fmaxf(p.segment, (float)followed * p.segment * each);
-    const int segment = followed > 0 && cut_up < uncut ? p.segment : max(longest, 1);
+    const int segment = p.entries > 0 && cut_pays(longest, sum, followed, p.segment, a.H / (float)p.parallel, p.fixed) ? p.segment : max(longest, 1);
     const float scale = (kBuckets - 1) / (float)segment;
     // the segments before a sequence's last one, the tokens of that, and its class
     auto full_of = [&](int len) { return len > 0 ? (int)((uint32_t)(len - 1) / (uint32_t)segment) : 0; };
@@ -164,16 +158,20 @@ __global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkP
 }
 
 // A segment's entry is floor(sequence's first token / segment) and its place in the sequence: distinct for those that have a
-// successor, whatever the lengths.
-inline int64_t entries_of(int64_t total_tokens, int64_t segment) { return total_tokens > 0 ? (total_tokens - 1) / segment : 0; }
+// successor, whatever the lengths.  (A single sequence's cut is decided here, as if it had all tokens: one of H = 64 and 768 tokens
+// 35 us cut, 26 uncut, of 4096 105 and 109; fp32, H = 16, 65 tokens 40 and 16, 256 43 and 55.)
+inline int64_t entries_of(int64_t total_tokens, int n_seqs, int H, const Cut &cut) {
+    const int64_t entries = total_tokens > 0 ? (total_tokens - 1) / cut.segment : 0;
+    return n_seqs > 1 || cut_pays(total_tokens, total_tokens, entries, cut.segment, H / (float)cut.parallel, cut.fixed) ? entries : 0;
+}
 
 struct Layout {
     size_t outputs, inner, cuts, decay, states, total;
 };
 // Lists pay for themselves from this many tokens on, if only by their order.
 constexpr int64_t kListTokens = 640;
-inline Layout layout(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
-    const int64_t entries = entries_of(total_tokens, segment);
+inline Layout layout(int64_t total_tokens, int n_seqs, int H, const Cut &cut) {
+    const int64_t entries = entries_of(total_tokens, n_seqs, H, cut);
     const bool lists = n_seqs > 1 && (entries > 0 || total_tokens > kListTokens);
     Layout l;
     l.outputs = lists ? 256 : 0;
@@ -187,20 +185,20 @@ inline Layout layout(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
 
 }  // namespace
 
-size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int64_t segment) {
-    return layout(total_tokens, n_seqs, H, segment).total;
+size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, const Cut &cut) {
+    return layout(total_tokens, n_seqs, H, cut).total;
 }
 
-ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment, int parallel, int fixed) {
-    const Layout l = layout(a.total_tokens, a.n_seqs, a.H, segment);
+ChunkParams plan_segments(const LinearChunkArgs &a, const Cut &cut) {
+    const Layout l = layout(a.total_tokens, a.n_seqs, a.H, cut);
     uint8_t *ws = (uint8_t *)a.workspace;
     ChunkParams p{a};
-    p.segment = (int)segment;
-    p.entries = (int)entries_of(a.total_tokens, segment);
+    p.segment = (int)cut.segment;
+    p.entries = (int)entries_of(a.total_tokens, a.n_seqs, a.H, cut);
     p.listed = a.n_seqs > 1 && (p.entries > 0 || (a.cu_seqlens && a.total_tokens > kListTokens));
     p.joined = p.entries > 0;
-    p.parallel = parallel;
-    p.fixed = fixed;
+    p.parallel = cut.parallel;
+    p.fixed = cut.fixed;
     p.counts = (int *)ws;
     p.outputs = (Item *)(ws + l.outputs);
     p.inner = (Item *)(ws + l.inner);

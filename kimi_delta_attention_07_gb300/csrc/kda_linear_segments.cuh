@@ -34,6 +34,16 @@ struct ChunkParams {
     float2 *decay;  // [entries][H], each the sum of two floats
 };
 
+// Whether a cut pays, by the time (in tokens of one segment and head) of the longest part, or of all (and a quarter of the longest for
+// the uneven end) where that is more.  A segment's own state takes half the time of its outputs.  each: H / parallel; followed:
+// segments with a successor.
+__host__ __device__ inline bool cut_pays(int64_t longest, int64_t sum, int64_t followed, int64_t segment, float each, int fixed) {
+    const float most = (float)longest, whole = (float)sum * each, part = (float)segment;
+    const float uncut = fmaxf(most, whole + 0.25f * most);
+    const float cut = fmaxf(part, whole + 0.25f * part) + fixed + 0.5f * fmaxf(part, (float)followed * part * each);
+    return followed > 0 && cut < uncut;
+}
+
 // Where the segments are found: in the lists; a single sequence needs none, nor do sequences that cannot be cut (no
 // entries), if they are of one length or have 640 tokens in all (5 of 17 to 200 tokens, 8 heads, take 12.2 us of the
 // device, 15.7 with lists).  Others are listed for their order though there is nothing to cut: with 77 heads and more (eight of 333 to
@@ -89,8 +99,13 @@ __device__ __forceinline__ float *state_after(const ChunkParams &p, const Item &
     return (s.w & kEnds) && a.final_state ? a.final_state + ((int64_t)s.z * a.H + head_of(s)) * kState : nullptr;
 }
 
-size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, int64_t segment);
-ChunkParams plan_segments(const LinearChunkArgs &a, int64_t segment, int parallel, int fixed);
+// How a call's sequences are cut: tokens of a segment, and the terms of what a cut costs (ChunkParams).
+struct Cut {
+    int64_t segment;
+    int parallel, fixed;
+};
+size_t segments_workspace_bytes(int64_t total_tokens, int n_seqs, int H, const Cut &cut);
+ChunkParams plan_segments(const LinearChunkArgs &a, const Cut &cut);
 cudaError_t launch_segment_lists(const ChunkParams &p, cudaStream_t stream);
 cudaError_t launch_segment_join(const ChunkParams &p, cudaStream_t stream);
 

@@ -157,3 +157,21 @@ def test_ragged_sequences_of_many_heads_are_listed(kda):
     o, s = kda.kda_linear_chunk_fwd(q, k, v, g, n_seqs=4)
     o2, s2 = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32([0, 1500, 3000, 4500, 6000]))
     assert torch.equal(o, o2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("dtype,T,H,cut", [
+    (torch.float32, 65, 16, False), (torch.float32, 128, 1, False), (torch.float32, 256, 64, False), (torch.float32, 512, 16, True),
+    (torch.float32, 1024, 4, True), (torch.bfloat16, 641, 64, False), (torch.bfloat16, 1024, 64, False),
+    (torch.bfloat16, 1024, 4, True), (torch.bfloat16, 4096, 32, True), (torch.bfloat16, 2500, 100, False)])
+def test_one_sequence_is_cut_where_it_pays(kda, dtype, T, H, cut):
+    """By the rule that several sequences are cut by; what is cut takes a workspace.  State and last outputs against 64 bits."""
+    code = kda.KDA_BF16 if dtype is torch.bfloat16 else kda.KDA_F32
+    assert (kda.kda_linear_chunk_workspace_bytes(T, 1, H, code) > 0) == cut
+    q, k, v = (normal((T, H, 128), i, dtype) for i in range(3))
+    g = -torch.rand((T, H), generator=torch.Generator("cuda").manual_seed(5), device="cuda") / 64
+    o, s = kda.kda_linear_chunk_fwd(q, k, v, g)
+    ref = final_state(k, v, g)
+    assert rel(s[0], ref) < 2.0 ** -20
+    # (bf16: o's rounding, and those of P and of the state in front of the chunk, 2^-8 / sqrt 3 at most each)
+    last = torch.einsum("hed,hd->he", ref, q[-1].double()) * 128 ** -0.5
+    assert rel(o[-1], last) < (2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -20)
