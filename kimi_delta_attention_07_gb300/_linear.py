@@ -29,10 +29,19 @@ def _stream_of(stream, dev):
 
 
 def _decay(g, tokens, H, dev):
-    """The address of g and its elements between tokens: [H] (0), or tokens' shape with H behind it."""
+    """The address of g and its elements between tokens: [H] (0), or tokens' shape with H behind it, whose
+    tokens are all at one stride (a slice of a projection, or one row expanded)."""
     if g.dim() == 1:
         return _need(g, "g", _f32, (H,), dev), 0
-    return _need(g, "g", _f32, (*tokens, H), dev), H
+    if g.is_contiguous():
+        return _need(g, "g", _f32, (*tokens, H), dev), H
+    if g.dtype is not _f32 or g.shape != (*tokens, H) or g.get_device() != dev:
+        _need(g.contiguous(), "g", _f32, (*tokens, H), dev)  # names what is wrong
+    steps = [s for s, n in zip(g.stride(), tokens) if n > 1]
+    stride = steps[-1] if steps else H
+    if (H > 1 and g.stride(-1) != 1) or (0 < stride < H) or (len(steps) == 2 and steps[0] != tokens[1] * stride):
+        raise ValueError(f"g: its heads must be next to each other and all tokens at one stride of at least {H} (or 0)")
+    return g.data_ptr(), stride
 
 
 def _states(t, name, H, dev):
@@ -113,9 +122,8 @@ def kda_linear_chunk_fwd(q, k, v, g, *, cu_seqlens=None, n_seqs=None, initial_st
     S <- exp(g) S + k v^T, o = scale S^T q (kda_linear_chunk_fwd in kda_linear.h).
 
     q, k [T, Hk, 128], v [T, H, 128] (Hk divides H; head h reads q and k of head
-    h // (H // Hk)), bf16 or fp32, token strides free; g fp32 [T, H], or [H] for
-    fixed decays.  cu_seqlens int32 [N+1] or None (n_seqs equal lengths,
-    default 1).  States are [N, H, 128, 128] ([V, K]) fp32, or with state_indices (int32
+    h // (H // Hk)), bf16 or fp32; g fp32 [T, H], or [H] for fixed decays; token
+    strides free.  cu_seqlens int32 [N+1] or None (n_seqs equal lengths, default 1).  States are [N, H, 128, 128] ([V, K]) fp32, or with state_indices (int32
     [N]) pools of them; final_state may be initial_state.  scale defaults to 128 ** -0.5.
     workspace is allocated where one is needed, unless given
     (kda_linear_chunk_workspace_bytes).  Returns (o, final_state).
@@ -224,7 +232,7 @@ def _step(name, q, k, v, g, state_pool, state_indices, num_accepted, scale, o, s
 def kda_linear_step(q, k, v, g, state_pool, *, state_indices=None, scale=None, o=None, stream=None):
     """One decode token per sequence, updating ``state_pool`` [slots, H, 128, 128] in place.
 
-    q, k [N, Hk, 128]; v [N, H, 128] (token strides free); g fp32 [N, H] or [H];
+    q, k [N, Hk, 128]; v [N, H, 128]; g fp32 [N, H] (token strides free) or [H];
     state_indices int32 [N] or None (slot n).  Returns o [N, H, 128].
     """
     return _step("kda_linear_step", q, k, v, g, state_pool, state_indices, None, scale, o, stream, (q.shape[0],))
