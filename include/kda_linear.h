@@ -48,7 +48,7 @@ extern "C" {
  *   pairs (a, b) of the rot_dim channels from rot_offset on:
  *     (a cos t - b sin t, b cos t + a sin t),   t = positions[axis(i)][token] * inv_freq[i]
  *   q       [T, Hq, D] dtype, q_stride elements between tokens; k [T, Hk, D] likewise
- *   q_weight, k_weight  fp32 [D], or NULL: ones
+ *   q_weight, k_weight  fp32 [D], 16-byte aligned, or NULL: ones; not looked at without the norm
  *   positions  int32 [n_axes, T]; a token whose position on axis 0 is negative is
  *           padding: its rows of q_out and k_out are left as they were.  NULL
  *           with rot_dim = 0: every token is real

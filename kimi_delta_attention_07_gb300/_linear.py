@@ -85,6 +85,8 @@ def kda_head_norm_rope(q, k=None, *, positions=None, inv_freq=None, sections=Non
         if k_out is None:
             k_out = _empty((T, Hk, D), dtype, q.device, stream)
         pok, sok = _rows(k_out, "k_out", dtype, (T, Hk, D), dev)
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights without the norm: they would not be applied")
     pwq = None if q_weight is None else _need(q_weight, "q_weight", _f32, (D,), dev)
     pwk = None if k_weight is None else _need(k_weight, "k_weight", _f32, (D,), dev)
     axes = 1

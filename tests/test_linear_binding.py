@@ -69,3 +69,13 @@ def test_decays_that_are_refused(kda):
     for bad in (normal((4, 5, 4), 1, torch.float32)[:, :3], normal((4, 1, 4), 1, torch.float32).expand(4, 3, 4)):
         with pytest.raises(ValueError, match="one stride"):
             kda.kda_linear_multi_step(q, k, v, bad, pool, index)
+
+
+def test_weights_without_the_norm_are_refused(kda):
+    q, k, w = normal((5, 2, 128), 0), normal((5, 1, 128), 1), torch.ones(128, device="cuda")
+    for weights in (dict(q_weight=w), dict(k_weight=w), dict(q_weight=w, k_weight=w)):
+        with pytest.raises(ValueError, match="without the norm"):
+            kda.kda_head_norm_rope(q, k, norm=False, **weights)
+        kda.kda_head_norm_rope(q, k, **weights)
+    a, b = kda.kda_head_norm_rope(q, k, norm=False)
+    assert torch.equal(a, q) and torch.equal(b, k)
