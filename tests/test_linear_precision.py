@@ -175,3 +175,109 @@ def test_one_sequence_is_cut_where_it_pays(kda, dtype, T, H, cut):
     # (bf16: o's rounding, and those of P and of the state in front of the chunk, 2^-8 / sqrt 3 at most each)
     last = torch.einsum("hed,hd->he", ref, q[-1].double()) * 128 ** -0.5
     assert rel(o[-1], last) < (2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -20)
+
+
+# ---- states behind every way of finding the segments ------------------------------------
+
+
+@pytest.mark.parametrize("lens,H", [([100], 4), ([200, 154, 108, 62, 17], 4), ([700] * 14, 8), ([3000], 4), ([1900, 40, 1500], 2)])
+@pytest.mark.parametrize("rate", [2.0 ** -3, 2.0 ** -5, 2.0 ** -8])
+def test_states_of_bf16_prompts_are_as_exact_as_fp32_sums(kda, lens, H, rate):
+    """A token's weight carries two exponentials (2^-22), three products and some roundings of its exponent (2^-24 each), the sums
+    a few more: 2^-20 of the norm.  Decayed keys as two bf16 terms instead of three would be off by 2.1e-6 to 2.5e-6,
+    more than twice as much, as one term by 1.6e-3."""
+    T = sum(lens)
+    q, k, v = (normal((T, H, 128), i) for i in range(3))
+    g = torch.full((H,), -rate, device="cuda")
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    _, s = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu))
+    for n, (a, b) in enumerate(zip(cu, cu[1:])):
+        assert rel(s[n], final_state(k[a:b], v[a:b], g.expand(T, H)[a:b])) < 2.0 ** -20, n
+
+
+# ---- sequences that are cut: values that are not finite, slots that are refused ----------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("which", ["k", "v", "g"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens,at", [([3000], 300), ([3000], 2999), ([40, 2900, 60], 1500)])
+def test_not_finite_in_a_sequence_that_is_cut(kda, dtype, which, value, lens, at):
+    H, T = 2, sum(lens)
+    q, k, v = (normal((T, H, 128), i, dtype) for i in range(3))
+    g = -torch.rand((T, H), generator=torch.Generator("cuda").manual_seed(5), device="cuda") / 16
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    n = next(i for i in range(len(lens)) if cu[i] <= at < cu[i + 1])
+    end = cu[n + 1]
+    clean, sc = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu))
+    x = dict(k=k, v=v, g=g)[which]
+    x[(at, 1) if which == "g" else (at, 1, 77)] = value
+    o, s = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu))
+    # (fp32: eight tokens of which one has no finite decay go token by token instead of by their common reference, and round
+    # otherwise: some products more or fewer, 2^-24 each, of |q| |k| |v|, which is ten times o)
+    same = at - (at - cu[n]) % 8 if which == "g" and dtype is torch.float32 else at
+    assert same == at or rel(o[same:at], clean[same:at].double()) < 2.0 ** -18
+    assert torch.equal(o[:same], clean[:same]) and torch.equal(o[end:], clean[end:]) and torch.equal(o[:, 0], clean[:, 0])
+    assert torch.equal(s[:, 0], sc[:, 0])
+    for i in range(len(lens)):
+        assert i == n or torch.equal(s[i], sc[i])
+    if which == "v":
+        other = torch.arange(128, device="cuda") != 77
+        assert not o[at:end, 1, 77].isfinite().any() and not s[n, 1, 77].isfinite().any()
+        assert torch.equal(o[:, 1, other], clean[:, 1, other]) and torch.equal(s[n, 1, other], sc[n, 1, other])
+    else:
+        assert not o[at:end, 1].isfinite().any()
+        assert not (s[n, 1, :, 77] if which == "k" else s[n, 1]).isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_long_sequence_without_a_slot(kda, dtype):
+    """Long enough to be cut, refused, beside one that is cut and one that is not: alone they come to the same within the
+    rounding of another cut (2^-18 of the state's norm, a rounding of bf16 of o's)."""
+    H, lens = 1, [2100, 1700, 50]
+    T, cu = sum(lens), [0, 2100, 3800, 3850]
+    q, k, v = (normal((T, H, 128), i, dtype) for i in range(3))
+    g = -torch.rand((T, H), generator=torch.Generator("cuda").manual_seed(5), device="cuda") / 16
+    pool = normal((5, H, 128, 128), 9, torch.float32)
+    start = pool.clone()
+    for slot in (-1, 5):
+        pool.copy_(start)
+        o, _ = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu), initial_state=pool, final_state=pool, state_indices=i32([slot, 3, 1]))
+        assert o[:2100].isnan().all()
+        for unused in (0, 2, 4):
+            assert torch.equal(pool[unused], start[unused])
+        for n, at in ((1, 3), (2, 1)):
+            rows = slice(cu[n], cu[n + 1])
+            one, s = kda.kda_linear_chunk_fwd(q[rows], k[rows], v[rows], g[rows], initial_state=start[at:at + 1])
+            assert rel(pool[at], s[0].double()) < 2.0 ** -18
+            assert rel(o[rows], one.double()) < (2.0 ** -7 if dtype is torch.bfloat16 else 2.0 ** -18)
+
+
+def test_one_sequence_without_a_slot(kda):
+    for dtype, T in ((torch.bfloat16, 3000), (torch.float32, 900), (torch.bfloat16, 30)):
+        q, k, v = (normal((T, 2, 128), i, dtype) for i in range(3))
+        pool = normal((3, 2, 128, 128), 9, torch.float32)
+        start = pool.clone()
+        o, _ = kda.kda_linear_chunk_fwd(q, k, v, torch.zeros(2, device="cuda"), initial_state=pool, final_state=pool, state_indices=i32([3]))
+        assert o.isnan().all() and torch.equal(pool, start)
+
+
+def test_one_sequence_that_ends_before_the_last_token(kda):
+    """A padded batch of one sequence: cut or not by all tokens, computed as far as it goes, the rows behind it left."""
+    for dtype, T, H in ((torch.bfloat16, 3000, 2), (torch.float32, 900, 2), (torch.float32, 200, 4)):
+        q, k, v = (normal((T, H, 128), i, dtype) for i in range(3))
+        g = torch.full((H,), -2.0 ** -6, device="cuda")
+        for n in (0, 1, 64, 65, 130, T // 2, T - 1):
+            o = torch.full((T, H, 128), 7.0, dtype=dtype, device="cuda")
+            _, s = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32([0, n]), o=o)
+            assert (o[n:] == 7.0).all()
+            if n == 0:
+                assert (s == 0).all()
+                continue
+            ref = final_state(k[:n], v[:n], g.expand(T, H)[:n])
+            last = torch.einsum("hed,hd->he", ref, q[n - 1].double()) * 128 ** -0.5
+            assert rel(s[0], ref) < 2.0 ** -20 and rel(o[n - 1], last) < (2.0 ** -7 if dtype is torch.bfloat16 else 2.0 ** -20)
