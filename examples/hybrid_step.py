@@ -6,11 +6,13 @@ The operators are the package's own; the projections between them are plain
 matrix products on random weights.  One page table serves the latent cache,
 one slot per request the KDA state pool:
 
-  kda_page_tables          lengths -> new table rows, slots, offsets
+  kda_page_tables          lengths -> new table rows, slots, positions, offsets
   kda_rms_norm             residual + norm in front of each layer
   kda_chunk_fwd_gated      KDA layer, prompts (final states into the pool)
   kda_recurrent_step_gated KDA layer, one token, in place on the pool
-  kda_latent_cache_write   latent layer: normed latent and key into the pages
+  kda_head_norm_rope       latent layer: queries' and key's positional channels
+                           turn by the token's position
+  kda_latent_cache_write   normed latent and key into the pages
   kda_latent_prefill       prompts, expanded keys and values
   kda_latent_decode        one token, on the cached vectors themselves
 
@@ -47,6 +49,7 @@ class HybridDecoder:
         # latent layer: queries, latent and positional key in one projection; up-projection; output
         self.q_width = heads * (HEAD + ROPE)
         self.latent_in = weight(hidden, self.q_width + LATENT + ROPE)
+        self.inv_freq = 10000.0 ** (-torch.arange(ROPE // 2, device="cuda") / (ROPE // 2))
         self.latent_norm = torch.ones(LATENT, device="cuda")
         self.up = weight(heads, LATENT, 2 * HEAD)     # a head's key part and value
         self.latent_out = weight(heads * HEAD, hidden)
@@ -72,7 +75,7 @@ class HybridDecoder:
             raise ValueError("a prompt needs requests without cached tokens")
         if not prompts and T != self.lens.numel():
             raise ValueError("a decode step takes one token a request")
-        cu, lens, slots, _, status = kda.kda_page_tables(
+        cu, lens, slots, positions, status = kda.kda_page_tables(
             self.lens, new_lens, self.free_pages, self.table, page_size=self.page_size, n_pages=self.n_pages,
             max_tokens=T, free_start=self.free_start)
         # A refused request's tokens have slot -1 and its length stays.  (A server that counts its pages on the host
@@ -95,6 +98,10 @@ class HybridDecoder:
         y, x, _ = kda.kda_rms_norm(o.view(T, -1) @ self.kda_out, self.norms[1], residual=x)
         fused = y @ self.latent_in
         q = fused[:, :self.q_width].unflatten(1, (H, HEAD + ROPE))
+        k_rope = fused[:, self.q_width + LATENT:].unflatten(1, (1, ROPE))
+        for t, offset in ((q, HEAD), (k_rope, 0)):  # in place, in the projection
+            kda.kda_head_norm_rope(t, positions=positions, inv_freq=self.inv_freq, rot_offset=offset, interleaved=True,
+                                   norm=False, q_out=t)
         kda.kda_latent_cache_write(fused[:, self.q_width:], self.latent_norm, self.cache, slots)
         if prompts:
             rows = self.cache.view(-1, LATENT + ROPE)[slots.long()]
