@@ -11,8 +11,6 @@ inline bool valid_dtype(int dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 
 inline size_t elem_bytes(int dt) { return dt == KDA_BF16 ? 2 : 4; }
 
-inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 // The chunk path a call takes: the tensor-core path for bf16 inputs unless
 // the precise path is requested.
 inline bool use_tensor_cores(int dtype, int flags) {

@@ -5,8 +5,6 @@ using namespace kda;
 
 namespace {
 
-inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 // log2 of a page size, -1 if it is not a power of two from 16 to 256
 inline int page_shift(int page_size) {
     for (int s = 4; s <= 8; ++s)
@@ -16,16 +14,6 @@ inline int page_shift(int page_size) {
 
 inline bool pool_ok(int64_t n_pages, int shift) {
     return shift >= 0 && n_pages > 0 && n_pages < ((int64_t)1 << (31 - shift));
-}
-
-template <typename F>
-int launched(F launch) {
-    cudaGetLastError();  // an earlier error is not this launch's
-    if (launch() != cudaSuccess) {
-        cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
-    return KDA_OK;
 }
 
 }  // namespace

@@ -72,6 +72,18 @@ enum StatusBits : int {
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Of the C entry points: a pointer's alignment, and a launcher's outcome as a status.
+inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+template <typename F>
+int launched(F launch) {
+    cudaGetLastError();  // an earlier error is not this launch's
+    if (launch() != cudaSuccess) {
+        cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    return KDA_OK;
+}
+
 __host__ __device__ inline int64_t max_chunks(int64_t total_tokens, int n_seqs) {
     // Sum over sequences of ceil(len / 64) <= floor(T / 64) + N.
     return total_tokens / kChunk + n_seqs;

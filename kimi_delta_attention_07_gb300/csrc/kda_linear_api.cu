@@ -5,23 +5,11 @@ using namespace kda;
 
 namespace {
 
-inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 inline bool dtype_ok(int dtype) { return dtype == KDA_F32 || dtype == KDA_BF16; }
 
 // A token stride for `heads` heads of `width`: a slice of a wider row, 16-byte aligned.
 inline bool stride_ok(int64_t stride, int64_t heads, int width) {
     return stride >= heads * width && stride % 8 == 0 && stride < ((int64_t)1 << 31);
-}
-
-template <typename F>
-int launched(F launch) {
-    cudaGetLastError();  // an earlier error is not this launch's
-    if (launch() != cudaSuccess) {
-        cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
-    return KDA_OK;
 }
 
 // What the chunked form and the steps have in common, but for the pointers.
