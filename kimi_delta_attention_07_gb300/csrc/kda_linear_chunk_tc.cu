@@ -734,12 +734,11 @@ __global__ void __launch_bounds__(OUTPUT ? 896 : 640, 1)
 }
 
 // Tokens of a segment: so many that the segments of all heads are about as many as SMs.  A cut costs two launches
-// and some 10 us, as much as three chunks: five chunks are left whole, no segment has fewer than two of them, or, where
+// and some 10 us, as much as three chunks: no segment has fewer than two of them, or, where
 // there are several sequences, four.  (5 sequences of 17 to 200 tokens, 8 heads: 22.8 us of the device cut by the chunk, 15.7 whole.)
 inline Cut cut_of(int64_t total_tokens, int n_seqs, int H) {
     const int64_t chunks = (total_tokens + kTok - 1) / kTok, each = std::max<int64_t>(1, sm_count() / H);
-    const int64_t least = n_seqs == 1 ? 2 : 4;
-    return {kTok * (chunks <= 5 ? std::max<int64_t>(1, chunks) : std::max(least, (chunks + each - 1) / each)), sm_count(), 3 * kTok};
+    return {kTok * std::max<int64_t>(n_seqs == 1 ? 2 : 4, (chunks + each - 1) / each), sm_count(), 3 * kTok};
 }
 
 }  // namespace

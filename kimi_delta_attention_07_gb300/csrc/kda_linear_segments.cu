@@ -158,21 +158,25 @@ __global__ void __launch_bounds__(kJoinThreads) segment_join_kernel(const ChunkP
 }
 
 // A segment's entry is floor(sequence's first token / segment) and its place in the sequence: distinct for those that have a
-// successor, whatever the lengths.  (A single sequence's cut is decided here, as if it had all tokens: one of H = 64 and 768 tokens
-// 35 us cut, 26 uncut, of 4096 105 and 109; fp32, H = 16, 65 tokens 40 and 16, 256 43 and 55.)
+// successor, whatever the lengths.  None where no cut can pay: a single sequence is taken to have all tokens (one of H = 64 and
+// 768 tokens 35 us cut, 26 uncut, of 4096 105 and 109; fp32, H = 16, 65 tokens 40 and 16, 256 43 and 55), several to be, at best,
+// nearly one, with one segment to add up (7 of 17 to 200 tokens, 8 heads: 12 us, 18 with launches that find nothing to cut).
 inline int64_t entries_of(int64_t total_tokens, int n_seqs, int H, const Cut &cut) {
-    const int64_t entries = total_tokens > 0 ? (total_tokens - 1) / cut.segment : 0;
-    return n_seqs > 1 || cut_pays(total_tokens, total_tokens, entries, cut.segment, H / (float)cut.parallel, cut.fixed) ? entries : 0;
+    const int64_t entries = total_tokens > 0 ? (total_tokens - 1) / cut.segment : 0, followed = n_seqs == 1 ? entries : std::min<int64_t>(entries, 1);
+    return cut_pays(total_tokens, total_tokens, followed, cut.segment, H / (float)cut.parallel, cut.fixed) ? entries : 0;
+}
+// Whether sequences that are not cut are listed for their order: more of them and heads than are worked on at the same time,
+// and more tokens than a list's launch counts for.
+inline bool order_pays(int64_t total_tokens, int n_seqs, int H, const Cut &cut) {
+    return total_tokens > 640 && (int64_t)n_seqs * H > cut.parallel;
 }
 
 struct Layout {
     size_t outputs, inner, cuts, decay, states, total;
 };
-// Lists pay for themselves from this many tokens on, if only by their order.
-constexpr int64_t kListTokens = 640;
 inline Layout layout(int64_t total_tokens, int n_seqs, int H, const Cut &cut) {
     const int64_t entries = entries_of(total_tokens, n_seqs, H, cut);
-    const bool lists = n_seqs > 1 && (entries > 0 || total_tokens > kListTokens);
+    const bool lists = n_seqs > 1 && (entries > 0 || order_pays(total_tokens, n_seqs, H, cut));
     Layout l;
     l.outputs = lists ? 256 : 0;
     l.inner = l.outputs + (lists ? align_up((size_t)(entries + n_seqs) * sizeof(Item), 256) : 0);
@@ -195,7 +199,7 @@ ChunkParams plan_segments(const LinearChunkArgs &a, const Cut &cut) {
     ChunkParams p{a};
     p.segment = (int)cut.segment;
     p.entries = (int)entries_of(a.total_tokens, a.n_seqs, a.H, cut);
-    p.listed = a.n_seqs > 1 && (p.entries > 0 || (a.cu_seqlens && a.total_tokens > kListTokens));
+    p.listed = a.n_seqs > 1 && (p.entries > 0 || (a.cu_seqlens && order_pays(a.total_tokens, a.n_seqs, a.H, cut)));
     p.joined = p.entries > 0;
     p.parallel = cut.parallel;
     p.fixed = cut.fixed;

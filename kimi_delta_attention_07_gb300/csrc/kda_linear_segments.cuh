@@ -45,9 +45,9 @@ __host__ __device__ inline bool cut_pays(int64_t longest, int64_t sum, int64_t f
 }
 
 // Where the segments are found: in the lists; a single sequence needs none, nor do sequences that cannot be cut (no
-// entries), if they are of one length or have 640 tokens in all (5 of 17 to 200 tokens, 8 heads, take 12.2 us of the
-// device, 15.7 with lists).  Others are listed for their order though there is nothing to cut: with 77 heads and more (eight of 333 to
-// 4001 tokens, 96 heads: 352 us; 414 in the order given, a rising one).  A kernel for each: with
+// entries), if they are few or short or of one length (5 of 17 to 200 tokens, 8 heads, take 12.2 us of the
+// device, 15.7 with lists).  Others are listed for their order though there is nothing to cut: eight of 333 to
+// 4001 tokens, 96 heads: 352 us; 414 in the order given, a rising one.  A kernel for each: with
 // a choice in every warp's loop, 131072 tokens of 8 heads take 335 instead of 316 us.
 enum Source { kListed, kOne, kWhole };
 inline Source source_of(const ChunkParams &p) { return p.listed ? kListed : p.entries > 0 ? kOne : kWhole; }

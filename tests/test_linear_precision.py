@@ -177,6 +177,21 @@ def test_one_sequence_is_cut_where_it_pays(kda, dtype, T, H, cut):
     assert rel(o[-1], last) < (2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -20)
 
 
+@pytest.mark.parametrize("lens,H,workspace", [([200, 154, 108, 62, 17, 90, 120], 8, False), ([500, 600], 8, False), ([4, 1100], 2, False),
+                                              ([200] * 12, 8, True), ([3000, 20], 8, True), ([40] * 20, 16, True), ([300, 500], 40, False)])
+def test_nothing_is_launched_for_a_cut_that_cannot_pay(kda, lens, H, workspace):
+    """By their tokens and heads alone; what may be cut, or is listed for its order, takes a workspace."""
+    assert (kda.kda_linear_chunk_workspace_bytes(sum(lens), len(lens), H) > 0) == workspace
+    data = [(normal((n, 2, 128), 5 * i), normal((n, 2, 128), 5 * i + 1), normal((n, H, 128), 5 * i + 2),
+             -torch.rand((n, H), generator=torch.Generator("cuda").manual_seed(i), device="cuda")) for i, n in enumerate(lens)]
+    together = run(kda, data, list(range(len(lens))), H)
+    for i, n in enumerate(lens):
+        if n <= 512 or not workspace:
+            o, s = run(kda, data, [i], H)[i]
+            assert torch.equal(together[i][0], o) or n > 512
+            assert rel(together[i][0], o.double()) < 2.0 ** -7 and rel(together[i][1], s.double()) < 2.0 ** -19
+
+
 # ---- states behind every way of finding the segments ------------------------------------
 
 
