@@ -13,7 +13,7 @@
 // Two sequences of 1001 and 500 tokens, 16 heads: 91 us; 135 with two rows a thread, 196 with
 // a product for each decay and one row a thread, 252 uncut and with an exchange a token.  What bounds it: 12 warps
 // a SM (their registers hold the state), whose fma and shared-memory pipes are each half busy (4096 tokens of
-// 32 heads: 375 us, of which 174 are its fmas at the pipe's rate).
+// 32 heads: 369 us, of which 174 are its fmas at the pipe's rate).
 //
 // A decay near one is the sum of two floats (decay_of).
 #include <algorithm>

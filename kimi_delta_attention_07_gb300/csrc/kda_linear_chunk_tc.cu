@@ -49,8 +49,9 @@
 // while Q . S is computed (in front of P 313 us for 131072 tokens, behind the scaling of O 327, here 300), the copy of S
 // while P . V is.
 //
-// 131072 tokens of 8 heads: 294 us, of which the segments' states take 104 (4.9 TB/s), the join 6 and the
-// outputs 189 (5.6 TB/s); 4096 tokens of 32 heads: 63 us; 8 sequences of 333 to 4001 tokens, 32 heads, uncut: 128 us.
+// 131072 tokens of 8 heads: 302 to 314 us, of which the segments' states take 105 (4.9 TB/s), the join 6 and the
+// outputs 193 (5.5 TB/s); 4096 tokens of 32 heads: 64 us; 8 sequences of 333 to 4001 tokens, 32 heads, uncut: 133 us.
+// (Decays as sums of two floats and the second terms of P are 3 to 4 % of that.)
 //
 // Warps: 0 TMA, 1 MMA of X and O, 2 MMA of D, 3 decays, 4..11 check of V and Kt, 12..27 P, the state
 // and the outputs; without outputs 4..19 all of it.

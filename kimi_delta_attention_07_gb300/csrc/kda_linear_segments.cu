@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kIndexThreads) segment_lists_kernel(const Chun
                 if (n0 + j * threads < a.n_seqs) f(span[j].first, span[j].len, slots[j]);
         }
     };
-    // Cut, or not.  (16 sequences of 4000 tokens, 8 heads: 142 us uncut, 200 cut, now 125; one of 60000 and 15 of 300: cut, 179.)
+    // Cut, or not.  (16 sequences of 4000 tokens, 8 heads: 142 us uncut, 200 cut at the time, now 129; one of 60000 and 15 of 300: cut, 185.)
     int my_longest = 0, my_followed = 0;
     uint32_t my_sum = 0;
     for_sequences([&](int, int len, int) {
