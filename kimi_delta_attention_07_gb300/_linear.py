@@ -58,7 +58,7 @@ def kda_head_norm_rope(q, k=None, *, positions=None, inv_freq=None, sections=Non
 
     q [T, Hq, D], k [T, Hk, D] or None, bf16 or fp32; their token strides are free
     (slices of a fused projection).  norm: x / sqrt(mean(x^2) + eps) * weight over the
-    D channels of a head (weights fp32 [D], None: ones).  inv_freq fp32
+    D channels of a head (weights fp32 [D], None: ones; refused without the norm).  inv_freq fp32
     [rot_dim / 2] (None: no rotation) turns the rot_dim channels from rot_offset
     on, in pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved; positions int32
     [T], or [A, T] with `sections`, the pairs of each axis.  A token whose first

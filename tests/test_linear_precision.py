@@ -296,3 +296,49 @@ def test_one_sequence_that_ends_before_the_last_token(kda):
             ref = final_state(k[:n], v[:n], g.expand(T, H)[:n])
             last = torch.einsum("hed,hd->he", ref, q[n - 1].double()) * 128 ** -0.5
             assert rel(s[0], ref) < 2.0 ** -20 and rel(o[n - 1], last) < (2.0 ** -7 if dtype is torch.bfloat16 else 2.0 ** -20)
+
+
+# ---- a captured call whose offsets change, offsets that are out of order ----------------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,H", [(2000, 8), (2000, 90), (1100, 8), (600, 2)])
+def test_a_captured_call_follows_its_offsets(kda, dtype, T, H):
+    """What is launched follows from the tokens and heads; which sequences there are, from the offsets at replay."""
+    q, k, v = (normal((T, n, 128), i, dtype) for i, n in enumerate((2, 2, H)))
+    g = -torch.rand((T, H), generator=torch.Generator("cuda").manual_seed(5), device="cuda") / 8
+    code = kda.KDA_BF16 if dtype is torch.bfloat16 else kda.KDA_F32
+    offsets = [[0, 40, 300, 310, T], [0, 0, 0, T, T], [0, T - 1, T - 1, T, T], [0, 1, 2, 3, 4], [0, T // 4, T // 2, T - T // 4, T]]
+    cu, o, s = i32(offsets[0]), torch.empty((T, H, 128), dtype=dtype, device="cuda"), torch.empty((4, H, 128, 128), device="cuda")
+    ws = torch.empty(max(256, kda.kda_linear_chunk_workspace_bytes(T, 4, H, code)), dtype=torch.uint8, device="cuda")
+    kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=cu, o=o, final_state=s, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=cu, o=o, final_state=s, workspace=ws)
+    for new in offsets:
+        cu.copy_(i32(new))
+        o.fill_(7.0), s.fill_(7.0), ws.fill_(255)
+        graph.replay()
+        want, end = kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(new))
+        assert torch.equal(o[:new[-1]], want[:new[-1]]) and torch.equal(s, end) and (o[new[-1]:] == 7.0).all()
+        for n, (a, b) in enumerate(zip(new, new[1:])):
+            assert (s[n] == 0).all() if a == b else rel(s[n], final_state(k[a:b].repeat_interleave(H // 2, 1), v[a:b], g[a:b])) < 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_refused_sequences_of_many_heads(kda, dtype):
+    """Listed though nothing is cut: a sequence without a slot, one that ends behind the last token, one that runs backwards."""
+    H, T = 80, 1000
+    q, k, v = (normal((T, n, 128), i, dtype) for i, n in enumerate((1, 1, H)))
+    g = torch.full((H,), -2.0 ** -5, device="cuda")
+    pool = normal((9, H, 128, 128), 3, torch.float32)
+    start, cu, slots = pool.clone(), [0, 400, 530, 900, T + 5, T], [6, 9, 0, 2, 4]
+    o = torch.full((T, H, 128), 7.0, dtype=dtype, device="cuda")
+    kda.kda_linear_chunk_fwd(q, k, v, g, cu_seqlens=i32(cu), final_state=pool, state_indices=i32(slots), o=o)
+    for n in (0, 2):
+        a, b = cu[n], cu[n + 1]
+        assert rel(pool[slots[n]], final_state(k[a:b].expand(-1, H, -1), v[a:b], g.expand(b - a, H))) < 2.0 ** -20
+        assert o[a:b].isfinite().all() and not (o[a:b] == 7.0).all(-1).any()
+    assert o[400:530].isnan().all() and (o[900:] == 7.0).all()
+    for slot in (1, 2, 3, 4, 5, 7, 8):
+        assert torch.equal(pool[slot], start[slot])
